@@ -65,7 +65,8 @@ def listed():
 
 
 def _logu(rng, lo, hi):
-    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    v = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    return v + (v % 1024 == 0)  # powers of two and their like stay with the listed cases
 
 
 def draw(rng):
@@ -83,7 +84,7 @@ def draw(rng):
         if op == "embed_grad":
             c["accumulate"] = rng.random() < 0.5
         return c
-    c["n"] = max(1, min(_logu(rng, 1, 16384), 8192 * 50257 * 2 // (BYTES[dtype] * vocab)))
+    c["n"] = max(1, min(_logu(rng, 1, 16384), 8000 * 50257 * 2 // (BYTES[dtype] * vocab)))
     if op == "logprobs":
         c["k"] = rng.choice([0, 0, 1, 5, 20, 64])
         c["entropy"] = rng.random() < 0.6
