@@ -10,7 +10,8 @@
  *  - Every call returns a zero3_status; nothing aborts, throws or exits.
  *  - Device buffers are owned by the caller (allocated with any CUDA
  *    allocator) and passed as raw pointers; every device pointer must be
- *    16-byte aligned (ZERO3_EINVAL otherwise).  Element offsets inside
+ *    16-byte aligned (ZERO3_EINVAL otherwise), except the matrices of the
+ *    vocabulary operators.  Element offsets inside
  *    buffers need no alignment: the kernels handle any phase.
  *  - Arrays of per-rank pointers (grads[], master[], ...) are HOST arrays of
  *    n_ranks device pointers.  The library reads them during the call only.
@@ -519,6 +520,134 @@ zero3_status zero3_save_16bit_weights(const zero3_plan* plan, const uint16_t* fu
  * is created; ZERO3_EIO otherwise.  Memory use is one 16 MiB buffer. */
 zero3_status zero3_merge_shards(const zero3_plan* plan, const char* const* shard_paths,
                                 const char* persistent_path, const char* out_path);
+
+/* ---------------------------------------------------- vocabulary operators
+ * The two ends of a language model around the sharded step: tokens become
+ * rows of the gathered embedding table (zero3_fetch_submodule) and the
+ * table's gradient lands in the rank's gradient buffer that zero3_step
+ * reduces; the head's logits become log probabilities or a distillation loss,
+ * with their gradient.
+ *  - Matrices are row-major with a row stride in elements, at least the
+ *    number of columns.  Matrix pointers need the alignment of their elements
+ *    only (a gathered tensor may start at any element); rows whose starts are
+ *    16-byte aligned, or equally far from a 16-byte boundary on both sides of
+ *    an elementwise call, take the wide path.
+ *  - dtypes: ZERO3_BF16 or ZERO3_F32 each.  Everything is computed in
+ *    binary32 and rounded once, to nearest even, when it is stored.
+ *  - Token ids are int32 or int64 (zero3_itype).  An id outside [0, vocab)
+ *    marks an ignored position (padding); it is never read through.
+ *  - Results do not depend on timing: sums have a fixed order.
+ *  - No call allocates, synchronises or keeps anything; each can be captured
+ *    in a CUDA graph.  Outputs must not overlap inputs except where a call
+ *    says so.  n = 0 is a valid empty call.
+ *  - ZERO3_EINVAL, with nothing launched: unknown dtype or id type; NULL or
+ *    misaligned pointer; vocab < 1 or above 2^30; a stride below the columns;
+ *    n < 0 or above 2^27 rows of logits (2^31 - 1 tokens); rows times columns
+ *    above 2^41, or n * ceil(vocab / 8192) above 2^31 - 1 in the calls that
+ *    can write a gradient of logits; a scale that is not finite, or an
+ *    inverse temperature that is not finite and positive. */
+
+typedef enum zero3_itype { ZERO3_I32 = 0, ZERO3_I64 = 1 } zero3_itype;
+
+#define ZERO3_MAX_TOP 64
+#define ZERO3_MAX_TEACHER 1024
+
+/* Embedding lookup with scaling: out[i, :] = scale * table[ids[i], :] for
+ * i < n, `dim` columns; an ignored position's row is zero. */
+zero3_status zero3_embedding_forward(const void* table, zero3_dtype table_dtype, int64_t vocab,
+                                     int64_t dim, int64_t table_stride, const void* ids,
+                                     zero3_itype id_type, int64_t n, float scale, void* out,
+                                     zero3_dtype out_dtype, int64_t out_stride,
+                                     zero3_stream stream);
+
+/* Bytes of device workspace that zero3_embedding_backward needs (about
+ * 4 * (vocab + n) + (n / 64 + 1) * 4 * dim). */
+zero3_status zero3_embedding_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes);
+
+/* Gradient of the lookup with respect to the table:
+ *   s[v, :] = sum over i with ids[i] = v of dout[i, :]
+ *   accumulate = 0: grad[v, :] = scale * s[v, :] for EVERY v (zero where no
+ *     position has the token);
+ *   accumulate != 0: grad[v, :] += scale * s[v, :] for the tokens that occur
+ *     (a tied table: the output head's gradient is in the buffer already);
+ *     other rows are not touched.
+ * The positions are sorted by token first; each token's rows are added in
+ * binary32 in an order that depends on the ids alone.  workspace: 16-byte
+ * aligned device memory of at least zero3_embedding_workspace bytes, free
+ * for any use once the call's work on the stream is done. */
+zero3_status zero3_embedding_backward(const void* dout, zero3_dtype dout_dtype, int64_t dout_stride,
+                                      const void* ids, zero3_itype id_type, int64_t n, float scale,
+                                      int32_t accumulate, void* grad, zero3_dtype grad_dtype,
+                                      int64_t vocab, int64_t dim, int64_t grad_stride,
+                                      void* workspace, int64_t workspace_bytes,
+                                      zero3_stream stream);
+
+/* Log probabilities of given tokens, with entropy and the k most probable
+ * alternatives.  Per row, with z = logits * inv_temperature:
+ *   lse = log sum_j exp(z_j)           (optional, NULL: not written)
+ *   logprob = z[target] - lse          (0 for an ignored target)
+ *   entropy = -sum_j p_j log p_j       (optional)
+ *   top_ids, top_logprobs [n, k]: the k largest logits in descending order,
+ *     ties to the lowest index, and their log probabilities; k = 0: neither
+ *     is used.
+ * Masked tokens are -inf logits.  A row that a mask leaves without any token
+ * has lse = -inf, entropy 0, log probabilities -inf and top_ids 0..k-1.  A row
+ * with a NaN or +inf has NaN in every output that depends on it, and top_ids
+ * -1.  EINVAL also for k outside [0, min(vocab, ZERO3_MAX_TOP)]. */
+zero3_status zero3_token_logprobs(const void* logits, zero3_dtype dtype, int64_t n, int64_t vocab,
+                                  int64_t stride, const void* targets, zero3_itype id_type,
+                                  float inv_temperature, int32_t k, float* logprob, float* lse,
+                                  float* entropy, int32_t* top_ids, float* top_logprobs,
+                                  zero3_stream stream);
+
+/* Gradient of the above: with g = dlogprob[row] (0 where the target is
+ * ignored), h = dentropy[row], p = exp(z - lse):
+ *   dlogits_j = inv_temperature * ([j = target] g - p_j (g + h (log p_j + entropy)))
+ * and zero in a row without any token (lse = -inf).  lse and entropy are
+ * what the forward call wrote.  Either of dlogprob and dentropy may be NULL
+ * (no such gradient), entropy too if dentropy is.  dlogits has the logits'
+ * dtype and may be the logits themselves (same pointer and stride). */
+zero3_status zero3_token_logprobs_backward(const void* logits, zero3_dtype dtype, int64_t n,
+                                           int64_t vocab, int64_t stride, const void* targets,
+                                           zero3_itype id_type, float inv_temperature,
+                                           const float* lse, const float* entropy,
+                                           const float* dlogprob, const float* dentropy,
+                                           void* dlogits, int64_t dlogits_stride,
+                                           zero3_stream stream);
+
+/* Distillation from a teacher's top logits.  Row i of the teacher lists k
+ * tokens and their logits (teacher_ids, teacher_logits: [n, k], both with
+ * teacher_stride); an entry counts if its token is not ignored and its logit
+ * is not -inf, so lists may be shorter than k.  With a = inv_temperature:
+ *   q = softmax over the entries that count of a * teacher_logits
+ *   log p = log softmax over the vocabulary of a * logits
+ *   loss = (sum q_k (log q_k - log p[id_k])) / a^2
+ * A token listed more than once has the sum of its entries' q.  A row without
+ * a counting entry, or without any student token (all -inf), has loss 0 and a
+ * zero gradient; a NaN makes its row's loss and gradient NaN.  lse (optional)
+ * is the student's log-sum-exp for zero3_distill_backward.
+ * With dlogits (optional) the gradient of sum_i row_weight[i] * loss[i] is
+ * written by the same call, from one read of the logits:
+ *   dlogits_j = row_weight (p_j - sum of q_k over id_k = j) / a;
+ * row_weight NULL: 1.  dlogits has the logits' dtype and may be the logits
+ * themselves (same pointer and stride).  EINVAL also for k outside
+ * [1, ZERO3_MAX_TEACHER]. */
+zero3_status zero3_distill_loss(const void* logits, zero3_dtype dtype, int64_t n, int64_t vocab,
+                                int64_t stride, const void* teacher_logits,
+                                zero3_dtype teacher_dtype, const void* teacher_ids,
+                                zero3_itype id_type, int32_t k, int64_t teacher_stride,
+                                float inv_temperature, const float* row_weight, float* loss,
+                                float* lse, void* dlogits, int64_t dlogits_stride,
+                                zero3_stream stream);
+
+/* The gradient alone, from the lse that zero3_distill_loss wrote, when the
+ * losses' gradients (dloss[n]; NULL: 1) are known only afterwards. */
+zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64_t n, int64_t vocab,
+                                    int64_t stride, const void* teacher_logits,
+                                    zero3_dtype teacher_dtype, const void* teacher_ids,
+                                    zero3_itype id_type, int32_t k, int64_t teacher_stride,
+                                    float inv_temperature, const float* lse, const float* dloss,
+                                    void* dlogits, int64_t dlogits_stride, zero3_stream stream);
 
 /* ------------------------------------------------------------- accounting */
 

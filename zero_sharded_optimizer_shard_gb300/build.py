@@ -29,10 +29,11 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC"
 
 LIBS = {
     "libzero3.so": ["plan.cpp", "api.cpp", "checkpoint.cpp", "coordinator.cpp", "kernels.cu",
-                    "pieces.cu"],
+                    "pieces.cu", "operators.cpp", "embedding.cu", "logprobs.cu", "distill.cu"],
     "libzero3_synth.so": ["synth.cu"],
 }
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "device_common.cuh"),
+           os.path.join(CSRC, "operators.h"), os.path.join(CSRC, "vocab_common.cuh"),
            os.path.join(INCLUDE, "zero3.h")]
 
 

@@ -1,0 +1,486 @@
+// Log probabilities of given tokens with entropy and top alternatives, and
+// their gradient (sm_103a).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "vocab_common.cuh"
+
+namespace z3 {
+namespace {
+
+// ------------------------------------------------------- top alternatives
+// Keys that order binary32 values as unsigned integers; -0 counts as +0.  A
+// row's part with a NaN (its sum says so) never comes here: an addition's
+// NaN has the key 0xffffffff, and a bound one above it would wrap to 0.  Key 0
+// is below every value.
+__device__ __forceinline__ uint32_t key_of(float x) {
+    const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+    return b ^ (b & 0x80000000u ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+// A candidate: larger is better, equal values go to the lower index.
+__device__ __forceinline__ uint64_t candidate(uint32_t key, int32_t index) {
+    return (static_cast<uint64_t>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(index));
+}
+
+constexpr int kGroups = 128;     // groups of threads whose maxima bound the k-th value
+constexpr int kCandidates = 640; // candidates a block ranks
+
+struct TopShared {
+    uint64_t cand[kCandidates];
+    uint64_t top[ZERO3_MAX_TOP];
+    uint32_t group[kGroups];
+    uint16_t thread[512];
+    uint32_t bound;
+    int flagged, count, ntop, sum, first;
+};
+
+// One block's part of a row: elements [lo, hi) of the row, chunks [c0, c1).
+template <typename T>
+struct Part {
+    const T* row;
+    RowCut<T> cut;
+    int32_t c0, c1, lo, hi;
+};
+
+template <typename T>
+__device__ __forceinline__ float chunk_value(const Chunk<T>& c, int e) {
+    float lo, hi;
+    upk2(c.pair(e >> 1), lo, hi);
+    return e & 1 ? hi : lo;
+}
+
+__device__ __forceinline__ void offer(TopShared& sh, uint32_t key, int32_t index) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCandidates) sh.cand[at] = candidate(key, index);
+}
+
+// Offers the elements of chunk c whose key is at least `bound`.
+template <typename T>
+__device__ __forceinline__ void offer_chunk(TopShared& sh, const Part<T>& p, int32_t c,
+                                            uint32_t bound) {
+    Chunk<T> x;
+    const int32_t at = p.cut.head + 8 * c;
+    x.load(p.row + at);
+    if (key_of(x.max()) < bound) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t key = key_of(chunk_value(x, e));
+        if (key >= bound) offer(sh, key, at + e);
+    }
+}
+
+// Offers the elements of the part that lie outside its whole chunks (at most
+// 14) with keys of at least `bound`.
+template <typename T>
+__device__ __forceinline__ void offer_edges(TopShared& sh, const Part<T>& p, uint32_t bound) {
+    const int32_t first = p.cut.head + 8 * p.c0, last = p.cut.head + 8 * p.c1;
+    const int32_t i = threadIdx.x < 8 ? p.lo + static_cast<int32_t>(threadIdx.x)
+                                      : last + static_cast<int32_t>(threadIdx.x) - 8;
+    if (threadIdx.x < 16 && (threadIdx.x < 8 ? i < first : i < p.hi)) {
+        const uint32_t key = key_of(to_f32(p.row[i]));
+        if (key >= bound) offer(sh, key, i);
+    }
+}
+
+// Offers every element of the part with a key of at least `bound`, and
+// returns how many there are.
+template <typename T, int NT>
+__device__ int offer_all(TopShared& sh, const Part<T>& p, uint32_t bound) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.count = 0;
+    __syncthreads();
+    for (int32_t c = p.c0 + threadIdx.x; c < p.c1; c += NT) offer_chunk(sh, p, c, bound);
+    offer_edges(sh, p, bound);
+    __syncthreads();
+    return sh.count;
+}
+
+// Number of elements of the part with a key of at least `bound`.
+template <typename T, int NT>
+__device__ int count_from(TopShared& sh, const Part<T>& p, uint32_t bound) {
+    int n = 0;
+    for (int32_t i = p.lo + threadIdx.x; i < p.hi; i += NT) n += key_of(to_f32(p.row[i])) >= bound;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.sum = 0;
+    __syncthreads();
+    atomicAdd(&sh.sum, n);
+    __syncthreads();
+    return sh.sum;
+}
+
+// Adds to the candidates the first `need` elements, by index, whose key
+// equals `key`.
+template <typename T, int NT>
+__device__ void offer_equal(TopShared& sh, const Part<T>& p, uint32_t key, int need) {
+    __syncthreads();
+    if (threadIdx.x == 0) sh.first = 0;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int have = 0;  // the same in every thread
+    for (int32_t base = p.lo; base < p.hi && have < need; base += NT) {
+        const int32_t i = base + threadIdx.x;
+        const bool eq = i < p.hi && key_of(to_f32(p.row[i])) == key;
+        const uint32_t m = __ballot_sync(0xffffffffu, eq);
+        if (lane == 0) sh.group[warp] = __popc(m);
+        __syncthreads();
+        int before = have, all = 0;
+        for (int w = 0; w < NT / 32; ++w) {
+            const int c = static_cast<int>(sh.group[w]);
+            if (w < warp) before += c;
+            all += c;
+        }
+        before += __popc(m & ((1u << lane) - 1u));
+        if (eq && before < need) offer(sh, key, i);
+        have += all;
+        __syncthreads();
+    }
+}
+
+// The part's k best elements, best first, into sh.top (sh.ntop of them:
+// fewer than k only if the part has fewer elements).
+//
+// Every thread knows the largest element of its share (best; `any`: it has
+// a share).  The k-th largest of the 128 groups' maxima is a lower bound of
+// the part's k-th largest element, and only the threads whose own maximum
+// reaches it hold candidates: about k to 1.5 k of them, whose shares are
+// read again (from L2) by the whole block.  The candidates are then ranked
+// by counting.  Masses of equal values or shares that hold the top in a
+// regular pattern overflow the candidate list; then the exact k-th value is
+// found bit by bit, and equal ones are taken in index order.
+template <typename T, int NT>
+__device__ void select_top(TopShared& sh, const Part<T>& p, float best, bool any, int k) {
+    const int tid = threadIdx.x;
+    const uint32_t mine = any ? key_of(best) : 0u;
+    uint32_t g = mine;
+#pragma unroll
+    for (int o = NT / kGroups / 2; o > 0; o >>= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid == 0) sh.flagged = sh.count = 0;
+    if (tid % (NT / kGroups) == 0) sh.group[tid / (NT / kGroups)] = g;
+    __syncthreads();
+    if (tid < kGroups) {
+        const uint32_t me = sh.group[tid];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < kGroups; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&sh.group[j]);
+            rank += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
+            rank += (o.x == me && j < tid) + (o.y == me && j + 1 < tid) + (o.z == me && j + 2 < tid) +
+                    (o.w == me && j + 3 < tid);
+        }
+        if (rank == k - 1) sh.bound = me;
+    }
+    __syncthreads();
+    uint32_t bound = sh.bound;
+    if (mine >= bound && any) {
+        const int at = atomicAdd(&sh.flagged, 1);
+        sh.thread[at] = static_cast<uint16_t>(tid);
+    }
+    __syncthreads();
+    const int flagged = sh.flagged;
+    const int share = (p.c1 - p.c0 + NT - 1) / NT;
+    bool over = flagged > 4 * k + 32;
+    if (!over) {
+        for (int i = tid; i < flagged * share; i += NT) {
+            const int32_t c = p.c0 + sh.thread[i % flagged] + (i / flagged) * NT;
+            if (c < p.c1) offer_chunk(sh, p, c, bound);
+        }
+        offer_edges(sh, p, bound);
+        __syncthreads();
+        over = sh.count > kCandidates;
+    }
+    if (over) {  // block-uniform
+        int above = offer_all<T, NT>(sh, p, bound + 1);
+        if (above > kCandidates) {
+            bound = 0;
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t c = bound | (1u << b);
+                if (count_from<T, NT>(sh, p, c) >= k) bound = c;
+            }
+            above = offer_all<T, NT>(sh, p, bound + 1);
+        }
+        if (above < k) offer_equal<T, NT>(sh, p, bound, k - above);
+        __syncthreads();
+    }
+    const int n = min(sh.count, kCandidates);
+    for (int i = tid; i < n; i += NT) {
+        const uint64_t me = sh.cand[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += sh.cand[j] > me;
+        if (rank < k) sh.top[rank] = me;
+    }
+    if (tid == 0) sh.ntop = n < k ? n : k;
+    __syncthreads();
+}
+
+// One row per cluster of a.cluster blocks (one block where rows abound).
+// Bound by HBM: the row is read once, each thread keeping the running
+// maximum, sum and weighted sum of its share in registers.
+template <typename T, int NT, int U, bool ENT, bool TOP>
+__global__ void __launch_bounds__(NT) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+    __shared__ Soft sh_soft[NT / 32];
+    __shared__ Soft sh_part;
+    __shared__ TopShared sh_top;
+    wait_prior_grids();
+    allow_next_grid();
+    const int tid = threadIdx.x;
+    const int C = a.cluster;
+    const int64_t r = blockIdx.x / C;
+    const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const T* row = static_cast<const T*>(a.x) + r * a.stride;
+    const RowCut<T> cut(row, a.vocab);
+    const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(cut.chunks) * part / C);
+    const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(cut.chunks) * (part + 1) / C);
+    const bool head = part == 0, tail = part == C - 1;
+    // the target's logit, wanted at the end
+    int32_t y = -1;
+    float xy = 0.0f;
+    if (part == 0 && tid == 0) {
+        y = load_id(a.targets, a.id64, r, a.vocab);
+        if (y >= 0) xy = to_f32(row[y]);
+    }
+    Soft q = soft_empty();
+    soft_stream<T, ENT, NT, U>(q, row, cut, c0, c1, head, tail, a.scale);
+    const float best = q.m;
+    soft_block<ENT, NT>(q, sh_soft);
+    Part<T> p{row, cut, c0, c1, 0, 0};
+    if (TOP) {
+        p.lo = head ? 0 : cut.head + 8 * c0;
+        p.hi = tail ? a.vocab : cut.head + 8 * c1;
+        const bool any = c0 + tid < c1 || (tid == 0 && head && cut.head) ||
+                         (tid == NT - 1 && tail && cut.tail);
+        __syncthreads();
+        if (isnan(q.s)) {  // the same in every thread
+            if (tid == 0) sh_top.ntop = 0;
+        } else {
+            select_top<T, NT>(sh_top, p, best, any, a.k);
+        }
+    }
+    if (C > 1) {
+        if (tid == 0) sh_part = q;
+        cluster_sync();
+        if (part == 0) {
+            Soft o = soft_empty();
+            const uint32_t lane = tid & 31;
+            if (lane < static_cast<uint32_t>(C)) {
+                o.mz = __uint_as_float(ld_cluster(&sh_part.mz, lane));
+                o.s = __uint_as_float(ld_cluster(&sh_part.s, lane));
+                if (ENT) o.a = __uint_as_float(ld_cluster(&sh_part.a, lane));
+            }
+            soft_lanes<ENT, 32>(o);
+            q = o;
+            if (TOP) {  // the parts' lists, ranked by counting
+                if (tid == 0) sh_top.count = 0;
+                __syncthreads();
+                for (int i = tid; i < C * a.k; i += NT) {
+                    const int from = i / a.k, at = i % a.k;
+                    if (at < static_cast<int>(ld_cluster(&sh_top.ntop, from))) {
+                        const uint32_t* e = reinterpret_cast<const uint32_t*>(&sh_top.top[at]);
+                        const uint32_t lo = ld_cluster(e, from), hi = ld_cluster(e + 1, from);
+                        const int w = atomicAdd(&sh_top.count, 1);
+                        sh_top.cand[w] = (static_cast<uint64_t>(hi) << 32) | lo;
+                    }
+                }
+                __syncthreads();
+                const int n = sh_top.count;
+                for (int i = tid; i < n; i += NT) {
+                    const uint64_t me = sh_top.cand[i];
+                    int rank = 0;
+                    for (int j = 0; j < n; ++j) rank += sh_top.cand[j] > me;
+                    if (rank < a.k) sh_top.top[rank] = me;
+                }
+                __syncthreads();
+            }
+        }
+        cluster_sync();  // the parts' shared memory has been read
+        if (part != 0) return;
+    }
+    // q.s > 0, 0 (no element with weight) or NaN
+    const bool none = q.s == 0.0f;
+    const float logs = none ? 0.0f : logf(q.s);
+    if (tid == 0) {
+        a.logprob[r] = y < 0 ? 0.0f
+                       : none ? neg_inf()
+                              : __fsub_rn(fmaf(xy, a.scale, -q.mz), logs);
+        if (a.lse) a.lse[r] = none ? neg_inf() : __fadd_rn(q.mz, logs);
+        if (ENT) a.entropy[r] = none ? 0.0f : __fsub_rn(logs, __fdiv_rn(__fmul_rn(q.a, kLn2), q.s));
+    }
+    if (TOP) {
+        const bool bad = isnan(q.s);
+        for (int i = tid; i < a.k; i += NT) {
+            const uint64_t c = sh_top.top[i];
+            const float x = value_of(static_cast<uint32_t>(c >> 32));
+            const int64_t o = r * a.k + i;
+            a.top_ids[o] = bad ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
+            a.top_logprobs[o] = none ? neg_inf() : bad ? q.s : __fsub_rn(fmaf(x, a.scale, -q.mz), logs);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// dx_j = scale ([j = y] g - p_j (g + h (log p_j + H))), log p_j = z_j - lse.
+struct GradRow {
+    float scale, neg_lse;
+    float c0, c1;  // dx_j = p_j (c0 + c1 (z_j - lse)) besides the target
+    float hit;     // what the target gets on top
+    int32_t y;
+};
+
+template <bool ENT>
+__device__ __forceinline__ float grad_value(float x, const GradRow& g) {
+    const float d = fmaf(x, g.scale, g.neg_lse);
+    const float p = exp2_approx(__fmul_rn(d, kLog2e));
+    if (!ENT) return __fmul_rn(p, g.c0);
+    return __fmul_rn(p, fmaf(max_nan(d, -1e30f), g.c1, g.c0));
+}
+
+template <typename T, bool ENT>
+__device__ __forceinline__ void grad_chunk(const Chunk<T>& c, T* out, int32_t at, const GradRow& g) {
+    const uint64_t sc = pk2(g.scale, g.scale), nl = pk2(g.neg_lse, g.neg_lse);
+    const uint64_t l2 = pk2(kLog2e, kLog2e), c0 = pk2(g.c0, g.c0), c1 = pk2(g.c1, g.c1);
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint64_t d = fma2(c.pair(k), sc, nl);
+        float t0, t1;
+        upk2(mul2(d, l2), t0, t1);
+        const uint64_t p = pk2(exp2_approx(t0), exp2_approx(t1));
+        uint64_t w = c0;
+        if (ENT) {  // d = -inf has weight 0: keep 0 * d finite
+            upk2(d, t0, t1);
+            w = fma2(pk2(max_nan(t0, -1e30f), max_nan(t1, -1e30f)), c1, c0);
+        }
+        upk2(mul2(p, w), f[2 * k], f[2 * k + 1]);
+    }
+    const uint32_t h = static_cast<uint32_t>(g.y - at);  // y < 0 never matches: at >= 0
+    if (h < 8u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (h == static_cast<uint32_t>(e)) f[e] = __fadd_rn(f[e], g.hit);
+    }
+    Chunk<T>::store(out + at, f);
+}
+
+// A block takes 8 * NT * U consecutive elements of one row.  Elementwise and
+// bound by HBM (one read, one write); in-place is allowed, so every element
+// is read by the thread that writes it.  SAME: row and gradient row start at
+// the same distance from a 16-byte boundary, so one cut serves both.
+template <typename T, bool ENT, bool SAME, int NT, int U>
+__global__ void __launch_bounds__(NT)
+    logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
+    wait_prior_grids();
+    allow_next_grid();
+    const int64_t r = blockIdx.x / a.segments;
+    const int32_t seg = static_cast<int32_t>(blockIdx.x - r * a.segments);
+    const int tid = threadIdx.x;
+    const T* row = static_cast<const T*>(a.x) + r * a.stride;
+    T* out = static_cast<T*>(a.dx) + r * a.dx_stride;
+    const RowCut<T> cut(row, a.vocab);
+    const int32_t i0 = seg * NT * U + tid;
+    Chunk<T> c[U];
+    if (SAME) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * NT < cut.chunks)
+                c[u].load_stream(row + cut.head + 8 * static_cast<int64_t>(i0 + u * NT));
+    }
+    GradRow g;
+    const float lse = a.lse[r];
+    g.y = load_id(a.targets, a.id64, r, a.vocab);
+    const float gl = g.y >= 0 && a.dlogprob ? a.dlogprob[r] : 0.0f;
+    g.scale = a.scale;
+    g.neg_lse = -lse;
+    g.hit = __fmul_rn(gl, a.scale);
+    g.c0 = -g.hit;
+    g.c1 = 0.0f;
+    if (ENT) {
+        const float h = __fmul_rn(a.dentropy[r], a.scale);
+        g.c0 = -fmaf(h, a.entropy[r], g.hit);
+        g.c1 = -h;
+    }
+    if (lse == neg_inf()) {  // nothing left in the row: no gradient
+        g.neg_lse = 0.0f;
+        g.scale = 0.0f;
+        g.c0 = g.c1 = g.hit = 0.0f;
+    }
+    const bool none = lse == neg_inf();
+    if (SAME) {
+        if (none) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) c[u].fill(0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * NT < cut.chunks)
+                grad_chunk<T, ENT>(c[u], out, cut.head + 8 * (i0 + u * NT), g);
+        if (seg == 0 && tid < 16) {
+            const int32_t i = tid < 8 ? tid : cut.head + 8 * cut.chunks + tid - 8;
+            if (tid < 8 ? i < cut.head : i < a.vocab) {
+                float v = none ? 0.0f : grad_value<ENT>(to_f32(row[i]), g);
+                if (i == g.y) v = __fadd_rn(v, g.hit);
+                out[i] = from_f32<T>(v);
+            }
+        }
+    } else {
+        const int64_t lo = static_cast<int64_t>(seg) * NT * U * 8;
+#pragma unroll 8
+        for (int u = 0; u < 8 * U; ++u) {
+            const int64_t i = lo + u * NT + tid;
+            if (i < a.vocab) {
+                float v = none ? 0.0f : grad_value<ENT>(to_f32(row[i]), g);
+                if (i == g.y) v = __fadd_rn(v, g.hit);
+                out[i] = from_f32<T>(v);
+            }
+        }
+    }
+}
+
+template <typename T, bool ENT, bool TOP>
+cudaError_t launch_fwd(LogprobArgs a, cudaStream_t stream) {
+    constexpr int NT = 256, U = 4;
+    const int64_t chunks = a.vocab / 8;
+    int C = 1;
+    while (C < 8 && a.n * C < 304 && chunks / (2 * C) >= 2 * NT) C *= 2;
+    a.cluster = C;
+    if (chunks <= 512)
+        return launch_vocab(logprob_kernel<T, 128, U, ENT, TOP>, a.n, 128, 0, 1, a, stream);
+    return launch_vocab(logprob_kernel<T, NT, U, ENT, TOP>, a.n * C, NT, 0, C, a, stream);
+}
+
+template <typename T>
+cudaError_t launch_fwd_type(const LogprobArgs& a, cudaStream_t stream) {
+    if (a.entropy)
+        return a.k ? launch_fwd<T, true, true>(a, stream) : launch_fwd<T, true, false>(a, stream);
+    return a.k ? launch_fwd<T, false, true>(a, stream) : launch_fwd<T, false, false>(a, stream);
+}
+
+template <typename T, bool ENT>
+cudaError_t launch_bwd(LogprobGradArgs a, cudaStream_t stream) {
+    constexpr int NT = 256, U = 4;
+    a.segments = (a.vocab + 8 * NT * U - 1) / (8 * NT * U);
+    const auto phase = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) / sizeof(T)) % Chunk<T>::kPhase; };
+    const bool same = phase(a.x) == phase(a.dx) &&
+                      (a.n == 1 || (a.stride - a.dx_stride) % Chunk<T>::kPhase == 0);
+    const int64_t grid = a.n * a.segments;
+    return same ? launch_vocab(logprob_grad_kernel<T, ENT, true, NT, U>, grid, NT, 0, 1, a, stream)
+                : launch_vocab(logprob_grad_kernel<T, ENT, false, NT, U>, grid, NT, 0, 1, a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t stream) {
+    return a.dtype == ZERO3_F32 ? launch_fwd_type<float>(a, stream)
+                                : launch_fwd_type<uint16_t>(a, stream);
+}
+
+cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, cudaStream_t stream) {
+    if (a.dtype == ZERO3_F32)
+        return a.dentropy ? launch_bwd<float, true>(a, stream) : launch_bwd<float, false>(a, stream);
+    return a.dentropy ? launch_bwd<uint16_t, true>(a, stream)
+                      : launch_bwd<uint16_t, false>(a, stream);
+}
+
+}  // namespace z3

@@ -18,8 +18,11 @@ from .build import lib_path
 
 OK, EINVAL, ESTATE, ECUDA, ENOMEM, EIO = 0, 1, 2, 3, 4, 5
 BF16, F32 = 0, 1
+I32, I64 = 0, 1
 NOT_AVAILABLE, INFLIGHT, AVAILABLE = 0, 1, 2
 MAX_RANKS = 64
+MAX_TOP = 64
+MAX_TEACHER = 1024
 
 _c_i64_p = C.POINTER(C.c_int64)
 _c_i32_p = C.POINTER(C.c_int32)
@@ -134,6 +137,24 @@ _SIGS = [
     ("zero3_load_persistent", C.c_int, [_vp, _c_i64_p, C.POINTER(PersistState), C.c_char_p, _vp]),
     ("zero3_save_16bit_weights", C.c_int, [_vp, _vp, _vp, C.c_char_p, _vp]),
     ("zero3_merge_shards", C.c_int, [_vp, C.POINTER(C.c_char_p), C.c_char_p, C.c_char_p]),
+    ("zero3_embedding_forward", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, _vp,
+                                          C.c_int, C.c_int64, C.c_float, _vp, C.c_int, C.c_int64,
+                                          _vp]),
+    ("zero3_embedding_workspace", C.c_int, [C.c_int64, C.c_int64, C.c_int64, _c_i64_p]),
+    ("zero3_embedding_backward", C.c_int, [_vp, C.c_int, C.c_int64, _vp, C.c_int, C.c_int64,
+                                           C.c_float, C.c_int32, _vp, C.c_int, C.c_int64,
+                                           C.c_int64, C.c_int64, _vp, C.c_int64, _vp]),
+    ("zero3_token_logprobs", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, _vp, C.c_int,
+                                       C.c_float, C.c_int32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("zero3_token_logprobs_backward", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, _vp,
+                                                C.c_int, C.c_float, _vp, _vp, _vp, _vp, _vp,
+                                                C.c_int64, _vp]),
+    ("zero3_distill_loss", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, _vp, C.c_int,
+                                     _vp, C.c_int, C.c_int32, C.c_int64, C.c_float, _vp, _vp, _vp,
+                                     _vp, C.c_int64, _vp]),
+    ("zero3_distill_backward", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, _vp,
+                                         C.c_int, _vp, C.c_int, C.c_int32, C.c_int64, C.c_float,
+                                         _vp, _vp, _vp, C.c_int64, _vp]),
     ("zero3_plan_memory_bytes", C.c_int, [_vp, C.c_int32, C.POINTER(C.c_double)]),
     ("zero3_memory_bytes", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.POINTER(C.c_double)]),
     ("zero3_comm_elems", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.POINTER(C.c_double)]),
@@ -425,6 +446,63 @@ def zero3_merge_shards(plan: Plan, shard_paths, persistent_path, out_path):
     _check(plan._lib.zero3_merge_shards(plan.handle, arr,
                                         _path(persistent_path) if persistent_path else None,
                                         _path(out_path)), "zero3_merge_shards")
+
+
+def zero3_embedding_forward(table, table_dtype, vocab, dim, table_stride, ids, id_type, n, scale,
+                            out, out_dtype, out_stride, stream=0):
+    _check(load().zero3_embedding_forward(table, table_dtype, vocab, dim, table_stride, ids, id_type,
+                                          n, scale, out, out_dtype, out_stride, stream),
+           "zero3_embedding_forward")
+
+
+def zero3_embedding_workspace(n, vocab, dim) -> int:
+    out = C.c_int64()
+    _check(load().zero3_embedding_workspace(n, vocab, dim, C.byref(out)),
+           "zero3_embedding_workspace")
+    return out.value
+
+
+def zero3_embedding_backward(dout, dout_dtype, dout_stride, ids, id_type, n, scale, accumulate, grad,
+                             grad_dtype, vocab, dim, grad_stride, workspace, workspace_bytes,
+                             stream=0):
+    _check(load().zero3_embedding_backward(dout, dout_dtype, dout_stride, ids, id_type, n, scale,
+                                           accumulate, grad, grad_dtype, vocab, dim, grad_stride,
+                                           workspace, workspace_bytes, stream),
+           "zero3_embedding_backward")
+
+
+def zero3_token_logprobs(logits, dtype, n, vocab, stride, targets, id_type, inv_temperature, k,
+                         logprob, lse=0, entropy=0, top_ids=0, top_logprobs=0, stream=0):
+    _check(load().zero3_token_logprobs(logits, dtype, n, vocab, stride, targets, id_type,
+                                       inv_temperature, k, logprob, lse, entropy, top_ids,
+                                       top_logprobs, stream), "zero3_token_logprobs")
+
+
+def zero3_token_logprobs_backward(logits, dtype, n, vocab, stride, targets, id_type,
+                                  inv_temperature, lse, entropy, dlogprob, dentropy, dlogits,
+                                  dlogits_stride, stream=0):
+    _check(load().zero3_token_logprobs_backward(logits, dtype, n, vocab, stride, targets, id_type,
+                                                inv_temperature, lse, entropy, dlogprob, dentropy,
+                                                dlogits, dlogits_stride, stream),
+           "zero3_token_logprobs_backward")
+
+
+def zero3_distill_loss(logits, dtype, n, vocab, stride, teacher_logits, teacher_dtype, teacher_ids,
+                       id_type, k, teacher_stride, inv_temperature, row_weight, loss, lse=0,
+                       dlogits=0, dlogits_stride=0, stream=0):
+    _check(load().zero3_distill_loss(logits, dtype, n, vocab, stride, teacher_logits, teacher_dtype,
+                                     teacher_ids, id_type, k, teacher_stride, inv_temperature,
+                                     row_weight, loss, lse, dlogits, dlogits_stride, stream),
+           "zero3_distill_loss")
+
+
+def zero3_distill_backward(logits, dtype, n, vocab, stride, teacher_logits, teacher_dtype,
+                           teacher_ids, id_type, k, teacher_stride, inv_temperature, lse, dloss,
+                           dlogits, dlogits_stride, stream=0):
+    _check(load().zero3_distill_backward(logits, dtype, n, vocab, stride, teacher_logits,
+                                         teacher_dtype, teacher_ids, id_type, k, teacher_stride,
+                                         inv_temperature, lse, dloss, dlogits, dlogits_stride,
+                                         stream), "zero3_distill_backward")
 
 
 def zero3_plan_memory_bytes(plan: Plan, stage) -> float:
