@@ -109,9 +109,8 @@ def test_refusal_raises_in_the_binding(z):
 def test_workspace(z):
     for n, V, d in [(0, 1, 1), (1, 50257, 2048), (32768, 50257, 2048), (5, 3, 7)]:
         b = z.zero3_embedding_workspace(n, V, d)
-        slots = n // 64 + 1
-        assert 4 * (V + 1 + n) + slots * 4 * d <= b
-        assert b <= 4 * (V + 1 + n) + slots * (4 * (d + 3) + 4 * (d // 256 + 1)) + 64
+        assert 4 * (V + 1) + 4 * n <= b
+        assert b <= 4 * (V + 600) + 16 * n + (n // 32 + 1) * (8 * (d + 3) + 4 * (d // 256 + 1)) + 80
     out = C.c_int64()
     for bad in [(-1, 5, 5), (1, 0, 5), (1, 5, 0), (1 << 31, 5, 5), (1, 5, 1 << 42)]:
         assert z.raw_status("zero3_embedding_workspace", *bad, C.byref(out)) == z.EINVAL

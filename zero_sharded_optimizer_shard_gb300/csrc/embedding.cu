@@ -72,51 +72,71 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
 // ---------------------------------------------------------------- gradient
 // grad[v] = rne(base + scale * sum over the positions i of token v, in
 // ascending order, of dout[i]), in two launches: a stable counting sort of
-// the positions by token, and the rows' sums.
-//
-// Sums are binary32 and their order depends on the tokens alone, so the
-// result does not depend on timing.  A token with at most kLight positions is
-// summed by one warp (per slab of columns).  One with more is cut into tiles
-// of kTile positions, a block each, whose warps' sums are joined in shared
-// memory in order; the tiles' sums are joined in order by whichever block
-// comes last.  Tile t of the token whose positions start at sorted index s
-// has slot ceil(s / kLight) + t: every slot j of a token lies inside the
-// token's own range of sorted indices (64 j), so no two share one and a block
-// finds its tile from the sorted index 64 j alone.
-constexpr int kLight = 64;
-constexpr int kTile = 256;
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kOwn = 352;  // tokens a sorting block owns at most
-constexpr int kSumThreads = 256;
+// the positions by token, and the rows' sums.  Sums are binary32 and their
+// order depends on the tokens alone, so the result does not depend on timing.
+constexpr int kOwn = 448;          // tokens a sorting block owns at most
+constexpr int kWarpRows = 8;       // sorted positions whose pieces a summing warp takes
+constexpr int kPiece = 32;         // shortest piece of a token that has several
+constexpr int kSumThreads = 128;
+constexpr int kRing = 8192;        // bytes of rows in flight per summing warp
 constexpr int kSumWarps = kSumThreads / 32;
-constexpr int kSlabMin = 256;  // narrowest slab of columns
+constexpr int kGroupCols = 256;    // columns of a warp: 8 per lane, times CU
+constexpr int kZeroTokens = 8;     // tokens whose untouched rows one warp clears
+
+// A sorted position: where it was, its token, the token's first sorted index
+// and number of positions.
+struct alignas(16) Sorted {
+    int32_t pos, token, first, count;
+};
 
 struct Workspace {
-    int32_t* off;      // [vocab + 1] first sorted index of each token
-    int32_t* perm;     // [n] positions by token, ascending
-    int32_t* arrived;  // [slots * slabs] tiles of a token that are done
-    float* partial;    // [slots * dim] tile sums
-    int64_t slots, arrivals, bytes;
+    int32_t* off;      // [places + 1] first sorted index of the token at each place
+    Sorted* sorted;    // [n] positions by token, ascending
+    int32_t* arrived;  // [buckets * groups] pieces of a token that are done
+    float* partial;    // [buckets * 2 * dim] pieces' sums
+    int64_t buckets, groups, step, bytes;
 };
+
+// Tokens are dealt out to the sorting blocks like cards (token v to block
+// v mod 2^shift), because in text the frequent ones are neighbours; `place`
+// is where a token stands in the sorted order.
+struct Deal {
+    int32_t shift, own;  // blocks = 2^shift, tokens per block
+    __host__ __device__ __forceinline__ int32_t place(int32_t v) const {
+        return (v & ((1 << shift) - 1)) * own + (v >> shift);
+    }
+};
+
+// Sorting blocks: a power of two, about the SMs' number, more where a block
+// would own too many tokens.
+inline Deal deal_of(int64_t vocab) {
+    Deal d;
+    d.shift = 7;
+    while ((vocab + (int64_t{1} << d.shift) - 1) >> d.shift > kOwn) ++d.shift;
+    d.own = static_cast<int32_t>((vocab + (int64_t{1} << d.shift) - 1) >> d.shift);
+    return d;
+}
 
 __host__ __device__ inline int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
 
-__host__ __device__ inline Workspace workspace_of(void* base, int64_t n, int64_t vocab,
-                                                  int64_t dim) {
+inline Workspace workspace_of(void* base, int64_t n, int64_t vocab, int64_t dim) {
+    const Deal d = deal_of(vocab);
+    const int64_t places = static_cast<int64_t>(d.own) << d.shift;
     Workspace w;
-    w.slots = n / kLight + 1;
-    w.arrivals = w.slots * ((dim + kSlabMin - 1) / kSlabMin);
+    w.buckets = n / kPiece + 1;
+    w.groups = (dim + kGroupCols - 1) / kGroupCols;
+    w.step = (dim + 3) / 4 * 4;
     char* p = static_cast<char*>(base);
     int64_t o = 0;
-    w.off = reinterpret_cast<int32_t*>(p + o);
-    o += up16(4 * (vocab + 1));
-    w.perm = reinterpret_cast<int32_t*>(p + o);
-    o += up16(4 * n);
-    w.arrived = reinterpret_cast<int32_t*>(p + o);
-    o += up16(4 * w.arrivals);
-    w.partial = reinterpret_cast<float*>(p + o);
-    o += 4 * w.slots * ((dim + 3) / 4 * 4);
+    const auto take = [&](int64_t bytes) {
+        char* at = p + o;
+        o += up16(bytes);
+        return at;
+    };
+    w.off = reinterpret_cast<int32_t*>(take(4 * (places + 1)));
+    w.sorted = reinterpret_cast<Sorted*>(take(static_cast<int64_t>(sizeof(Sorted)) * n));
+    w.arrived = reinterpret_cast<int32_t*>(take(4 * w.buckets * w.groups));
+    w.partial = reinterpret_cast<float*>(take(8 * w.buckets * w.step));
     w.bytes = o;
     return w;
 }
@@ -124,276 +144,544 @@ __host__ __device__ inline Workspace workspace_of(void* base, int64_t n, int64_t
 struct SortArgs {
     const void* ids;
     Workspace w;
+    Deal deal;
     int64_t n;
-    int32_t vocab, own, id64;
+    int32_t vocab, id64;
 };
 
 // Stable counting sort without communication between blocks: every block
-// reads all ids, counts those below its own range of tokens (which gives the
-// range's first sorted index) and, warp by warp, those of each own token;
-// then each warp places its positions in order.
-__global__ void __launch_bounds__(kSortThreads)
-    embed_sort_kernel(const __grid_constant__ SortArgs a) {
-    __shared__ int32_t cnt[kSortWarps][kOwn];
-    __shared__ int32_t sh[kSortWarps], sh_scan[kSortWarps];
+// reads all ids, counts those of the blocks before it (which gives the first
+// sorted index of its own) and lists, warp by warp and in order, those of its
+// own tokens; the lists are counted by token, the counts summed up, and each
+// warp places its positions in order.  A warp's list that overflows (a token
+// that fills the batch) is read from the ids again.  Latency-bound: all that
+// counts is that a warp's loads are in flight together and that little is done
+// per id that is not the block's.
+template <int W, int J>
+__global__ void __launch_bounds__(32 * W) embed_sort_kernel(const __grid_constant__ SortArgs a) {
+    constexpr int NT = 32 * W;
+    constexpr int kList = 192;
+    __shared__ int32_t cnt[W][kOwn];
+    __shared__ uint32_t list[W][kList];  // token, position from i0 on
+    __shared__ int32_t first[kOwn], count[kOwn];
+    __shared__ int32_t sh[W], sh_scan[W];
     wait_prior_grids();
     allow_next_grid();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t v0 = blockIdx.x * a.own;
-    const int32_t own = min(a.own, a.vocab - v0);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < a.w.arrivals;
-         i += static_cast<int64_t>(gridDim.x) * kSortThreads)
-        a.w.arrived[i] = 0;
-    for (int i = tid; i < kSortWarps * kOwn; i += kSortThreads) (&cnt[0][0])[i] = 0;
-    __syncthreads();
-    const int64_t per = (a.n + kSortThreads - 1) / kSortThreads * 32;
+    const uint32_t below = (1u << lane) - 1u;
+    const int32_t me = blockIdx.x, mask = (1 << a.deal.shift) - 1, own = a.deal.own;
+    const int64_t per = (a.n + NT - 1) / NT * 32;
     const int64_t i0 = per * warp, i1 = i0 + per < a.n ? i0 + per : a.n;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * NT + tid; i < a.w.buckets * a.w.groups;
+         i += static_cast<int64_t>(gridDim.x) * NT)
+        a.w.arrived[i] = 0;
+    for (int k = lane; k < own; k += 32) cnt[warp][k] = 0;
+    __syncwarp();
     int32_t less = 0;
-#pragma unroll 4
-    for (int64_t i = i0 + lane; i < i1; i += 32) {
-        const int32_t id = load_id(a.ids, a.id64, i, a.vocab);
-        less += id >= 0 && id < v0;
-        const int32_t k = id - v0;
-        if (id >= v0 && k < own) atomicAdd(&cnt[warp][k], 1);
+    int n = 0;  // own positions of the warp
+    for (int64_t b = i0; b < i1; b += 32 * J) {
+        // an id as two words: valid if the high one is 0 and the low one
+        // below the vocabulary
+        uint32_t lo[J], hi[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int64_t i = b + 32 * j + lane;
+            lo[j] = 0xffffffffu;
+            hi[j] = 0;
+            if (i < i1) {
+                if (a.id64) {
+                    const uint2 x = static_cast<const uint2*>(a.ids)[i];
+                    lo[j] = x.x;
+                    hi[j] = x.y;
+                } else {
+                    lo[j] = static_cast<const uint32_t*>(a.ids)[i];
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool valid = hi[j] == 0 && lo[j] < static_cast<uint32_t>(a.vocab);
+            const int32_t o = valid ? static_cast<int32_t>(lo[j]) & mask : 0x7fffffff;
+            less += o < me;
+            const bool in = o == me;
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            if (!m) continue;
+            if (in) {
+                const int32_t k = static_cast<int32_t>(lo[j]) >> a.deal.shift;
+                const int at = n + __popc(m & below);
+                if (at < kList)
+                    list[warp][at] = static_cast<uint32_t>(k) << 16 |
+                                     static_cast<uint32_t>(b - i0 + 32 * j + lane);
+                atomicAdd(&cnt[warp][k], 1);
+            }
+            n += __popc(m);
+        }
     }
     for (int o = 16; o > 0; o >>= 1) less += __shfl_xor_sync(0xffffffffu, less, o);
     if (lane == 0) sh[warp] = less;
     __syncthreads();
-    // exclusive scan over the own tokens' totals, one token per thread
-    int32_t total = 0;
-    if (tid < own)
-        for (int w = 0; w < kSortWarps; ++w) total += cnt[w][tid];
-    int32_t incl = total;
+    // exclusive scan over the own tokens' totals, kPer tokens per thread
+    constexpr int kPer = (kOwn + NT - 1) / NT;
+    int32_t total[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int k = tid * kPer + j;
+        total[j] = 0;
+        if (k < own) {
+#pragma unroll 8
+            for (int w = 0; w < W; ++w) total[j] += cnt[w][k];
+        }
+        sum += total[j];
+    }
+    int32_t incl = sum;
     for (int o = 1; o < 32; o <<= 1) {
         const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) sh_scan[warp] = incl;
     __syncthreads();
-    int32_t run = incl - total;
-    for (int w = 0; w < kSortWarps; ++w) {
+    int32_t run = incl - sum;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
         run += sh[w];
         if (w < warp) run += sh_scan[w];
     }
-    if (tid < own) {
-        a.w.off[v0 + tid] = run;
-        if (v0 + tid == a.vocab - 1) a.w.off[a.vocab] = run + total;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int32_t c = cnt[w][tid];
-            cnt[w][tid] = run;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int k = tid * kPer + j;
+        if (k >= own) break;
+        a.w.off[me * own + k] = run;
+        if (me == mask && k == own - 1) a.w.off[(mask + 1) * own] = run + total[j];
+        first[k] = run;
+        count[k] = total[j];
+        if (total[j] == 0) continue;
+        for (int w = 0; w < W; ++w) {
+            const int32_t c = cnt[w][k];
+            cnt[w][k] = run;
             run += c;
         }
     }
     __syncthreads();
-    for (int64_t b = i0; b < i1; b += 32) {
-        const int64_t i = b + lane;
-        const int32_t id = i < i1 ? load_id(a.ids, a.id64, i, a.vocab) : -1;
-        const int32_t k = id - v0;
-        const bool in = id >= v0 && k < own;
-        if (!__any_sync(0xffffffffu, in)) continue;
-        const uint32_t peers = __match_any_sync(0xffffffffu, in ? k : -1);
-        const int rank = __popc(peers & ((1u << lane) - 1u));
-        if (in) a.w.perm[cnt[warp][k] + rank] = static_cast<int32_t>(i);
+    // places 32 positions i (those >= 0) of tokens k, in lane order
+    const auto place = [&](int32_t i, int32_t k) {
+        if (!__any_sync(0xffffffffu, i >= 0)) return;
+        const uint32_t peers = __match_any_sync(0xffffffffu, k);
+        const int rank = __popc(peers & below);
+        if (i >= 0) {
+            Sorted x;
+            x.pos = i;
+            x.token = (k << a.deal.shift) | me;
+            x.first = first[k];
+            x.count = count[k];
+            *reinterpret_cast<int4*>(a.w.sorted + cnt[warp][k] + rank) =
+                *reinterpret_cast<const int4*>(&x);
+        }
         __syncwarp();
-        if (in && rank == 0) cnt[warp][k] += __popc(peers);
+        if (i >= 0 && rank == 0) cnt[warp][k] += __popc(peers);
         __syncwarp();
+    };
+    if (n <= kList && per < 65536) {
+        for (int b = 0; b < n; b += 32) {
+            const bool in = b + lane < n;
+            const uint32_t x = in ? list[warp][b + lane] : 0;
+            place(in ? static_cast<int32_t>(i0 + (x & 0xffffu)) : -1, in ? static_cast<int32_t>(x >> 16) : -1);
+        }
+        return;
+    }
+    for (int64_t b = i0; b < i1; b += 32 * J) {
+        int32_t id[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int64_t i = b + 32 * j + lane;
+            id[j] = i < i1 ? load_id(a.ids, a.id64, i, a.vocab) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const bool in = id[j] >= 0 && (id[j] & mask) == me;
+            place(in ? static_cast<int32_t>(b + 32 * j + lane) : -1,
+                  in ? id[j] >> a.deal.shift : -1);
+        }
     }
 }
 
 struct SumArgs {
     EmbedGradArgs a;
     Workspace w;
+    Deal deal;
     int32_t slabs;
-    int64_t heavy_blocks;
+    int64_t sum_blocks;
 };
 
-// A lane's columns of a slab: CU chunks of 8, 32 chunks apart (VEC), or 8 CU
-// single columns, 32 apart.
-template <typename TD, bool VEC, int CU>
-struct Columns {
-    float acc[8 * CU];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int k = 0; k < 8 * CU; ++k) acc[k] = 0.0f;
-    }
-    // column of acc[k]
-    static __device__ __forceinline__ int32_t col(int32_t c0, int lane, int k) {
-        return VEC ? c0 + 8 * (lane + 32 * (k / 8)) + k % 8 : c0 + lane + 32 * k;
-    }
-    // adds rows perm[s..e) in order
-    __device__ __forceinline__ void add_rows(const SumArgs& p, int32_t s, int32_t e, int32_t c0,
-                                             int lane) {
-        const TD* dout = static_cast<const TD*>(p.a.dout);
-        const int32_t dim = static_cast<int32_t>(p.a.dim);
-        constexpr int R = VEC ? 2 : 4;  // rows in flight
-        for (int32_t b = s; b < e; b += 32) {
-            const int n = min(32, e - b);
-            const int32_t mine = lane < n ? p.w.perm[b + lane] : 0;
-            int j = 0;
-            for (; j + R <= n; j += R) rows<R>(dout, p.a.dout_stride, mine, j, c0, lane, dim);
-            for (; j < n; ++j) rows<1>(dout, p.a.dout_stride, mine, j, c0, lane, dim);
-        }
-    }
-    template <int R>
-    __device__ __forceinline__ void rows(const TD* dout, int64_t stride, int32_t mine, int j,
-                                         int32_t c0, int lane, int32_t dim) {
-        const TD* row[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            row[r] = dout + __shfl_sync(0xffffffffu, mine, j + r) * stride;
-        if (VEC) {
-            Chunk<TD> c[R][CU];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int u = 0; u < CU; ++u) {
-                    const int32_t at = c0 + 8 * (lane + 32 * u);
-                    c[r][u].fill(0.0f);
-                    if (at < dim) c[r][u].load_stream(row[r] + at);
-                }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int u = 0; u < CU; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float x, y;
-                        upk2(c[r][u].pair(k), x, y);
-                        acc[8 * u + 2 * k] = __fadd_rn(acc[8 * u + 2 * k], x);
-                        acc[8 * u + 2 * k + 1] = __fadd_rn(acc[8 * u + 2 * k + 1], y);
-                    }
-        } else {
-            float x[R][8 * CU];
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < 8 * CU; ++k) {
-                    const int32_t at = c0 + lane + 32 * k;
-                    x[r][k] = at < dim ? to_f32(row[r][at]) : 0.0f;
-                }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int k = 0; k < 8 * CU; ++k) acc[k] = __fadd_rn(acc[k], x[r][k]);
-        }
-    }
-};
-
-// grad[v][col] = rne(base + scale * x)
-template <typename TG>
-__device__ __forceinline__ void put(const SumArgs& p, int32_t v, int32_t col, float x) {
-    if (col >= p.a.dim) return;
-    TG* g = static_cast<TG*>(p.a.grad) + v * p.a.grad_stride + col;
-    *g = from_f32<TG>(p.a.accumulate ? fmaf(x, p.a.scale, to_f32(*g)) : __fmul_rn(x, p.a.scale));
+// A lane's columns: CU groups of 8, each a chunk (VEC) or 8 single columns,
+// 32 apart.  Group u starts at:
+template <bool VEC>
+__device__ __forceinline__ int32_t column(int32_t c0, int lane, int u) {
+    return c0 + kGroupCols * u + (VEC ? 8 * lane : lane);
 }
 
-template <typename TD, typename TG, bool VEC, int CU>
-__device__ __forceinline__ void put_row(const SumArgs& p, int32_t v, int32_t c0, int lane,
-                                        const Columns<TD, VEC, CU>& s) {
-    using Col = Columns<TD, VEC, CU>;
-    if (!VEC) {
-#pragma unroll
-        for (int k = 0; k < 8 * CU; ++k) put<TG>(p, v, Col::col(c0, lane, k), s.acc[k]);
-        return;
+// One group of a row.
+template <typename T, bool VEC>
+struct Group {
+    Chunk<T> c;
+    __device__ __forceinline__ void load(const T* row, int32_t at, int32_t dim) {
+        c.fill(0.0f);
+        if (at < dim) c.load_stream(row + at);
     }
-    TG* g = static_cast<TG*>(p.a.grad) + v * p.a.grad_stride;
-    Chunk<TG> old[CU];
-    if (p.a.accumulate) {
-#pragma unroll
-        for (int u = 0; u < CU; ++u) {
-            const int32_t at = c0 + 8 * (lane + 32 * u);
-            if (at < p.a.dim) old[u].load_stream(g + at);
-        }
+    // of what another SM has written during this launch (from L2)
+    __device__ __forceinline__ void load_far(const float* row, int32_t at, int32_t dim) {
+        c.fill(0.0f);
+        if (at >= dim) return;
+        c.a = __ldcg(reinterpret_cast<const float4*>(row + at));
+        c.b = __ldcg(reinterpret_cast<const float4*>(row + at + 4));
     }
+    __device__ __forceinline__ uint64_t pair(int k) const { return c.pair(k); }
+    static __device__ __forceinline__ void store(T* row, int32_t at, int32_t dim, const float* f) {
+        if (at < dim) Chunk<T>::store(row + at, f);
+    }
+};
+template <typename T>
+struct Group<T, false> {
+    float x[8];
+    __device__ __forceinline__ void load(const T* row, int32_t at, int32_t dim) {
 #pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = at + 32 * k < dim ? to_f32(row[at + 32 * k]) : 0.0f;
+    }
+    __device__ __forceinline__ void load_far(const float* row, int32_t at, int32_t dim) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = at + 32 * k < dim ? __ldcg(row + at + 32 * k) : 0.0f;
+    }
+    __device__ __forceinline__ uint64_t pair(int k) const { return pk2(x[2 * k], x[2 * k + 1]); }
+    static __device__ __forceinline__ void store(T* row, int32_t at, int32_t dim, const float* f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (at + 32 * k < dim) row[at + 32 * k] = from_f32<T>(f[k]);
+    }
+};
+
+template <typename TG, bool VEC, bool ACC>
+__device__ __forceinline__ void put_group(const SumArgs& p, int32_t v, int32_t at,
+                                          const uint64_t* acc, const Group<TG, VEC>& old) {
+    const uint64_t sc = pk2(p.a.scale, p.a.scale);
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        upk2(ACC ? fma2(acc[k], sc, old.pair(k)) : mul2(acc[k], sc), f[2 * k], f[2 * k + 1]);
+    Group<TG, VEC>::store(static_cast<TG*>(p.a.grad) + v * p.a.grad_stride, at,
+                          static_cast<int32_t>(p.a.dim), f);
+}
+
+// Clears the rows of tokens without a position: a warp takes kZeroTokens
+// tokens and all columns.
+template <typename TG, bool VEC>
+__device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t v0, int lane) {
+    const int64_t v = v0 + lane;
+    bool empty = false;
+    if (lane < kZeroTokens && v < p.a.vocab) {
+        const int32_t at = p.deal.place(static_cast<int32_t>(v));
+        empty = p.w.off[at] == p.w.off[at + 1];
+    }
+    uint32_t m = __ballot_sync(0xffffffffu, empty);
+    const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    while (m) {
+        TG* g = static_cast<TG*>(p.a.grad) + (v0 + __ffs(m) - 1) * p.a.grad_stride;
+        m &= m - 1;
+        if (VEC)
+            for (int64_t c = 8 * lane; c < p.a.dim; c += 256) Chunk<TG>::store(g + c, zero);
+        else
+            for (int64_t c = lane; c < p.a.dim; c += 32) g[c] = from_f32<TG>(0.0f);
+    }
+}
+
+// Positions of a piece: a token with up to 1024 positions is cut every 32,
+// longer ones so that neither a piece nor the number of pieces gets long.
+__device__ __forceinline__ int32_t piece_rows(int32_t count) {
+    return count <= 32 * kPiece ? kPiece
+           : count <= 128 * kPiece ? 2 * kPiece
+           : count <= 512 * kPiece ? 4 * kPiece
+                                   : 8 * kPiece;
+}
+// Row of `partial` for the piece that starts at sorted index `at`: the
+// pieces of tokens with several start at least kPiece apart but where one
+// token's last and the next one's first meet, so a bucket of kPiece indices
+// holds at most one first piece and one later one.
+__device__ __forceinline__ int64_t piece_slot(int32_t at, bool first) {
+    return 2 * static_cast<int64_t>(at / kPiece) + (first ? 1 : 0);
+}
+
+// Adds up a token's pieces in order and writes its row.
+template <typename TG, bool VEC, bool ACC, int CU>
+__device__ __forceinline__ void join(const SumArgs& p, int32_t v, int32_t first, int32_t count,
+                                  int32_t c0, int lane) {
+    const int32_t step = piece_rows(count), dim = static_cast<int32_t>(p.a.dim);
+    const TG* g = static_cast<const TG*>(p.a.grad) + v * p.a.grad_stride;
     for (int u = 0; u < CU; ++u) {
-        const int32_t at = c0 + 8 * (lane + 32 * u);
-        if (at >= p.a.dim) continue;
-        float f[8];
+        const int32_t at = column<VEC>(c0, lane, u);
+        Group<TG, VEC> old;
+        if (ACC) old.load(g, at, dim);
+        uint64_t acc[4] = {0, 0, 0, 0};
+        constexpr int R = 4;
+        for (int32_t b = 0; b < count; b += R * step) {
+            Group<float, VEC> x[R];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float x = 0.0f, y = 0.0f;
-            if (p.a.accumulate) {
-                upk2(old[u].pair(k), x, y);
-                f[2 * k] = fmaf(s.acc[8 * u + 2 * k], p.a.scale, x);
-                f[2 * k + 1] = fmaf(s.acc[8 * u + 2 * k + 1], p.a.scale, y);
-            } else {
-                f[2 * k] = __fmul_rn(s.acc[8 * u + 2 * k], p.a.scale);
-                f[2 * k + 1] = __fmul_rn(s.acc[8 * u + 2 * k + 1], p.a.scale);
+            for (int r = 0; r < R; ++r)
+                if (b + r * step < count)
+                    x[r].load_far(p.w.partial + piece_slot(first + b + r * step, b + r == 0) * p.w.step,
+                                  at, dim);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (b + r * step >= count) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = add2(acc[k], x[r].pair(k));
             }
         }
-        Chunk<TG>::store(g + at, f);
+        put_group<TG, VEC, ACC>(p, v, at, acc, old);
     }
 }
 
-template <typename TD, typename TG, bool VEC, int CU>
+// The pieces that a warp sums: those that start among kWarpRows consecutive
+// sorted positions, which together are consecutive rows [a, e) of the sorted
+// order (counted from j0).  Lane l knows position j0 + l.
+struct Pieces {
+    Sorted x;
+    uint32_t starts;
+    int32_t j0, a, e, count;
+    __device__ __forceinline__ bool last(int l) const {  // of its piece
+        return l == e - 1 || (l < kWarpRows - 1 && (starts >> (l + 1) & 1u));
+    }
+    __device__ __forceinline__ int piece_of(int l) const {  // where row l's piece starts
+        return 31 - __clz(l >= kWarpRows ? starts : starts & ((2u << l) - 1u));
+    }
+};
+
+// False if no piece starts there.
+__device__ __forceinline__ bool find_pieces(const SumArgs& p, int64_t tile, int lane, Pieces& q) {
+    const int64_t j = tile * kWarpRows;
+    if (j >= p.a.n) return false;
+    q.j0 = static_cast<int32_t>(j);
+    q.x = Sorted{0, -1, 0, 0};
+    if (j + lane < p.a.n)  // stale beyond the count, which arrives with it
+        *reinterpret_cast<int4*>(&q.x) = *reinterpret_cast<const int4*>(p.w.sorted + j + lane);
+    q.count = p.w.off[p.deal.own << p.deal.shift];  // ignored positions are not sorted
+    const int32_t size = piece_rows(q.x.count), at = q.j0 + lane;
+    q.starts = __ballot_sync(0xffffffffu, lane < kWarpRows && at < q.count &&
+                                              ((at - q.x.first) & (size - 1)) == 0);
+    if (!q.starts) return false;
+    q.a = __ffs(q.starts) - 1;
+    const int32_t end = min(at + size, q.x.first + q.x.count) - q.j0;
+    q.e = __shfl_sync(0xffffffffu, end, 31 - __clz(q.starts));
+    return true;
+}
+
+// Ends the piece that starts at lane `from`: the sum of a whole token is
+// written as it is (on top of `old`); one of several goes to `partial`, and
+// true is returned if it was the token's last to arrive.
+template <typename TG, bool VEC, bool ACC, int CU>
+__device__ __forceinline__ bool end_piece(const SumArgs& p, const Pieces& q, int from, int32_t slab,
+                                          int lane, uint64_t (&acc)[CU][4],
+                                          const Group<TG, VEC> (&old)[CU]) {
+    const int32_t c0 = slab * (kGroupCols * CU);
+    const int32_t v = __shfl_sync(0xffffffffu, q.x.token, from);
+    const int32_t n = __shfl_sync(0xffffffffu, q.x.count, from);
+    bool done = false;
+    if (n <= kPiece) {
+#pragma unroll
+        for (int u = 0; u < CU; ++u)
+            put_group<TG, VEC, ACC>(p, v, column<VEC>(c0, lane, u), acc[u], old[u]);
+    } else {
+        const int32_t first = __shfl_sync(0xffffffffu, q.x.first, from);
+        float* to = p.w.partial + piece_slot(q.j0 + from, q.j0 + from == first) * p.w.step;
+#pragma unroll
+        for (int u = 0; u < CU; ++u) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) upk2(acc[u][k], f[2 * k], f[2 * k + 1]);
+            Group<float, VEC>::store(to, column<VEC>(c0, lane, u), static_cast<int32_t>(p.a.dim), f);
+        }
+        __threadfence();
+        __syncwarp();
+        const int32_t step = piece_rows(n);
+        int all = 0;
+        if (lane == 0)
+            all = atomicAdd(p.w.arrived + static_cast<int64_t>(first / kPiece) * p.slabs + slab, 1) ==
+                  (n + step - 1) / step - 1;
+        done = __shfl_sync(0xffffffffu, all, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < CU; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[u][k] = 0;  // packed +0
+    return done;
+}
+
+template <typename TG, bool VEC, bool ACC, int CU>
+__device__ __forceinline__ void join_pieces(const SumArgs& p, const Pieces& q, uint32_t joins,
+                                            int32_t slab, int lane) {
+    while (joins) {
+        __threadfence();
+        const int from = __ffs(joins) - 1;
+        joins &= joins - 1;
+        join<TG, VEC, ACC, CU>(p, __shfl_sync(0xffffffffu, q.x.token, from),
+                               __shfl_sync(0xffffffffu, q.x.first, from),
+                               __shfl_sync(0xffffffffu, q.x.count, from),
+                               slab * (kGroupCols * CU), lane);
+    }
+}
+
+// The sums.  The sorted positions are cut into pieces (all of a token's
+// positions, or piece_rows of them), and a warp takes the pieces that start
+// among kWarpRows consecutive positions, for CU groups of columns: the work
+// is even however often a token occurs.  Pieces of one token are added up in
+// order by whichever warp of the token comes last.  Bound by HBM once there
+// are some thousand positions: each row is read once.
+//
+// Rows on 16-byte boundaries pass through a ring of D slots per warp in
+// shared memory, filled by asynchronous 16-byte copies (each lane reads what
+// it copied itself, so there are no barriers); the row that a sum is added to
+// takes a slot like the others, behind its piece's last row.
+template <typename TD, typename TG, bool ACC, int CU>
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_constant__ SumArgs p) {
-    constexpr int W = 256 * CU;  // columns of a slab
-    __shared__ float sh[kSumWarps][W];
-    __shared__ int sh_last;
+    constexpr int PD = sizeof(TD) / 2, PG = sizeof(TG) / 2;  // 16-byte parts per group
+    constexpr int P = CU * (ACC && PG > PD ? PG : PD);       // parts per slot
+    constexpr int D = kRing / (512 * P);
+    __shared__ __align__(16) uint4 ring[kSumWarps][D][P][32];
     wait_prior_grids();
     allow_next_grid();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Columns<TD, VEC, CU> s;
-    s.clear();
-    const int32_t* off = p.w.off;
-    if (blockIdx.x >= p.heavy_blocks) {  // one token per warp
-        const int64_t b = blockIdx.x - p.heavy_blocks;
-        const int64_t v = b / p.slabs * kSumWarps + warp;
-        const int32_t c0 = static_cast<int32_t>(b % p.slabs) * W;
-        if (v >= p.a.vocab) return;
-        const int32_t s0 = off[v], e0 = off[v + 1];
-        if (e0 - s0 > kLight || (e0 == s0 && p.a.accumulate)) return;
-        s.add_rows(p, s0, e0, c0, lane);
-        put_row<TD, TG, VEC, CU>(p, static_cast<int32_t>(v), c0, lane, s);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= p.sum_blocks) {
+        const int64_t b = blockIdx.x - p.sum_blocks;
+        clear_rows<TG, true>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
         return;
     }
-    // one tile of a token with many positions
-    const int32_t slot = static_cast<int32_t>(blockIdx.x / p.slabs);
-    const int32_t slab = static_cast<int32_t>(blockIdx.x % p.slabs);
-    const int32_t c0 = slab * W;
-    const int64_t at = static_cast<int64_t>(slot) * kLight;
-    if (at >= off[p.a.vocab]) return;
-    const int32_t v = load_id(p.a.ids, p.a.id64, p.w.perm[at], p.a.vocab);
-    const int32_t s0 = off[v], e0 = off[v + 1];
-    const int32_t first = (s0 + kLight - 1) / kLight, tile = slot - first;
-    const int32_t tiles = (e0 - s0 + kTile - 1) / kTile;
-    if (e0 - s0 <= kLight || tile >= tiles) return;
-    const int32_t t0 = s0 + tile * kTile, t1 = min(t0 + kTile, e0);
-    constexpr int kRows = kTile / kSumWarps;
-    const int32_t r0 = min(t0 + warp * kRows, t1), r1 = min(r0 + kRows, t1);
-    s.add_rows(p, r0, r1, c0, lane);
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp;
+    const int64_t tile = w / p.slabs;
+    const int32_t slab = static_cast<int32_t>(w - tile * p.slabs);
+    const int32_t c0 = slab * (kGroupCols * CU), dim = static_cast<int32_t>(p.a.dim);
+    Pieces q;
+    if (!find_pieces(p, tile, lane, q)) return;
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&ring[warp][0][0][lane]));
+    const auto copy = [&](const void* row, int parts, int bytes, int slot) {
 #pragma unroll
-    for (int k = 0; k < 8 * CU; ++k)
-        sh[warp][Columns<TD, VEC, CU>::col(0, lane, k)] = s.acc[k];
-    __syncthreads();
-    float* part = p.w.partial + static_cast<int64_t>(slot) * ((p.a.dim + 3) / 4 * 4);
-    for (int i = tid; i < W; i += kSumThreads) {
-        float x = sh[0][i];
+        for (int u = 0; u < CU; ++u) {
+            const int32_t at = column<true>(c0, lane, u);
+            if (at >= dim) continue;
+            const char* from = static_cast<const char*>(row) + static_cast<int64_t>(at) * bytes;
 #pragma unroll
-        for (int w = 1; w < kSumWarps; ++w) x = __fadd_rn(x, sh[w][i]);
-        if (tiles == 1)
-            put<TG>(p, v, c0 + i, x);
-        else if (c0 + i < p.a.dim)
-            part[c0 + i] = x;
+            for (int h = 0; h < 2; ++h)
+                if (h < parts)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     to + static_cast<uint32_t>((slot * P + u * parts + h) * 512)),
+                                 "l"(from + 16 * h)
+                                 : "memory");
+        }
+    };
+    int next = q.a, slot = 0;   // the next row to copy, and its slot
+    bool base = false;          // first the row that the sum before it is added to
+    int32_t pos = q.x.pos;
+    const auto issue = [&] {
+        if (ACC && base) {
+            base = false;
+            const int from = q.piece_of(next - 1);
+            copy(static_cast<const TG*>(p.a.grad) +
+                     __shfl_sync(0xffffffffu, q.x.token, from) * p.a.grad_stride,
+                 PG, sizeof(TG), slot);
+        } else if (next < q.e) {
+            if (next >= 32 && (next & 31) == 0)
+                pos = q.j0 + next + lane < q.count ? p.w.sorted[q.j0 + next + lane].pos : 0;
+            copy(static_cast<const TD*>(p.a.dout) +
+                     __shfl_sync(0xffffffffu, pos, next & 31) * p.a.dout_stride,
+                 PD, sizeof(TD), slot);
+            base = ACC && q.last(next);
+            ++next;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        slot = slot + 1 == D ? 0 : slot + 1;
+    };
+    const auto arrive = [&] { asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory"); };
+#pragma unroll 1
+    for (int i = 0; i < D; ++i) issue();
+    uint64_t acc[CU][4];
+#pragma unroll
+    for (int u = 0; u < CU; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[u][k] = 0;  // packed +0
+    uint32_t joins = 0;
+#pragma unroll 1
+    for (int l = q.a; l < q.e; ++l) {
+        arrive();
+#pragma unroll
+        for (int u = 0; u < CU; ++u) {
+            Group<TD, true> row;
+            row.c.from_parts(&ring[warp][slot][u * PD][lane], 32);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[u][k] = add2(acc[u][k], row.pair(k));
+        }
+        issue();
+        if (!q.last(l)) continue;
+        Group<TG, true> old[CU];
+        if (ACC) {
+            arrive();
+#pragma unroll
+            for (int u = 0; u < CU; ++u) old[u].c.from_parts(&ring[warp][slot][u * PG][lane], 32);
+            issue();
+        }
+        const int from = q.piece_of(l);
+        if (end_piece<TG, true, ACC, CU>(p, q, from, slab, lane, acc, old)) joins |= 1u << from;
     }
-    if (tiles == 1) return;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0)
-        sh_last = atomicAdd(&p.w.arrived[static_cast<int64_t>(first) * p.slabs + slab], 1) == tiles - 1;
-    __syncthreads();
-    if (!sh_last) return;
-    __threadfence();
-    const int64_t step = (p.a.dim + 3) / 4 * 4;
-    const float* all = p.w.partial + static_cast<int64_t>(first) * step;
-    for (int i = tid; i < W; i += kSumThreads) {
-        if (c0 + i >= p.a.dim) continue;
-        float x = 0.0f;
-#pragma unroll 8
-        for (int32_t t = 0; t < tiles; ++t) x = __fadd_rn(x, __ldcg(all + t * step + c0 + i));
-        put<TG>(p, v, c0 + i, x);
+    join_pieces<TG, true, ACC, CU>(p, q, joins, slab, lane);
+}
+
+// The same for rows at any alignment: single elements through registers, R
+// rows in flight.
+template <typename TD, typename TG, bool ACC>
+__global__ void __launch_bounds__(kSumThreads)
+    embed_sum_scalar_kernel(const __grid_constant__ SumArgs p) {
+    constexpr int R = 8;
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= p.sum_blocks) {
+        const int64_t b = blockIdx.x - p.sum_blocks;
+        clear_rows<TG, false>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
+        return;
     }
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp;
+    const int64_t tile = w / p.slabs;
+    const int32_t slab = static_cast<int32_t>(w - tile * p.slabs);
+    const int32_t at = column<false>(slab * kGroupCols, lane, 0), dim = static_cast<int32_t>(p.a.dim);
+    Pieces q;
+    if (!find_pieces(p, tile, lane, q)) return;
+    const TD* dout = static_cast<const TD*>(p.a.dout);
+    int32_t pos = q.x.pos;
+    uint64_t acc[1][4] = {{0, 0, 0, 0}};  // packed +0
+    uint32_t joins = 0;
+#pragma unroll 1
+    for (int b = q.a; b < q.e; b += R) {
+        Group<TD, false> rows[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int l = b + r;
+            if (l >= q.e) break;
+            if (l >= 32 && (l & 31) == 0)
+                pos = q.j0 + l + lane < q.count ? p.w.sorted[q.j0 + l + lane].pos : 0;
+            rows[r].load(dout + __shfl_sync(0xffffffffu, pos, l & 31) * p.a.dout_stride, at, dim);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int l = b + r;
+            if (l >= q.e) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[0][k] = add2(acc[0][k], rows[r].pair(k));
+            if (!q.last(l)) continue;
+            const int from = q.piece_of(l);
+            Group<TG, false> old[1];
+            if (ACC)
+                old[0].load(static_cast<const TG*>(p.a.grad) +
+                                __shfl_sync(0xffffffffu, q.x.token, from) * p.a.grad_stride,
+                            at, dim);
+            if (end_piece<TG, false, ACC, 1>(p, q, from, slab, lane, acc, old)) joins |= 1u << from;
+        }
+    }
+    join_pieces<TG, false, ACC, 1>(p, q, joins, slab, lane);
 }
 
 bool aligned_rows(const void* p, int64_t stride, int32_t dtype) {
@@ -420,25 +708,39 @@ cudaError_t embed_vec(const EmbedArgs& a, cudaStream_t stream) {
     return vec ? embed_typed<TT, TO, true>(a, stream) : embed_typed<TT, TO, false>(a, stream);
 }
 
-template <typename TD, typename TG, bool VEC, int CU>
-cudaError_t sum_typed(const EmbedGradArgs& a, const Workspace& w, cudaStream_t stream) {
+template <typename TD, typename TG, bool VEC, bool ACC, int CU>
+cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t stream) {
     SumArgs p;
     p.a = a;
     p.w = w;
-    p.slabs = static_cast<int32_t>((a.dim + 256 * CU - 1) / (256 * CU));
-    p.heavy_blocks = a.n > kLight ? w.slots * p.slabs : 0;
-    const int64_t grid = p.heavy_blocks + (a.vocab + kSumWarps - 1) / kSumWarps * p.slabs;
-    return launch_vocab(embed_sum_kernel<TD, TG, VEC, CU>, grid, kSumThreads, 0, 1, p, stream);
+    p.deal = deal_of(a.vocab);
+    p.slabs = static_cast<int32_t>((a.dim + kGroupCols * CU - 1) / (kGroupCols * CU));
+    p.sum_blocks = ((a.n + kWarpRows - 1) / kWarpRows * p.slabs + kSumWarps - 1) / kSumWarps;
+    const int64_t each = kSumWarps * kZeroTokens;
+    const int64_t grid = p.sum_blocks + (ACC ? 0 : (a.vocab + each - 1) / each);
+    if constexpr (VEC)
+        return launch_vocab(embed_sum_kernel<TD, TG, ACC, CU>, grid, kSumThreads, 0, 1, p, stream);
+    else
+        return launch_vocab(embed_sum_scalar_kernel<TD, TG, ACC>, grid, kSumThreads, 0, 1, p, stream);
+}
+
+template <typename TD, typename TG, bool VEC, bool ACC>
+cudaError_t sum_typed(const EmbedGradArgs& a, const Workspace& w, cudaStream_t stream) {
+    // two groups of columns per lane where that leaves few lanes idle
+    if (VEC && (a.dim % (2 * kGroupCols) == 0 || a.dim >= 8 * kGroupCols))
+        return sum_launch<TD, TG, VEC, ACC, VEC ? 2 : 1>(a, w, stream);
+    return sum_launch<TD, TG, VEC, ACC, 1>(a, w, stream);
 }
 
 template <typename TD, typename TG>
 cudaError_t sum_vec(const EmbedGradArgs& a, const Workspace& w, cudaStream_t stream) {
     const bool vec = a.dim % 8 == 0 && aligned_rows(a.dout, a.dout_stride, a.dout_dtype) &&
                      aligned_rows(a.grad, a.grad_stride, a.grad_dtype);
-    if (!vec) return sum_typed<TD, TG, false, 1>(a, w, stream);
-    if (a.dim <= 256) return sum_typed<TD, TG, true, 1>(a, w, stream);
-    if (a.dim <= 512) return sum_typed<TD, TG, true, 2>(a, w, stream);
-    return sum_typed<TD, TG, true, 4>(a, w, stream);
+    if (a.accumulate)
+        return vec ? sum_typed<TD, TG, true, true>(a, w, stream)
+                   : sum_typed<TD, TG, false, true>(a, w, stream);
+    return vec ? sum_typed<TD, TG, true, false>(a, w, stream)
+               : sum_typed<TD, TG, false, false>(a, w, stream);
 }
 
 }  // namespace
@@ -462,10 +764,11 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t stream) {
     s.n = a.n;
     s.vocab = static_cast<int32_t>(a.vocab);
     s.id64 = a.id64;
-    const int64_t each = (a.vocab + 151) / 152;
-    s.own = static_cast<int32_t>(each < 32 ? 32 : each > kOwn ? kOwn : each);
-    const int64_t grid = (a.vocab + s.own - 1) / s.own;
-    const cudaError_t e = launch_vocab(embed_sort_kernel, grid, kSortThreads, 0, 1, s, stream);
+    s.deal = deal_of(a.vocab);
+    const int64_t grid = int64_t{1} << s.deal.shift;
+    const cudaError_t e =
+        a.n <= 1024 ? launch_vocab(embed_sort_kernel<8, 4>, grid, 256, 0, 1, s, stream)
+                    : launch_vocab(embed_sort_kernel<16, 16>, grid, 512, 0, 1, s, stream);
     if (e != cudaSuccess) return e;
     if (a.dout_dtype == ZERO3_F32)
         return a.grad_dtype == ZERO3_F32 ? sum_vec<float, float>(a, s.w, stream)

@@ -70,6 +70,8 @@ struct Chunk<uint16_t> {
         r = *reinterpret_cast<const uint4*>(p);
     }
     __device__ __forceinline__ void load_stream(const uint16_t* p) { r = ldcs16(p); }
+    // from 16-byte parts that lie `step` apart
+    __device__ __forceinline__ void from_parts(const uint4* p, int) { r = *p; }
     // the largest element; NaNs are passed over
     __device__ __forceinline__ float max() const {
         uint32_t a, b;
@@ -106,6 +108,10 @@ struct Chunk<float> {
     __device__ __forceinline__ void load_stream(const float* p) {
         a = __ldcs(reinterpret_cast<const float4*>(p));
         b = __ldcs(reinterpret_cast<const float4*>(p + 4));
+    }
+    __device__ __forceinline__ void from_parts(const uint4* p, int step) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + step);
     }
     __device__ __forceinline__ float max() const {
         return fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
