@@ -433,7 +433,7 @@ def distill_case(Z, n, vocab, K, dtype, td, kind, xkind="normal", pads=(0, 0), o
     # the loss alone, and without the optional output
     l2 = torch.empty(n, device="cuda")
     Z.zero3_distill_loss(x.ptr, *head, None, l2.data_ptr(), None, None, 0, stream())
-    assert torch.equal(l2, loss)
+    close(l2.cpu(), rl, np.where(np.isfinite(ltol), ltol, 0))
     # the gradient alone
     gtol = gtol + wa * p * (st + 4 * U * (1 + big))[:, None]
     out.t.fill_(4.0)

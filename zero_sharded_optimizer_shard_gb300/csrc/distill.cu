@@ -4,6 +4,12 @@
 //   q = softmax over the row's valid teacher entries of t_k * scale
 //   loss = sum_k q_k (log q_k - log p_{id_k}) / scale^2,  p = softmax(x * scale)
 //   d loss / d x_j = (p_j - sum_{k: id_k = j} q_k) / scale
+//
+// A block has NT threads that stream logits and one more warp that works on
+// the teacher's list meanwhile: a list costs several dependent loads (token,
+// then the student's logit there) and a softmax of its own.  The gradient's
+// elements at the teacher's tokens are written by the list's warp, after the
+// streaming threads have announced that theirs are; those do not wait.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -13,80 +19,225 @@
 namespace z3 {
 namespace {
 
-// A row's teacher list in shared memory.
+enum class Make { kLoss, kBoth, kGrad };
+
+// ------------------------------------------------------------------- teacher
+constexpr int kMapBits = 65536;
+
+// A row's list in shared memory, k entries, and room to find repeated tokens.
 struct Teacher {
-    float q[ZERO3_MAX_TEACHER];        // probabilities; 0 where the entry does not count
-    float x[ZERO3_MAX_TEACHER];        // the student's logits at its tokens
-    alignas(16) int32_t id[ZERO3_MAX_TEACHER];  // tokens, -1 where the entry does not count
+    float* q;       // logits, then probabilities
+    float* x;       // the student's logits at the tokens
+    int32_t* id;    // tokens; -1 where the entry does not count or repeats a token
+    uint32_t* map;  // a bit per token of the block's part, or list_merge's table
+    int32_t map_bytes;
+    __device__ __forceinline__ Teacher(void* p, const DistillArgs& a)
+        : q(static_cast<float*>(p)), x(q + a.k), id(reinterpret_cast<int32_t*>(x + a.k)),
+          map(reinterpret_cast<uint32_t*>(static_cast<char*>(p) + entry_bytes(a.k))),
+          map_bytes(a.map_bytes) {}
+    __host__ __device__ static constexpr int entry_bytes(int k) { return (12 * k + 15) / 16 * 16; }
+    // slots of list_merge's table: a power of two, at most half full
+    __host__ __device__ static constexpr int table(int k) {
+        int t = 32;
+        while (t < 2 * k) t *= 2;
+        return t;
+    }
+    // of the map, for parts of up to `tokens`
+    __host__ static int bytes_of_map(int k, int64_t tokens) {
+        const int64_t bits = tokens < kMapBits ? tokens : kMapBits;
+        const int64_t map = (bits + 127) / 128 * 16, both = 8 * table(k);
+        return static_cast<int>(map > both ? map : both);
+    }
 };
 
-__device__ __forceinline__ float teacher_value(const DistillArgs& a, int64_t r, int k) {
-    const int64_t i = r * a.teacher_stride + k;
-    return a.teacher_dtype == ZERO3_F32 ? static_cast<const float*>(a.teacher)[i]
-                                        : bf16_f32(static_cast<const uint16_t*>(a.teacher)[i]);
-}
+// What the loss needs of a list: with r the largest student z among the
+// tokens, sum q (log q - z + r).  loss = that + (lse - r).
+struct ListSums {
+    float cross, ref;
+};
 
-// Loads row r's list and the student's logits at its tokens, and returns the
-// softmax statistics of the list (s = 0: no entry counts).  An entry counts
-// if its token lies in the vocabulary and its logit is not -inf.  Leaves
-// weights relative to the returned maximum in T.q.  Contains barriers.
-template <typename T, int NT>
-__device__ __forceinline__ Soft teacher_load(const DistillArgs& a, int64_t r, const T* row,
-                                             Teacher& t, Soft* sh) {
-    Soft s = soft_empty();
-    for (int k = threadIdx.x; k < a.k; k += NT) {
-        int32_t id = load_id(a.teacher_ids, a.id64, r * a.teacher_stride + k, a.vocab);
-        const float v = teacher_value(a, r, k);
-        if (v == neg_inf()) id = -1;
-        t.id[k] = id;
-        t.q[k] = v;
-        t.x[k] = id >= 0 ? to_f32(row[id]) : 0.0f;
-        if (id >= 0) s.m = fmaxf(s.m, v);
-    }
-    s.mz = __fmul_rn(s.m, a.scale);
-    if (s.mz == neg_inf()) s.mz = 0.0f;
-    for (int k = threadIdx.x; k < a.k; k += NT) {
-        if (t.id[k] < 0) continue;
-        s.s = __fadd_rn(s.s, exp2_approx(__fmul_rn(fmaf(t.q[k], a.scale, -s.mz), kLog2e)));
-    }
-    soft_block<false, NT>(s, sh);
-    return s;
-}
+// What a list is as a whole.
+enum ListKind : int { kListPlain, kListEmpty, kListNan };
 
-// Turns the list's logits into probabilities and returns this thread's part
-// of sum_k q_k (log q_k - (x_k scale - mz - logs)).
-template <int NT>
-__device__ __forceinline__ float teacher_loss(const DistillArgs& a, Teacher& t, const Soft& s,
-                                              float mz, float logs) {
-    const float tlog = logf(s.s);
-    float sum = 0.0f;
-    for (int k = threadIdx.x; k < a.k; k += NT) {
-        float q = 0.0f;
-        if (t.id[k] >= 0) {
-            const float d = fmaf(t.q[k], a.scale, -s.mz);
-            q = __fdiv_rn(exp2_approx(__fmul_rn(d, kLog2e)), s.s);
-            if (q != 0.0f) {
-                const float lp = __fsub_rn(fmaf(t.x[k], a.scale, -mz), logs);
-                sum = fmaf(q, __fsub_rn(__fsub_rn(d, tlog), lp), sum);
+// The list's warp, for row r, first step: its entries.  An entry counts if its
+// token lies in the vocabulary and its logit is not -inf.  Returns the list's
+// kind (in every lane): empty if no entry counts, NaN if the softmax of those
+// that do is.
+constexpr int kEntries = 4;  // entries per lane whose loads are in flight together
+__device__ __forceinline__ ListKind list_entries(const DistillArgs& a, int64_t r, const Teacher& t) {
+    const int lane = threadIdx.x & 31;
+    const int64_t base = r * a.teacher_stride;
+    bool some = false, nan = false;
+    for (int b = lane; b < a.k; b += 32 * kEntries) {
+        // loads without branches between them (a lane past the end takes the
+        // last entry), so that all are in flight together
+        uint32_t lo[kEntries], hi[kEntries];
+        float v[kEntries];
+        if (a.id64) {
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u) {
+                const uint2 x = static_cast<const uint2*>(a.teacher_ids)[base + min(b + 32 * u, a.k - 1)];
+                lo[u] = x.x;
+                hi[u] = x.y;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u) {
+                lo[u] = static_cast<const uint32_t*>(a.teacher_ids)[base + min(b + 32 * u, a.k - 1)];
+                hi[u] = 0;
             }
         }
+        if (a.teacher_dtype == ZERO3_F32) {
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u)
+                v[u] = static_cast<const float*>(a.teacher)[base + min(b + 32 * u, a.k - 1)];
+        } else {
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u)
+                v[u] = bf16_f32(static_cast<const uint16_t*>(a.teacher)[base + min(b + 32 * u, a.k - 1)]);
+        }
+#pragma unroll
+        for (int u = 0; u < kEntries; ++u) {
+            const int k = b + 32 * u;
+            if (k >= a.k) break;
+            const bool counts = hi[u] == 0 && lo[u] < static_cast<uint32_t>(a.vocab) && v[u] != neg_inf();
+            t.id[k] = counts ? static_cast<int32_t>(lo[u]) : -1;
+            t.q[k] = v[u];
+            some = some || counts;
+            nan = nan || (counts && !(__fmul_rn(v[u], a.scale) < -neg_inf()));
+        }
+    }
+    return __any_sync(0xffffffffu, nan) ? kListNan
+           : __any_sync(0xffffffffu, some) ? kListPlain
+                                           : kListEmpty;
+}
+
+// Second step: the student's logits at its tokens in [lo, hi).
+template <typename T>
+__device__ __forceinline__ void list_logits(const DistillArgs& a, const T* row, int32_t lo, int32_t hi,
+                                            const Teacher& t) {
+    const int lane = threadIdx.x & 31;
+    for (int b = lane; b < a.k; b += 32 * kEntries) {
+        T x[kEntries];
+#pragma unroll
+        for (int u = 0; u < kEntries; ++u) {  // without branches, as above
+            const int32_t id = t.id[min(b + 32 * u, a.k - 1)];
+            x[u] = row[id >= lo && id < hi ? id : 0];
+        }
+#pragma unroll
+        for (int u = 0; u < kEntries; ++u)
+            if (b + 32 * u < a.k) t.x[b + 32 * u] = to_f32(x[u]);
+    }
+}
+
+// Third step: the softmax; t.q turns from logits into probabilities.
+__device__ __forceinline__ ListSums list_softmax(const DistillArgs& a, const Teacher& t) {
+    const int lane = threadIdx.x & 31;
+    float top = neg_inf(), ref = neg_inf();
+    for (int k = lane; k < a.k; k += 32) {
+        if (t.id[k] < 0) continue;
+        top = fmaxf(top, t.q[k]);
+        ref = fmaxf(ref, t.x[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    }
+    top = __fmul_rn(top, a.scale);
+    if (top == neg_inf()) top = 0.0f;  // a list that is empty
+    ref = __fmul_rn(ref, a.scale);
+    if (ref == neg_inf()) ref = 0.0f;
+    float sum = 0.0f;
+    for (int k = lane; k < a.k; k += 32) {
+        if (t.id[k] < 0) continue;
+        const float d = fmaf(t.q[k], a.scale, -top);
+        sum = __fadd_rn(sum, exp2_approx(__fmul_rn(d, kLog2e)));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+    const float inv = __fdiv_rn(1.0f, sum), logs = logf(sum);
+    float cross = 0.0f;
+    for (int k = lane; k < a.k; k += 32) {
+        if (t.id[k] < 0) continue;
+        const float d = fmaf(t.q[k], a.scale, -top);
+        const float q = __fmul_rn(exp2_approx(__fmul_rn(d, kLog2e)), inv);
+        if (q != 0.0f)  // log q - (z - ref)
+            cross = fmaf(q, __fsub_rn(__fsub_rn(d, logs), fmaf(t.x[k], a.scale, -ref)), cross);
         t.q[k] = q;
     }
-    return sum;
-}
-
-template <int NT>
-__device__ __forceinline__ float block_sum(float x, float* sh) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0f;
-    for (int w = 0; w < NT / 32; ++w) x = __fadd_rn(x, sh[w]);
-    return x;
+    for (int o = 16; o > 0; o >>= 1) cross = __fadd_rn(cross, __shfl_xor_sync(0xffffffffu, cross, o));
+    return ListSums{cross, ref};
 }
 
+// Whether a token in [lo, hi) may be listed twice (in every lane): a bit per
+// token, shared by tokens kMapBits apart.  The map is Teacher::map.
+__device__ __forceinline__ bool list_repeats(const DistillArgs& a, const Teacher& t, int32_t lo,
+                                             int32_t hi) {
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < t.map_bytes / 16; i += 32)
+        reinterpret_cast<uint4*>(t.map)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    bool twice = false;
+    for (int k = lane; k < a.k; k += 32) {
+        const int32_t id = t.id[k];
+        if (id < lo || id >= hi) continue;
+        const uint32_t bit = static_cast<uint32_t>(id - lo) & (kMapBits - 1);
+        twice = twice || (atomicOr(t.map + bit / 32, 1u << (bit & 31)) >> (bit & 31) & 1u);
+    }
+    return __any_sync(0xffffffffu, twice);
+}
+
+// Leaves one entry per distinct token, which holds the sum of its entries'
+// probabilities in list order (fixed, 32 entries at a time); the others' id
+// turns -1.  A hash table over the map's memory finds the entry of a token.
+// Slow (a chain of atomics): only where tokens repeat.
+__device__ __noinline__ void list_merge(int count, const Teacher t) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t slots = Teacher::table(count), mask = slots - 1u;
+    int32_t* const key = reinterpret_cast<int32_t*>(t.map);  // tokens, and after them
+    int32_t* const at = key + slots;                          // the entry that stands for each
+    __syncwarp();
+    for (uint32_t s = lane; s < slots; s += 32) key[s] = -1;
+    for (int b = 0; b < count; b += 32) {
+        __syncwarp();
+        const int k = b + lane;
+        int32_t id = k < count ? t.id[k] : -1;
+        float q = id >= 0 ? t.q[k] : 0.0f;
+        // entries of this 32 with the same token: the first adds up the others
+        const uint32_t peers = __match_any_sync(0xffffffffu, id);
+        const bool lead = id >= 0 && (peers & ((1u << lane) - 1u)) == 0;
+        for (int l = 1; l < 32; ++l) {
+            const float o = __shfl_sync(0xffffffffu, q, l);
+            if (lead && l > lane && (peers >> l & 1u)) q = __fadd_rn(q, o);
+        }
+        // and stands in the table or adds to the entry that does
+        if (lead) {
+            uint32_t s = static_cast<uint32_t>(id) * 2654435761u >> 12 & mask;
+            for (uint32_t tries = 0; tries <= mask; ++tries) {  // at most half are taken
+                const int32_t there = atomicCAS(&key[s], -1, id);
+                if (there == -1) {
+                    at[s] = k;
+                    t.q[k] = q;
+                    break;
+                }
+                if (there == id) {
+                    t.q[at[s]] = __fadd_rn(t.q[at[s]], q);
+                    id = -1;
+                    break;
+                }
+                s = (s + 1) & mask;
+            }
+        } else {
+            id = -1;
+        }
+        if (k < count) t.id[k] = id;
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ gradient
 // What a sweep over a row writes: dx_j = coef 2^((x_j scale - base) log2 e),
 // less c q_k at the teacher's tokens.
 struct Sweep {
@@ -110,38 +261,24 @@ __device__ __forceinline__ void sweep_chunk(const Chunk<T>& c, T* out, const Swe
     }
     Chunk<T>::store(out, f);
 }
-
-// Elements of a part outside its whole chunks, [lo, first) and [last, hi):
-// at most seven each.
-template <typename T>
-__device__ __forceinline__ void sweep_edges(const T* row, T* out, int32_t lo, int32_t first,
-                                            int32_t last, int32_t hi, const Sweep& w) {
-    if (threadIdx.x >= 16) return;
-    const int32_t i = threadIdx.x < 8 ? lo + static_cast<int32_t>(threadIdx.x)
-                                      : last + static_cast<int32_t>(threadIdx.x) - 8;
-    if (threadIdx.x < 8 ? i < first : i < hi) out[i] = from_f32<T>(sweep_value(to_f32(row[i]), w));
+// The element of a part outside its whole chunks ([lo, first) and [last, hi),
+// at most seven each) that this thread has, or -1.
+__device__ __forceinline__ int32_t edge_element(int32_t lo, int32_t first, int32_t last, int32_t hi) {
+    const int tid = static_cast<int>(threadIdx.x);
+    if (tid < 8) return lo + tid < first ? lo + tid : -1;
+    if (tid < 16) return last + tid - 8 < hi ? last + tid - 8 : -1;
+    return -1;
 }
 
-// Writes the teacher's tokens in [lo, hi) over the sweep's values (after a
-// barrier).  A token listed more than once is written by its first entry,
-// which adds up the others' probabilities in list order.
-template <typename T, int NT>
+// Writes the gradient at the teacher's tokens in [lo, hi): `threads` threads
+// from `tid` on.
+template <typename T>
 __device__ __forceinline__ void write_teacher(const DistillArgs& a, const Teacher& t, T* out,
-                                              int64_t lo, int64_t hi, const Sweep& w) {
-    for (int k = threadIdx.x; k < a.k; k += NT) {
+                                              int64_t lo, int64_t hi, const Sweep& w, int tid,
+                                              int threads) {
+    for (int k = tid; k < a.k; k += threads) {
         const int32_t id = t.id[k];
-        if (id < lo || id >= hi) continue;
-        float q = t.q[k];
-        bool first = true;
-        for (int j = 0; j < a.k; ++j) {
-            if (t.id[j] != id || j == k) continue;
-            if (j < k) {
-                first = false;
-                break;
-            }
-            q = __fadd_rn(q, t.q[j]);
-        }
-        if (first) out[id] = from_f32<T>(fmaf(-w.c, q, sweep_value(t.x[k], w)));
+        if (id >= lo && id < hi) out[id] = from_f32<T>(fmaf(-w.c, t.q[k], sweep_value(t.x[k], w)));
     }
 }
 
@@ -150,150 +287,298 @@ __device__ __forceinline__ float row_coef(const DistillArgs& a, int64_t r) {
     return __fdiv_rn(w, a.scale);
 }
 
-// One row per cluster of a.cluster blocks: the row's statistics in one pass
-// over HBM, and with GRAD a second pass (from L2) that writes the gradient.
-template <typename T, bool GRAD, bool SAME, int NT, int U>
-__global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ DistillArgs a) {
-    __shared__ Teacher t;
-    __shared__ Soft sh_soft[NT / 32], sh_teacher[NT / 32];
+// ---------------------------------------------------------------------- loss
+// The row's statistics, joined over the block's W warps and a cluster's C
+// blocks.  `sh` has been filled and a barrier passed; every thread calls.
+template <int W>
+__device__ __forceinline__ Soft soft_all(const Soft* sh, Soft* sh_part, int C) {
+    Soft q = sh[(threadIdx.x & 31) % W];
+    soft_lanes<false, W>(q);
+    if (C == 1) return q;
+    if (threadIdx.x == 0) *sh_part = q;
+    cluster_sync();
+    Soft o = soft_empty();
+    const uint32_t lane = threadIdx.x & 31;
+    if (lane < static_cast<uint32_t>(C)) {
+        o.mz = __uint_as_float(ld_cluster(&sh_part->mz, lane));
+        o.s = __uint_as_float(ld_cluster(&sh_part->s, lane));
+    }
+    soft_lanes<false, 32>(o);
+    cluster_sync();  // every part's statistics have been read
+    return o;
+}
+
+__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t r, const Soft& q,
+                                           const ListSums& l, ListKind kind, float logs) {
+    const bool none = q.s == 0.0f;
+    float loss = 0.0f;
+    if (kind == kListNan)
+        loss = __int_as_float(0x7fffffff);
+    else if (!none && kind != kListEmpty)
+        loss = __fadd_rn(l.cross, __fadd_rn(__fsub_rn(q.mz, l.ref), logs));
+    a.loss[r] = __fdiv_rn(__fdiv_rn(loss, a.scale), a.scale);
+    if (a.lse) a.lse[r] = none ? neg_inf() : __fadd_rn(q.mz, logs);
+}
+
+// A block's part of a row: `n` chunks from element `start` on, elements
+// [lo, hi).
+template <typename T>
+struct RowPart {
+    const T* row;
+    int32_t start, n, lo, hi;
+    __device__ __forceinline__ RowPart(const DistillArgs& a, int64_t r, int part) {
+        row = static_cast<const T*>(a.x) + r * a.stride;
+        const RowCut<T> cut(row, a.vocab);
+        const int shift = 31 - __clz(a.cluster);
+        const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(cut.chunks) * part >> shift);
+        const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(cut.chunks) * (part + 1) >> shift);
+        start = cut.head + 8 * c0;
+        n = c1 - c0;
+        lo = part == 0 ? 0 : start;
+        hi = part + 1 == a.cluster ? a.vocab : start + 8 * n;
+    }
+};
+
+// The gradient, with (kBoth) or without (kGrad) the loss, of logits whose
+// gradient's rows are equally far from a 16-byte boundary.  One row per
+// cluster of a.cluster blocks.
+//
+// Bound by HBM (each logit read once, its gradient written once); kBoth reads
+// a row twice, the second time from L2, where the rows in flight (a few per
+// SM) stay.  What it takes is bytes in flight and few instructions per chunk:
+// the chunks of both passes come through one ring of two batches per thread
+// in shared memory, filled by asynchronous 16-byte copies (each thread reads
+// what it copied itself, so no barrier orders them), and the second pass's
+// first chunks are on their way while the block joins the row's statistics.
+template <typename T, Make M, int NT>
+__global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant__ DistillArgs a) {
+    constexpr bool LOSS = M == Make::kBoth;
+    constexpr int P = sizeof(T) / 2;  // 16-byte parts per chunk
+    constexpr int U = 4 / P;          // chunks per batch; two batches fill the ring
+    extern __shared__ uint4 dyn[];
+    __shared__ Soft sh[NT / 32];
     __shared__ Soft sh_part;
-    __shared__ float sh_sum[NT / 32];
+    __shared__ ListKind sh_kind;
     wait_prior_grids();
     allow_next_grid();
     const int tid = threadIdx.x;
     const int C = a.cluster;
     const int64_t r = blockIdx.x / C;
     const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const T* row = static_cast<const T*>(a.x) + r * a.stride;
-    const RowCut<T> cut(row, a.vocab);
-    const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(cut.chunks) * part / C);
-    const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(cut.chunks) * (part + 1) / C);
-    const bool head = part == 0, tail = part == C - 1;
-    const bool teach = GRAD || part == 0;  // uniform in a block
-    Soft ts = soft_empty();
-    if (teach) ts = teacher_load<T, NT>(a, r, row, t, sh_teacher);
-    Soft q = soft_empty();
-    soft_stream<T, false, NT, U>(q, row, cut, c0, c1, head, tail, a.scale);
-    soft_block<false, NT>(q, sh_soft);
-    if (C > 1) {
-        if (tid == 0) sh_part = q;
-        cluster_sync();
-        Soft o = soft_empty();
-        if (teach) {
-            const uint32_t lane = tid & 31;
-            if (lane < static_cast<uint32_t>(C)) {
-                o.mz = __uint_as_float(ld_cluster(&sh_part.mz, lane));
-                o.s = __uint_as_float(ld_cluster(&sh_part.s, lane));
-            }
-            soft_lanes<false, 32>(o);
-            q = o;
-        }
-        cluster_sync();  // every part's statistics have been read
-        if (!teach) return;
-    }
-    const bool none = q.s == 0.0f;
-    const bool dead = none || ts.s == 0.0f;
-    const float logs = none ? 0.0f : logf(q.s);
-    float loss = 0.0f;
-    if (!dead) loss = teacher_loss<NT>(a, t, ts, q.mz, logs);
-    loss = block_sum<NT>(loss, sh_sum);
-    if (part == 0 && tid == 0) {
-        a.loss[r] = __fdiv_rn(__fdiv_rn(loss, a.scale), a.scale);
-        if (a.lse) a.lse[r] = none ? neg_inf() : __fadd_rn(q.mz, logs);
-    }
-    if (!GRAD) return;
-    T* out = static_cast<T*>(a.dx) + r * a.dx_stride;
-    const int32_t lo = head ? 0 : cut.head + 8 * c0;
-    const int32_t hi = tail ? a.vocab : cut.head + 8 * c1;
-    if (dead) {
-        for (int32_t i = lo + tid; i < hi; i += NT) out[i] = from_f32<T>(0.0f);
-        return;
-    }
+    const RowPart<T> p(a, r, part);
+    T* const out = static_cast<T*>(a.dx) + r * a.dx_stride;
+    const int32_t last = p.start + 8 * p.n;
     Sweep w;
     w.scale = a.scale;
-    w.base = q.mz;
-    w.c = row_coef(a, r);
-    w.coef = __fdiv_rn(w.c, q.s);
-    if (isnan(ts.s)) w.coef = ts.s;
-    if (SAME) {
-        const T* p = row + cut.head;
-        T* d = out + cut.head;
-        int32_t i = c0 + tid;
-        for (; i + (U - 1) * NT < c1; i += U * NT) {
-            Chunk<T> c[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) c[u].load_stream(p + 8 * static_cast<int64_t>(i + u * NT));
+    if (tid >= NT) {  // the list's warp
+        const int lane = tid - NT;
+        const Teacher t(dyn + 2 * U * P * NT, a);
+        // the loss wants the logits at all tokens, from its first part
+        const bool all = LOSS && part == 0;
+        const ListKind kind = list_entries(a, r, t);
+        if (lane == 0) sh_kind = kind;
+        // the others' writes wait for the logits only where they overwrite them
+        const bool in_place = a.dx == a.x;
+        if (!LOSS && !in_place) __syncthreads();
+        list_logits<T>(a, p.row, all ? 0 : p.lo, all ? a.vocab : p.hi, t);
+        if (!LOSS && in_place) __syncthreads();
+        const ListSums l = list_softmax(a, t);
+        if (list_repeats(a, t, p.lo, p.hi)) list_merge(a.k, t);
+        if (LOSS) __syncthreads();
+        Soft q = soft_empty();
+        if (LOSS) {
+            q = soft_all<NT / 32>(sh, &sh_part, C);
+            if (part == 0 && lane == 0) write_loss(a, r, q, l, kind, q.s == 0.0f ? 0.0f : logf(q.s));
+        }
+        const float lse = LOSS ? 0.0f : a.lse[r];
+        if (kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf())) return;
+        w.base = LOSS ? q.mz : lse;
+        w.c = row_coef(a, r);
+        w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
+        if (kind == kListNan) w.coef = __int_as_float(0x7fffffff);
+        asm volatile("barrier.sync 1, %0;" ::"n"(NT + 32) : "memory");  // the others have written
+        write_teacher<T>(a, t, out, p.lo, p.hi, w, lane, 32);
+        return;
+    }
+    // batches of U chunks per thread, B of them per pass
+    uint4* const ring = dyn + tid;  // batch b, chunk u, part h: [((b & 1) * U + u) * P + h) * NT]
+    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const int full = p.n / (U * NT);                      // batches without a gap
+    const int B = (p.n + U * NT - 1) / (U * NT);
+    const int all = LOSS ? 2 * B : B;
+    const T* const first = p.row + p.start + 8 * tid;
+    // L2 keeps a row from the first pass for the second one
+    uint64_t keep, drop;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
+    const auto issue = [&](int b) {
+        if (b < all) {
+            const int c = (LOSS && b >= B ? b - B : b) * U * NT;  // chunks before the batch
+            const T* from = first + 8 * static_cast<int64_t>(c);
+            const uint32_t to = ring_at + static_cast<uint32_t>((b & 1) * (16 * U * P * NT));
+            const bool gaps = c + U * NT > p.n;
+            const uint64_t policy = b < B ? keep : drop;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                sweep_chunk<T>(c[u], d + 8 * static_cast<int64_t>(i + u * NT), w);
+                if (!gaps || c + u * NT + tid < p.n) {
+#pragma unroll
+                    for (int h = 0; h < P; ++h)
+                        if (LOSS)
+                            asm volatile(
+                                "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
+                                    to + 16 * NT * (u * P + h)),
+                                "l"(from + 8 * NT * u + h * (8 / P)), "l"(policy)
+                                : "memory");
+                        else
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             to + 16 * NT * (u * P + h)),
+                                         "l"(from + 8 * NT * u + h * (8 / P))
+                                         : "memory");
+                }
         }
-        for (; i < c1; i += NT) {
-            Chunk<T> c;
-            c.load_stream(p + 8 * static_cast<int64_t>(i));
-            sweep_chunk<T>(c, d + 8 * static_cast<int64_t>(i), w);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // takes batch b out of the ring and sends batch b + 2 after it
+    const auto take = [&](int b, Chunk<T> (&c)[U]) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint4* from = ring + (b & 1) * (U * P * NT);
+#pragma unroll
+        for (int u = 0; u < U; ++u) c[u].from_parts(from + u * P * NT, NT);
+        issue(b + 2);
+    };
+    issue(0);
+    issue(1);
+    const int32_t edge = edge_element(p.lo, p.start, last, p.hi);
+    const float edge_x = edge >= 0 ? to_f32(p.row[edge]) : 0.0f;
+    Soft q = soft_empty();
+    if (LOSS) {
+        if (edge >= 0) {
+            Chunk<T> c[1];
+            c[0].fill(neg_inf());
+            c[0].set(0, p.row[edge]);
+            soft_add<T, false, 1>(q, c, a.scale);
         }
-        sweep_edges<T>(row, out, lo, cut.head + 8 * c0, cut.head + 8 * c1, hi, w);
-    } else {
-        for (int32_t i = lo + tid; i < hi; i += NT)
-            out[i] = from_f32<T>(sweep_value(to_f32(row[i]), w));
+#pragma unroll 1
+        for (int b = 0; b < full; ++b) {
+            Chunk<T> c[U];
+            take(b, c);
+            soft_add<T, false, U>(q, c, a.scale);
+        }
+        if (full < B) {
+            Chunk<T> c[U];
+            take(full, c);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if ((full * U + u) * NT + tid < p.n)
+                    soft_add<T, false, 1>(q, reinterpret_cast<Chunk<T>(&)[1]>(c[u]), a.scale);
+        }
+        soft_lanes<false, 32>(q);
+        if ((tid & 31) == 0) sh[tid >> 5] = q;
     }
     __syncthreads();
-    write_teacher<T, NT>(a, t, out, lo, hi, w);
-}
-
-// The gradient from a saved lse.  A block takes 8 * NT * U consecutive
-// elements of one row.
-template <typename T, bool SAME, int NT, int U>
-__global__ void __launch_bounds__(NT) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
-    __shared__ Teacher t;
-    __shared__ Soft sh_teacher[NT / 32];
-    wait_prior_grids();
-    allow_next_grid();
-    const int64_t r = blockIdx.x / a.segments;
-    const int32_t seg = static_cast<int32_t>(blockIdx.x - r * a.segments);
-    const int tid = threadIdx.x;
-    const T* row = static_cast<const T*>(a.x) + r * a.stride;
-    T* out = static_cast<T*>(a.dx) + r * a.dx_stride;
-    const RowCut<T> cut(row, a.vocab);
-    // chunks [c0, c1) and, for the first and last block, the row's edges
-    const int32_t c0 = min(seg * NT * U, cut.chunks), c1 = min(c0 + NT * U, cut.chunks);
-    const int32_t lo = seg == 0 ? 0 : cut.head + 8 * c0;
-    const int32_t hi = seg == a.segments - 1 ? a.vocab : cut.head + 8 * c1;
-    const float lse = a.lse[r];
-    const Soft ts = teacher_load<T, NT>(a, r, row, t, sh_teacher);
-    if (ts.s == 0.0f || lse == neg_inf()) {
-        for (int32_t i = lo + tid; i < hi; i += NT) out[i] = from_f32<T>(0.0f);
+    if (LOSS) q = soft_all<NT / 32>(sh, &sh_part, C);
+    const float lse = LOSS ? 0.0f : a.lse[r];
+    const ListKind kind = sh_kind;
+    const bool dead = kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf());
+    w.base = LOSS ? q.mz : lse;
+    w.c = row_coef(a, r);
+    w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
+    if (kind == kListNan) w.coef = __int_as_float(0x7fffffff);
+    T* to = out + p.start + 8 * tid;
+    if (dead) {
+        const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int32_t c = tid; c < p.n; c += NT, to += 8 * NT) Chunk<T>::store(to, zero);
+        if (edge >= 0) out[edge] = from_f32<T>(0.0f);
         return;
     }
-    for (int k = tid; k < a.k; k += NT) {
-        const float d = fmaf(t.q[k], a.scale, -ts.mz);
-        t.q[k] = t.id[k] >= 0 ? __fdiv_rn(exp2_approx(__fmul_rn(d, kLog2e)), ts.s) : 0.0f;
+#pragma unroll 1
+    for (int b = 0; b < full; ++b, to += 8 * U * NT) {
+        Chunk<T> c[U];
+        take(LOSS ? B + b : b, c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
+    }
+    if (full < B) {
+        Chunk<T> c[U];
+        take(LOSS ? B + full : full, c);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if ((full * U + u) * NT + tid < p.n) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
+    }
+    if (edge >= 0) out[edge] = from_f32<T>(sweep_value(edge_x, w));
+    __threadfence_block();
+    asm volatile("barrier.arrive 1, %0;" ::"n"(NT + 32) : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The loss alone, and the gradient of rows that are not as far from a 16-byte
+// boundary as the gradient's rows: one row per cluster of a.cluster blocks,
+// the gradient written by single elements.
+template <typename T, Make M, int NT, int U>
+__global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_constant__ DistillArgs a) {
+    constexpr bool GRAD = M != Make::kLoss, LOSS = M != Make::kGrad;
+    extern __shared__ uint4 dyn[];
+    __shared__ Soft sh[NT / 32];
+    __shared__ Soft sh_part;
+    __shared__ ListSums sh_list;
+    __shared__ ListKind sh_kind;
+    wait_prior_grids();
+    allow_next_grid();
+    const Teacher t(dyn, a);
+    const int tid = threadIdx.x;
+    const int C = a.cluster;
+    const int64_t r = blockIdx.x / C;
+    const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const RowPart<T> p(a, r, part);
+    const RowCut<T> cut(p.row, a.vocab);
+    const int32_t c0 = (p.start - cut.head) / 8;
+    if (tid >= NT) {
+        if (GRAD || part == 0) {
+            const ListKind kind = list_entries(a, r, t);
+            list_logits<T>(a, p.row, 0, a.vocab, t);
+            const ListSums l = list_softmax(a, t);
+            if (GRAD && list_repeats(a, t, p.lo, p.hi)) list_merge(a.k, t);
+            if (tid == NT) {
+                sh_kind = kind;
+                sh_list = l;
+            }
+        }
+    } else if (LOSS) {
+        Soft q = soft_empty();
+        soft_stream<T, false, NT, U>(q, p.row, cut, c0, c0 + p.n, part == 0, part == C - 1, a.scale);
+        soft_lanes<false, 32>(q);
+        if ((tid & 31) == 0) sh[tid >> 5] = q;
+    }
+    __syncthreads();
+    Soft q = soft_empty();
+    if (LOSS)
+        q = soft_all<NT / 32>(sh, &sh_part, C);
+    else if (C > 1)
+        cluster_sync();  // in place, every part's list has read the row
+    if (LOSS && part == 0 && tid == 0)
+        write_loss(a, r, q, sh_list, sh_kind, q.s == 0.0f ? 0.0f : logf(q.s));
+    if (!GRAD) return;
+    T* out = static_cast<T*>(a.dx) + r * a.dx_stride;
+    const float lse = LOSS ? 0.0f : a.lse[r];
+    if (sh_kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf())) {
+        for (int32_t i = p.lo + tid; i < p.hi; i += NT + 32) out[i] = from_f32<T>(0.0f);
+        return;
     }
     Sweep w;
     w.scale = a.scale;
-    w.base = lse;
+    w.base = LOSS ? q.mz : lse;
     w.c = row_coef(a, r);
-    w.coef = isnan(ts.s) ? ts.s : w.c;
-    __syncthreads();  // the row's logits at the teacher's tokens have been read
-    if (SAME) {
-        Chunk<T> c[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + tid + u * NT < c1)
-                c[u].load_stream(row + cut.head + 8 * static_cast<int64_t>(c0 + tid + u * NT));
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + tid + u * NT < c1)
-                sweep_chunk<T>(c[u], out + cut.head + 8 * static_cast<int64_t>(c0 + tid + u * NT), w);
-        sweep_edges<T>(row, out, lo, cut.head + 8 * c0, cut.head + 8 * c1, hi, w);
-    } else {
-        for (int32_t i = lo + tid; i < hi; i += NT)
-            out[i] = from_f32<T>(sweep_value(to_f32(row[i]), w));
-    }
+    w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
+    if (sh_kind == kListNan) w.coef = __int_as_float(0x7fffffff);
+#pragma unroll 4
+    for (int32_t i = p.lo + tid; i < p.hi; i += NT + 32)
+        out[i] = from_f32<T>(sweep_value(to_f32(p.row[i]), w));
     __syncthreads();
-    write_teacher<T, NT>(a, t, out, lo, hi, w);
+    write_teacher<T>(a, t, out, p.lo, p.hi, w, tid, NT + 32);
 }
 
+// ------------------------------------------------------------------ launches
 template <typename T>
 bool same_phase(const DistillArgs& a) {
     const auto phase = [](const void* p) {
@@ -303,28 +588,46 @@ bool same_phase(const DistillArgs& a) {
            (a.n == 1 || (a.stride - a.dx_stride) % Chunk<T>::kPhase == 0);
 }
 
-template <typename T>
-cudaError_t launch_loss(DistillArgs a, cudaStream_t stream) {
-    constexpr int NT = 256, U = 4;
-    const int64_t chunks = a.vocab / 8;
+// Blocks per row: more than one where rows are few and long.
+int row_blocks(int64_t n, int64_t chunks, int threads) {
     int C = 1;
-    while (C < 8 && a.n * C < 304 && chunks / (2 * C) >= 2 * NT) C *= 2;
-    a.cluster = C;
-    if (!a.dx)
-        return launch_vocab(distill_kernel<T, false, true, NT, U>, a.n * C, NT, 0, C, a, stream);
-    return same_phase<T>(a)
-               ? launch_vocab(distill_kernel<T, true, true, NT, U>, a.n * C, NT, 0, C, a, stream)
-               : launch_vocab(distill_kernel<T, true, false, NT, U>, a.n * C, NT, 0, C, a, stream);
+    while (C < 8 && n * C < 304 && chunks / (2 * C) >= 2 * threads) C *= 2;
+    return C;
+}
+
+template <typename T, Make M, int NT>
+cudaError_t launch(DistillArgs a, cudaStream_t stream) {
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    const int64_t chunks = a.vocab / 8;
+    a.cluster = row_blocks(a.n, chunks, NT);
+    // a part has at most this many tokens: its chunks and 14 elements
+    a.map_bytes = M == Make::kLoss ? 0 : Teacher::bytes_of_map(a.k, 8 * (chunks / a.cluster + 1) + 14);
+    const int list = Teacher::entry_bytes(a.k) + a.map_bytes;
+    if constexpr (M != Make::kLoss) {
+        constexpr int kRing = 8 * 16 * NT, kMost = 96 * 1024;
+        if (same_phase<T>(a)) {
+            if (kRing + list > 46 * 1024) {
+                const cudaError_t e = cudaFuncSetAttribute(
+                    distill_kernel<T, M, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+                if (e != cudaSuccess) return e;
+            }
+            return launch_vocab(distill_kernel<T, M, NT>, a.n * a.cluster, NT + 32, kRing + list,
+                                a.cluster, a, stream);
+        }
+    }
+    return launch_vocab(distill_plain_kernel<T, M, NT, U>, a.n * a.cluster, NT + 32, list, a.cluster,
+                        a, stream);
+}
+
+template <typename T, Make M>
+cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
+    // short rows: more and smaller blocks
+    return a.vocab <= 8192 ? launch<T, M, 128>(a, stream) : launch<T, M, 256>(a, stream);
 }
 
 template <typename T>
-cudaError_t launch_grad(DistillArgs a, cudaStream_t stream) {
-    constexpr int NT = 256, U = 4;
-    a.segments = (a.vocab + 8 * NT * U - 1) / (8 * NT * U);
-    const int64_t grid = a.n * a.segments;
-    return same_phase<T>(a)
-               ? launch_vocab(distill_grad_kernel<T, true, NT, U>, grid, NT, 0, 1, a, stream)
-               : launch_vocab(distill_grad_kernel<T, false, NT, U>, grid, NT, 0, 1, a, stream);
+cudaError_t launch_loss(const DistillArgs& a, cudaStream_t stream) {
+    return a.dx ? launch<T, Make::kBoth>(a, stream) : launch<T, Make::kLoss>(a, stream);
 }
 
 }  // namespace
@@ -334,7 +637,8 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_distill_grad(const DistillArgs& a, cudaStream_t stream) {
-    return a.dtype == ZERO3_F32 ? launch_grad<float>(a, stream) : launch_grad<uint16_t>(a, stream);
+    return a.dtype == ZERO3_F32 ? launch<float, Make::kGrad>(a, stream)
+                                : launch<uint16_t, Make::kGrad>(a, stream);
 }
 
 }  // namespace z3

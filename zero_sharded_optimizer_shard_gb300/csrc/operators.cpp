@@ -221,7 +221,7 @@ z3::DistillArgs distill_args(const void* logits, zero3_dtype dtype, int64_t n, i
     a.teacher_dtype = teacher_dtype;
     a.id64 = id_type == ZERO3_I64;
     a.cluster = 1;
-    a.segments = 1;
+    a.map_bytes = 0;
     return a;
 }
 

@@ -73,8 +73,8 @@ struct DistillArgs {
     int32_t vocab, k;
     float scale;
     int32_t dtype, teacher_dtype, id64;
-    int32_t cluster;       // forward: blocks per row (set by the launch)
-    int32_t segments;      // backward: blocks per row (set by the launch)
+    int32_t cluster;       // blocks per row (set by the launch)
+    int32_t map_bytes;     // of the map of listed tokens (set by the launch)
 };
 
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
