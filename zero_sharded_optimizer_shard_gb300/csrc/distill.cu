@@ -9,7 +9,7 @@
 // the teacher's list meanwhile: a list costs several dependent loads (token,
 // then the student's logit there) and a softmax of its own.  The gradient's
 // elements at the teacher's tokens are written by the list's warp, after the
-// streaming threads have announced that theirs are; those do not wait.
+// streaming threads' stores.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -193,7 +193,7 @@ __device__ __forceinline__ bool list_repeats(const DistillArgs& a, const Teacher
 // probabilities in list order (fixed, 32 entries at a time); the others' id
 // turns -1.  A hash table over the map's memory finds the entry of a token.
 // Slow (a chain of atomics): only where tokens repeat.
-__device__ __noinline__ void list_merge(int count, const Teacher t) {
+__device__ __forceinline__ void list_merge(int count, const Teacher& t) {
     const int lane = threadIdx.x & 31;
     const uint32_t slots = Teacher::table(count), mask = slots - 1u;
     int32_t* const key = reinterpret_cast<int32_t*>(t.map);  // tokens, and after them
@@ -261,15 +261,6 @@ __device__ __forceinline__ void sweep_chunk(const Chunk<T>& c, T* out, const Swe
     }
     Chunk<T>::store(out, f);
 }
-// The element of a part outside its whole chunks ([lo, first) and [last, hi),
-// at most seven each) that this thread has, or -1.
-__device__ __forceinline__ int32_t edge_element(int32_t lo, int32_t first, int32_t last, int32_t hi) {
-    const int tid = static_cast<int>(threadIdx.x);
-    if (tid < 8) return lo + tid < first ? lo + tid : -1;
-    if (tid < 16) return last + tid - 8 < hi ? last + tid - 8 : -1;
-    return -1;
-}
-
 // Writes the gradient at the teacher's tokens in [lo, hi): `threads` threads
 // from `tid` on.
 template <typename T>
@@ -289,23 +280,17 @@ __device__ __forceinline__ float row_coef(const DistillArgs& a, int64_t r) {
 
 // ---------------------------------------------------------------------- loss
 // The row's statistics, joined over the block's W warps and a cluster's C
-// blocks.  `sh` has been filled and a barrier passed; every thread calls.
+// blocks, which have arrived when they started.  `sh` has been filled and a
+// barrier passed; every thread calls.
 template <int W>
-__device__ __forceinline__ Soft soft_all(const Soft* sh, Soft* sh_part, int C) {
+__device__ __forceinline__ Soft soft_all(const Soft* sh, Soft* parts, int C, int part) {
     Soft q = sh[(threadIdx.x & 31) % W];
     soft_lanes<false, W>(q);
     if (C == 1) return q;
-    if (threadIdx.x == 0) *sh_part = q;
+    cluster_wait();  // every block has started
+    if (threadIdx.x < static_cast<unsigned>(C)) send_cluster(parts + part, threadIdx.x, q);
     cluster_sync();
-    Soft o = soft_empty();
-    const uint32_t lane = threadIdx.x & 31;
-    if (lane < static_cast<uint32_t>(C)) {
-        o.mz = __uint_as_float(ld_cluster(&sh_part->mz, lane));
-        o.s = __uint_as_float(ld_cluster(&sh_part->s, lane));
-    }
-    soft_lanes<false, 32>(o);
-    cluster_sync();  // every part's statistics have been read
-    return o;
+    return soft_parts<false>(parts, C);
 }
 
 __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t r, const Soft& q,
@@ -353,16 +338,16 @@ struct RowPart {
 template <typename T, Make M, int NT>
 __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant__ DistillArgs a) {
     constexpr bool LOSS = M == Make::kBoth;
-    constexpr int P = sizeof(T) / 2;  // 16-byte parts per chunk
-    constexpr int U = 4 / P;          // chunks per batch; two batches fill the ring
+    constexpr int U = RowRing<T, NT>::U;
     extern __shared__ uint4 dyn[];
     __shared__ Soft sh[NT / 32];
-    __shared__ Soft sh_part;
+    __shared__ Soft sh_parts[kMaxCluster];
     __shared__ ListKind sh_kind;
     wait_prior_grids();
     allow_next_grid();
     const int tid = threadIdx.x;
     const int C = a.cluster;
+    if (LOSS && C > 1) cluster_arrive();
     const int64_t r = blockIdx.x / C;
     const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const RowPart<T> p(a, r, part);
@@ -372,7 +357,7 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
     w.scale = a.scale;
     if (tid >= NT) {  // the list's warp
         const int lane = tid - NT;
-        const Teacher t(dyn + 2 * U * P * NT, a);
+        const Teacher t(dyn + RowRing<T, NT>::kBytes / 16, a);
         // the loss wants the logits at all tokens, from its first part
         const bool all = LOSS && part == 0;
         const ListKind kind = list_entries(a, r, t);
@@ -387,7 +372,7 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
         if (LOSS) __syncthreads();
         Soft q = soft_empty();
         if (LOSS) {
-            q = soft_all<NT / 32>(sh, &sh_part, C);
+            q = soft_all<NT / 32>(sh, sh_parts, C, part);
             if (part == 0 && lane == 0) write_loss(a, r, q, l, kind, q.s == 0.0f ? 0.0f : logf(q.s));
         }
         const float lse = LOSS ? 0.0f : a.lse[r];
@@ -396,87 +381,25 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
         w.c = row_coef(a, r);
         w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
         if (kind == kListNan) w.coef = __int_as_float(0x7fffffff);
-        asm volatile("barrier.sync 1, %0;" ::"n"(NT + 32) : "memory");  // the others have written
+        __syncthreads();  // the others have written
         write_teacher<T>(a, t, out, p.lo, p.hi, w, lane, 32);
         return;
     }
-    // batches of U chunks per thread, B of them per pass
-    uint4* const ring = dyn + tid;  // batch b, chunk u, part h: [((b & 1) * U + u) * P + h) * NT]
-    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    const int full = p.n / (U * NT);                      // batches without a gap
-    const int B = (p.n + U * NT - 1) / (U * NT);
-    const int all = LOSS ? 2 * B : B;
-    const T* const first = p.row + p.start + 8 * tid;
-    // L2 keeps a row from the first pass for the second one
-    uint64_t keep, drop;
-    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
-    const auto issue = [&](int b) {
-        if (b < all) {
-            const int c = (LOSS && b >= B ? b - B : b) * U * NT;  // chunks before the batch
-            const T* from = first + 8 * static_cast<int64_t>(c);
-            const uint32_t to = ring_at + static_cast<uint32_t>((b & 1) * (16 * U * P * NT));
-            const bool gaps = c + U * NT > p.n;
-            const uint64_t policy = b < B ? keep : drop;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (!gaps || c + u * NT + tid < p.n) {
-#pragma unroll
-                    for (int h = 0; h < P; ++h)
-                        if (LOSS)
-                            asm volatile(
-                                "cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
-                                    to + 16 * NT * (u * P + h)),
-                                "l"(from + 8 * NT * u + h * (8 / P)), "l"(policy)
-                                : "memory");
-                        else
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                             to + 16 * NT * (u * P + h)),
-                                         "l"(from + 8 * NT * u + h * (8 / P))
-                                         : "memory");
-                }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    // takes batch b out of the ring and sends batch b + 2 after it
-    const auto take = [&](int b, Chunk<T> (&c)[U]) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        const uint4* from = ring + (b & 1) * (U * P * NT);
-#pragma unroll
-        for (int u = 0; u < U; ++u) c[u].from_parts(from + u * P * NT, NT);
-        issue(b + 2);
-    };
-    issue(0);
-    issue(1);
+    const RowRing<T, NT> ring(dyn, p.row + p.start, p.n, tid, LOSS ? 2 : 1);
+    ring.send(0);
+    ring.send(1);
     const int32_t edge = edge_element(p.lo, p.start, last, p.hi);
-    const float edge_x = edge >= 0 ? to_f32(p.row[edge]) : 0.0f;
+    T edge_x = from_f32<T>(0.0f);
+    if (edge >= 0) edge_x = p.row[edge];
     Soft q = soft_empty();
     if (LOSS) {
-        if (edge >= 0) {
-            Chunk<T> c[1];
-            c[0].fill(neg_inf());
-            c[0].set(0, p.row[edge]);
-            soft_add<T, false, 1>(q, c, a.scale);
-        }
-#pragma unroll 1
-        for (int b = 0; b < full; ++b) {
-            Chunk<T> c[U];
-            take(b, c);
-            soft_add<T, false, U>(q, c, a.scale);
-        }
-        if (full < B) {
-            Chunk<T> c[U];
-            take(full, c);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((full * U + u) * NT + tid < p.n)
-                    soft_add<T, false, 1>(q, reinterpret_cast<Chunk<T>(&)[1]>(c[u]), a.scale);
-        }
+        if (edge >= 0) soft_element<T, false>(q, edge_x, a.scale);
+        soft_ring<T, false, NT>(q, ring, a.scale);
         soft_lanes<false, 32>(q);
         if ((tid & 31) == 0) sh[tid >> 5] = q;
     }
     __syncthreads();
-    if (LOSS) q = soft_all<NT / 32>(sh, &sh_part, C);
+    if (LOSS) q = soft_all<NT / 32>(sh, sh_parts, C, part);
     const float lse = LOSS ? 0.0f : a.lse[r];
     const ListKind kind = sh_kind;
     const bool dead = kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf());
@@ -487,29 +410,31 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
     T* to = out + p.start + 8 * tid;
     if (dead) {
         const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        drain_copies();
         for (int32_t c = tid; c < p.n; c += NT, to += 8 * NT) Chunk<T>::store(to, zero);
         if (edge >= 0) out[edge] = from_f32<T>(0.0f);
         return;
     }
+    const int b0 = LOSS ? ring.per : 0;
 #pragma unroll 1
-    for (int b = 0; b < full; ++b, to += 8 * U * NT) {
+    for (int b = 0; b < ring.full; ++b, to += 8 * U * NT) {
         Chunk<T> c[U];
-        take(LOSS ? B + b : b, c);
+        ring.take(b0 + b, c);
+        ring.send(b0 + b + 2);
 #pragma unroll
         for (int u = 0; u < U; ++u) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
     }
-    if (full < B) {
+    if (ring.full < ring.per) {
         Chunk<T> c[U];
-        take(LOSS ? B + full : full, c);
+        ring.take(b0 + ring.full, c);
+        ring.send(b0 + ring.full + 2);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if ((full * U + u) * NT + tid < p.n) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
+            if (ring.has(u)) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
     }
-    if (edge >= 0) out[edge] = from_f32<T>(sweep_value(edge_x, w));
-    __threadfence_block();
-    asm volatile("barrier.arrive 1, %0;" ::"n"(NT + 32) : "memory");
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (edge >= 0) out[edge] = from_f32<T>(sweep_value(to_f32(edge_x), w));
+    drain_copies();
+    __syncthreads();
 }
 
 // The loss alone, and the gradient of rows that are not as far from a 16-byte
@@ -520,7 +445,7 @@ __global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_con
     constexpr bool GRAD = M != Make::kLoss, LOSS = M != Make::kGrad;
     extern __shared__ uint4 dyn[];
     __shared__ Soft sh[NT / 32];
-    __shared__ Soft sh_part;
+    __shared__ Soft sh_parts[kMaxCluster];
     __shared__ ListSums sh_list;
     __shared__ ListKind sh_kind;
     wait_prior_grids();
@@ -528,6 +453,7 @@ __global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_con
     const Teacher t(dyn, a);
     const int tid = threadIdx.x;
     const int C = a.cluster;
+    if (LOSS && C > 1) cluster_arrive();
     const int64_t r = blockIdx.x / C;
     const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const RowPart<T> p(a, r, part);
@@ -546,14 +472,15 @@ __global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_con
         }
     } else if (LOSS) {
         Soft q = soft_empty();
-        soft_stream<T, false, NT, U>(q, p.row, cut, c0, c0 + p.n, part == 0, part == C - 1, a.scale);
+        soft_stream<T, false, NT, U>(q, p.row, cut, c0, c0 + p.n, part == 0, part == C - 1, a.scale,
+                                      tid);
         soft_lanes<false, 32>(q);
         if ((tid & 31) == 0) sh[tid >> 5] = q;
     }
     __syncthreads();
     Soft q = soft_empty();
     if (LOSS)
-        q = soft_all<NT / 32>(sh, &sh_part, C);
+        q = soft_all<NT / 32>(sh, sh_parts, C, part);
     else if (C > 1)
         cluster_sync();  // in place, every part's list has read the row
     if (LOSS && part == 0 && tid == 0)
@@ -604,7 +531,7 @@ cudaError_t launch(DistillArgs a, cudaStream_t stream) {
     a.map_bytes = M == Make::kLoss ? 0 : Teacher::bytes_of_map(a.k, 8 * (chunks / a.cluster + 1) + 14);
     const int list = Teacher::entry_bytes(a.k) + a.map_bytes;
     if constexpr (M != Make::kLoss) {
-        constexpr int kRing = 8 * 16 * NT, kMost = 96 * 1024;
+        constexpr int kRing = RowRing<T, NT>::kBytes, kMost = 96 * 1024;
         if (same_phase<T>(a)) {
             if (kRing + list > 46 * 1024) {
                 const cudaError_t e = cudaFuncSetAttribute(

@@ -30,12 +30,12 @@ constexpr int kGroups = 128;     // groups of threads whose maxima bound the k-t
 constexpr int kCandidates = 640; // candidates a block ranks
 
 struct TopShared {
-    uint64_t cand[kCandidates];
-    uint64_t top[ZERO3_MAX_TOP];
-    uint32_t group[kGroups];
+    alignas(16) uint64_t cand[kCandidates];
+    uint64_t list[kMaxCluster * ZERO3_MAX_TOP];  // what a cluster's blocks have sent
+    alignas(16) uint32_t group[kGroups];
     uint16_t thread[512];
     uint32_t bound;
-    int flagged, count, ntop, sum, first;
+    int flagged, count, sum;
 };
 
 // One block's part of a row: elements [lo, hi) of the row, chunks [c0, c1).
@@ -116,9 +116,6 @@ __device__ int count_from(TopShared& sh, const Part<T>& p, uint32_t bound) {
 // equals `key`.
 template <typename T, int NT>
 __device__ void offer_equal(TopShared& sh, const Part<T>& p, uint32_t key, int need) {
-    __syncthreads();
-    if (threadIdx.x == 0) sh.first = 0;
-    __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int have = 0;  // the same in every thread
     for (int32_t base = p.lo; base < p.hi && have < need; base += NT) {
@@ -140,19 +137,20 @@ __device__ void offer_equal(TopShared& sh, const Part<T>& p, uint32_t key, int n
     }
 }
 
-// The part's k best elements, best first, into sh.top (sh.ntop of them:
-// fewer than k only if the part has fewer elements).
+// Finds candidates for the part's k best elements, sh.cand, and returns their
+// number: at least k unless the part has fewer elements.
 //
 // Every thread knows the largest element of its share (best; `any`: it has
 // a share).  The k-th largest of the 128 groups' maxima is a lower bound of
 // the part's k-th largest element, and only the threads whose own maximum
 // reaches it hold candidates: about k to 1.5 k of them, whose shares are
-// read again (from L2) by the whole block.  The candidates are then ranked
-// by counting.  Masses of equal values or shares that hold the top in a
+// read again (from L2) by the whole block.  (Of a binary32 bound only the upper
+// half is found, which admits a few candidates more.)  They are then ranked by
+// counting.  Masses of equal values or shares that hold the top in a
 // regular pattern overflow the candidate list; then the exact k-th value is
 // found bit by bit, and equal ones are taken in index order.
 template <typename T, int NT>
-__device__ void select_top(TopShared& sh, const Part<T>& p, float best, bool any, int k) {
+__device__ int find_top(TopShared& sh, const Part<T>& p, float best, bool any, int k) {
     const int tid = threadIdx.x;
     const uint32_t mine = any ? key_of(best) : 0u;
     uint32_t g = mine;
@@ -161,23 +159,36 @@ __device__ void select_top(TopShared& sh, const Part<T>& p, float best, bool any
     if (tid == 0) sh.flagged = sh.count = 0;
     if (tid % (NT / kGroups) == 0) sh.group[tid / (NT / kGroups)] = g;
     __syncthreads();
-    if (tid < kGroups) {
-        const uint32_t me = sh.group[tid];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < kGroups; j += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(&sh.group[j]);
-            rank += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
-            rank += (o.x == me && j < tid) + (o.y == me && j + 1 < tid) + (o.z == me && j + 2 < tid) +
-                    (o.w == me && j + 3 < tid);
+    // the bound, bit by bit from the top: 16 bits here, the others if it has to
+    // be exact
+    const int lane = tid & 31;
+    uint32_t bound = 0;
+    const auto settle = [&](int from, int to) {  // two bits at a time
+        const uint4 x = *reinterpret_cast<const uint4*>(&sh.group[4 * lane]);
+        for (int b = from - 1; b >= to; b -= 2) {
+            int n[4];
+#pragma unroll
+            for (int t = 1; t < 4; ++t) {
+                const uint32_t c = bound + (static_cast<uint32_t>(t) << b);
+                n[t] = __reduce_add_sync(0xffffffffu,
+                                         (x.x >= c) + (x.y >= c) + (x.z >= c) + (x.w >= c));
+            }
+            bound += static_cast<uint32_t>(n[3] >= k ? 3 : n[2] >= k ? 2 : n[1] >= k ? 1 : 0) << b;
         }
-        if (rank == k - 1) sh.bound = me;
+    };
+    if (tid < 32) {
+        settle(31, 16);
+        if (sizeof(T) == 2 && !(bound >> 31)) bound |= 0xffffu;  // the key of a negative bf16
+        if (tid == 0) sh.bound = bound;
     }
     __syncthreads();
-    uint32_t bound = sh.bound;
-    if (mine >= bound && any) {
-        const int at = atomicAdd(&sh.flagged, 1);
-        sh.thread[at] = static_cast<uint16_t>(tid);
+    bound = sh.bound;
+    const uint32_t reach = __ballot_sync(0xffffffffu, mine >= bound && any);
+    if (reach) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.flagged, __popc(reach));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(reach & ((1u << lane) - 1u));
+        if (reach >> lane & 1u) sh.thread[at] = static_cast<uint16_t>(tid);
     }
     __syncthreads();
     const int flagged = sh.flagged;
@@ -193,6 +204,7 @@ __device__ void select_top(TopShared& sh, const Part<T>& p, float best, bool any
         over = sh.count > kCandidates;
     }
     if (over) {  // block-uniform
+        if (sizeof(T) == 4) settle(15, 0);
         int above = offer_all<T, NT>(sh, p, bound + 1);
         if (above > kCandidates) {
             bound = 0;
@@ -205,29 +217,70 @@ __device__ void select_top(TopShared& sh, const Part<T>& p, float best, bool any
         if (above < k) offer_equal<T, NT>(sh, p, bound, k - above);
         __syncthreads();
     }
-    const int n = min(sh.count, kCandidates);
-    for (int i = tid; i < n; i += NT) {
-        const uint64_t me = sh.cand[i];
+    return min(sh.count, kCandidates);
+}
+
+// put(rank, candidate) for the k best of n candidates: ranked by counting.
+template <int NT, typename Put>
+__device__ __forceinline__ void rank_top(const uint64_t* cand, int n, int k, const Put& put) {
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const uint64_t me = cand[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.cand[j] > me;
-        if (rank < k) sh.top[rank] = me;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank += cand[j] > me;
+        if (rank < k) put(rank, me);
     }
-    if (tid == 0) sh.ntop = n < k ? n : k;
-    __syncthreads();
+}
+
+// The row's outputs but for the alternatives.  q.s > 0, 0 (no element with
+// weight) or NaN; y: the target, whose logit is xy, or -1.
+template <bool ENT>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t r, const Soft& q, float logs,
+                                          int32_t y, float xy) {
+    const bool none = q.s == 0.0f;
+    a.logprob[r] = y < 0 ? 0.0f
+                   : none ? neg_inf()
+                          : __fsub_rn(fmaf(xy, a.scale, -q.mz), logs);
+    if (a.lse) a.lse[r] = none ? neg_inf() : __fadd_rn(q.mz, logs);
+    if (ENT) a.entropy[r] = none ? 0.0f : __fsub_rn(logs, __fdiv_rn(__fmul_rn(q.a, kLn2), q.s));
+}
+
+// One row per warp, for many short rows: nothing is joined across warps.
+template <typename T, int U, bool ENT>
+__global__ void __launch_bounds__(128) logprob_warp_kernel(const __grid_constant__ LogprobArgs a) {
+    wait_prior_grids();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (r >= a.n) return;
+    const T* row = static_cast<const T*>(a.x) + r * a.stride;
+    const RowCut<T> cut(row, a.vocab);
+    int32_t y = -1;
+    float xy = 0.0f;
+    if (lane == 0) {
+        y = load_id(a.targets, a.id64, r, a.vocab);
+        if (y >= 0) xy = to_f32(row[y]);
+    }
+    Soft q = soft_empty();
+    soft_stream<T, ENT, 32, U>(q, row, cut, 0, cut.chunks, true, true, a.scale, lane);
+    soft_lanes<ENT, 32>(q);
+    if (lane == 0) write_row<ENT>(a, r, q, q.s == 0.0f ? 0.0f : logf(q.s), y, xy);
 }
 
 // One row per cluster of a.cluster blocks (one block where rows abound).
 // Bound by HBM: the row is read once, each thread keeping the running
 // maximum, sum and weighted sum of its share in registers.
 template <typename T, int NT, int U, bool ENT, bool TOP>
-__global__ void __launch_bounds__(NT) logprob_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(NT, TOP ? (sizeof(T) == 2 ? 1536 : 1024) / NT : 1)
+    logprob_kernel(const __grid_constant__ LogprobArgs a) {
     __shared__ Soft sh_soft[NT / 32];
-    __shared__ Soft sh_part;
+    __shared__ Soft sh_parts[kMaxCluster];
     __shared__ TopShared sh_top;
     wait_prior_grids();
     allow_next_grid();
     const int tid = threadIdx.x;
     const int C = a.cluster;
+    if (C > 1) cluster_arrive();
     const int64_t r = blockIdx.x / C;
     const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0;
     const T* row = static_cast<const T*>(a.x) + r * a.stride;
@@ -243,81 +296,50 @@ __global__ void __launch_bounds__(NT) logprob_kernel(const __grid_constant__ Log
         if (y >= 0) xy = to_f32(row[y]);
     }
     Soft q = soft_empty();
-    soft_stream<T, ENT, NT, U>(q, row, cut, c0, c1, head, tail, a.scale);
+    soft_stream<T, ENT, NT, U>(q, row, cut, c0, c1, head, tail, a.scale, tid);
     const float best = q.m;
     soft_block<ENT, NT>(q, sh_soft);
-    Part<T> p{row, cut, c0, c1, 0, 0};
-    if (TOP) {
-        p.lo = head ? 0 : cut.head + 8 * c0;
-        p.hi = tail ? a.vocab : cut.head + 8 * c1;
+    int n = 0;  // candidates
+    const uint64_t* cand = sh_top.cand;
+    if (TOP && !isnan(q.s)) {  // the same in every thread
+        const Part<T> p{row, cut, c0, c1, head ? 0 : cut.head + 8 * c0,
+                        tail ? a.vocab : cut.head + 8 * c1};
         const bool any = c0 + tid < c1 || (tid == 0 && head && cut.head) ||
                          (tid == NT - 1 && tail && cut.tail);
-        __syncthreads();
-        if (isnan(q.s)) {  // the same in every thread
-            if (tid == 0) sh_top.ntop = 0;
-        } else {
-            select_top<T, NT>(sh_top, p, best, any, a.k);
-        }
+        n = find_top<T, NT>(sh_top, p, best, any, a.k);
     }
     if (C > 1) {
-        if (tid == 0) sh_part = q;
-        cluster_sync();
-        if (part == 0) {
-            Soft o = soft_empty();
-            const uint32_t lane = tid & 31;
-            if (lane < static_cast<uint32_t>(C)) {
-                o.mz = __uint_as_float(ld_cluster(&sh_part.mz, lane));
-                o.s = __uint_as_float(ld_cluster(&sh_part.s, lane));
-                if (ENT) o.a = __uint_as_float(ld_cluster(&sh_part.a, lane));
-            }
-            soft_lanes<ENT, 32>(o);
-            q = o;
-            if (TOP) {  // the parts' lists, ranked by counting
-                if (tid == 0) sh_top.count = 0;
-                __syncthreads();
-                for (int i = tid; i < C * a.k; i += NT) {
-                    const int from = i / a.k, at = i % a.k;
-                    if (at < static_cast<int>(ld_cluster(&sh_top.ntop, from))) {
-                        const uint32_t* e = reinterpret_cast<const uint32_t*>(&sh_top.top[at]);
-                        const uint32_t lo = ld_cluster(e, from), hi = ld_cluster(e + 1, from);
-                        const int w = atomicAdd(&sh_top.count, 1);
-                        sh_top.cand[w] = (static_cast<uint64_t>(hi) << 32) | lo;
-                    }
-                }
-                __syncthreads();
-                const int n = sh_top.count;
-                for (int i = tid; i < n; i += NT) {
-                    const uint64_t me = sh_top.cand[i];
-                    int rank = 0;
-                    for (int j = 0; j < n; ++j) rank += sh_top.cand[j] > me;
-                    if (rank < a.k) sh_top.top[rank] = me;
-                }
-                __syncthreads();
-            }
+        cluster_wait();  // the first block has started
+        if (tid == 0) send_cluster(&sh_parts[part], 0, q);
+        if (TOP) {  // the best k, or as many as there are and then zeros
+            uint64_t* const to = &sh_top.list[part * a.k];
+            rank_top<NT>(cand, n, a.k, [&](int i, uint64_t c) { send_cluster(to + i, 0, c); });
+            if (tid < a.k && tid >= n) send_cluster(to + tid, 0, 0);
         }
-        cluster_sync();  // the parts' shared memory has been read
+        cluster_sync();
         if (part != 0) return;
+        q = soft_parts<ENT>(sh_parts, C);
+        cand = sh_top.list;
+        n = C * a.k;
     }
-    // q.s > 0, 0 (no element with weight) or NaN
     const bool none = q.s == 0.0f;
     const float logs = none ? 0.0f : logf(q.s);
-    if (tid == 0) {
-        a.logprob[r] = y < 0 ? 0.0f
-                       : none ? neg_inf()
-                              : __fsub_rn(fmaf(xy, a.scale, -q.mz), logs);
-        if (a.lse) a.lse[r] = none ? neg_inf() : __fadd_rn(q.mz, logs);
-        if (ENT) a.entropy[r] = none ? 0.0f : __fsub_rn(logs, __fdiv_rn(__fmul_rn(q.a, kLn2), q.s));
-    }
-    if (TOP) {
-        const bool bad = isnan(q.s);
-        for (int i = tid; i < a.k; i += NT) {
-            const uint64_t c = sh_top.top[i];
-            const float x = value_of(static_cast<uint32_t>(c >> 32));
-            const int64_t o = r * a.k + i;
-            a.top_ids[o] = bad ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
-            a.top_logprobs[o] = none ? neg_inf() : bad ? q.s : __fsub_rn(fmaf(x, a.scale, -q.mz), logs);
+    if (tid == 0) write_row<ENT>(a, r, q, logs, y, xy);
+    if (!TOP) return;
+    int32_t* const ids = a.top_ids + r * a.k;
+    float* const lps = a.top_logprobs + r * a.k;
+    if (isnan(q.s)) {
+        if (tid < a.k) {
+            ids[tid] = -1;
+            lps[tid] = q.s;
         }
+        return;
     }
+    rank_top<NT>(cand, n, a.k, [&](int i, uint64_t c) {
+        ids[i] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(c));
+        const float x = value_of(static_cast<uint32_t>(c >> 32));
+        lps[i] = none ? neg_inf() : __fsub_rn(fmaf(x, a.scale, -q.mz), logs);
+    });
 }
 
 // ---------------------------------------------------------------- gradient
@@ -438,16 +460,23 @@ __global__ void __launch_bounds__(NT)
     }
 }
 
-template <typename T, bool ENT, bool TOP>
-cudaError_t launch_fwd(LogprobArgs a, cudaStream_t stream) {
-    constexpr int NT = 256, U = 4;
+template <typename T, bool ENT, bool TOP, int NT>
+cudaError_t launch_blocks(LogprobArgs a, cudaStream_t stream) {
+    constexpr int U = sizeof(T) == 2 || TOP ? 4 : 2;
     const int64_t chunks = a.vocab / 8;
     int C = 1;
     while (C < 8 && a.n * C < 304 && chunks / (2 * C) >= 2 * NT) C *= 2;
     a.cluster = C;
-    if (chunks <= 512)
-        return launch_vocab(logprob_kernel<T, 128, U, ENT, TOP>, a.n, 128, 0, 1, a, stream);
     return launch_vocab(logprob_kernel<T, NT, U, ENT, TOP>, a.n * C, NT, 0, C, a, stream);
+}
+
+template <typename T, bool ENT, bool TOP>
+cudaError_t launch_fwd(const LogprobArgs& a, cudaStream_t stream) {
+    if (!TOP && a.vocab <= 8192 && a.n >= 608)
+        return launch_vocab(logprob_warp_kernel<T, sizeof(T) == 2 ? 4 : 2, ENT>, (a.n + 3) / 4, 128, 0,
+                            1, a, stream);
+    return a.vocab <= 8192 ? launch_blocks<T, ENT, TOP, 128>(a, stream)
+                           : launch_blocks<T, ENT, TOP, 256>(a, stream);
 }
 
 template <typename T>

@@ -173,7 +173,7 @@ struct RowCut {
 // no difference of two infinities is taken), s = sum 2^t and a = sum t 2^t
 // with t = (z - mz) log2(e).  Products are exact inside the FMA: z is never
 // rounded by itself.  A NaN element is passed over by m and turns s into NaN.
-struct Soft {
+struct alignas(16) Soft {
     float m, mz, s, a;
 };
 
@@ -275,15 +275,14 @@ __device__ __forceinline__ void soft_block(Soft& q, Soft* sh) {
     soft_lanes<ENT, W>(q);
 }
 
-// The thread's share of a row's chunks [c0, c1): chunk c0 + tid, + NT, ...
-// in batches of U loads; the head elements go to thread 0, the tail elements
-// to the block's last thread, when `head` / `tail` say that they are this
-// block's.
+// Thread tid's share, of NT, of a row's chunks [c0, c1): chunk c0 + tid, + NT,
+// ... in batches of U loads; the head elements go to thread 0, the tail
+// elements to the last thread, when `head` / `tail` say that they are the
+// caller's.
 template <typename T, bool ENT, int NT, int U>
 __device__ __forceinline__ void soft_stream(Soft& q, const T* row, const RowCut<T>& cut,
                                             int32_t c0, int32_t c1, bool head, bool tail,
-                                            float scale) {
-    const int tid = threadIdx.x;
+                                            float scale, int tid) {
     if ((tid == 0 && head && cut.head) || (tid == NT - 1 && tail && cut.tail)) {
         Chunk<T> c[1];
         const bool h = tid == 0 && head && cut.head;
@@ -312,22 +311,144 @@ __device__ __forceinline__ void soft_stream(Soft& q, const T* row, const RowCut<
 
 __device__ __forceinline__ Soft soft_empty() { return Soft{neg_inf(), 0.0f, 0.0f, 0.0f}; }
 
+// Chunks of a row on their way to a thread: its share (chunk tid, + NT, ... of
+// n from `first` on), once or twice over, in batches of U through a ring of two
+// batches in shared memory, filled by asynchronous 16-byte copies.  A thread
+// reads what it copied itself, so no barrier orders them; bytes in flight cost
+// no registers.
+template <typename T, int NT>
+struct RowRing {
+    static constexpr int P = sizeof(T) / 2;  // 16-byte parts per chunk
+    static constexpr int U = 4 / P;          // chunks per batch
+    static constexpr int kBytes = 8 * 16 * NT;
+    const uint4* ring;
+    uint32_t at;
+    const T* mine;
+    int tid, n, full, per, all;  // full: batches without a gap; per pass, in all
+    __device__ __forceinline__ RowRing(uint4* mem, const T* first, int n_, int tid_, int passes)
+        : ring(mem + tid_),
+          at(static_cast<uint32_t>(__cvta_generic_to_shared(mem + tid_))),
+          mine(first + 8 * tid_),
+          tid(tid_),
+          n(n_),
+          full(n_ / (U * NT)),
+          per((n_ + U * NT - 1) / (U * NT)),
+          all(passes * per) {}
+    // Sends batch b.
+    __device__ __forceinline__ void send(int b) const {
+        if (b < all) {
+            const int c = (b >= per ? b - per : b) * U * NT;  // chunks before the batch
+            const T* from = mine + 8 * static_cast<int64_t>(c);
+            const uint32_t to = at + static_cast<uint32_t>((b & 1) * (16 * U * P * NT));
+            const bool gaps = c + U * NT > n;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (!gaps || c + u * NT + tid < n) {
+#pragma unroll
+                    for (int h = 0; h < P; ++h)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         to + 16 * NT * (u * P + h)),
+                                     "l"(from + 8 * NT * u + h * (8 / P))
+                                     : "memory");
+                }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Takes batch b, of two that have been sent, out of the ring.
+    __device__ __forceinline__ void take(int b, Chunk<T> (&c)[U]) const {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const uint4* from = ring + (b & 1) * (U * P * NT);
+#pragma unroll
+        for (int u = 0; u < U; ++u) c[u].from_parts(from + u * P * NT, NT);
+    }
+    // Whether the thread has chunk u of a batch that has gaps (batch `full` of
+    // its pass).
+    __device__ __forceinline__ bool has(int u) const { return (full * U + u) * NT + tid < n; }
+};
+__device__ __forceinline__ void drain_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Adds the first pass of a ring, two batches of which have been sent.
+template <typename T, bool ENT, int NT>
+__device__ __forceinline__ void soft_ring(Soft& q, const RowRing<T, NT>& g, float scale) {
+    constexpr int U = RowRing<T, NT>::U;
+#pragma unroll 1
+    for (int b = 0; b < g.full; ++b) {
+        Chunk<T> c[U];
+        g.take(b, c);
+        g.send(b + 2);
+        soft_add<T, ENT, U>(q, c, scale);
+    }
+    if (g.full < g.per) {
+        Chunk<T> c[U];
+        g.take(g.full, c);
+        g.send(g.full + 2);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (g.has(u)) soft_add<T, ENT, 1>(q, reinterpret_cast<Chunk<T>(&)[1]>(c[u]), scale);
+    }
+}
+
+// The element of a row's part outside its whole chunks ([lo, first) and
+// [last, hi), at most seven each) that this thread has, or -1.
+__device__ __forceinline__ int32_t edge_element(int32_t lo, int32_t first, int32_t last, int32_t hi) {
+    const int tid = static_cast<int>(threadIdx.x);
+    if (tid < 8) return lo + tid < first ? lo + tid : -1;
+    if (tid < 16) return last + tid - 8 < hi ? last + tid - 8 : -1;
+    return -1;
+}
+template <typename T, bool ENT>
+__device__ __forceinline__ void soft_element(Soft& q, T x, float scale) {
+    Chunk<T> c[1];
+    c[0].fill(neg_inf());
+    c[0].set(0, x);
+    soft_add<T, ENT, 1>(q, c, scale);
+}
+
 // ----------------------------------------------------------------- clusters
+// A cluster's blocks send their results to one another's shared memory: all
+// arrive when they start (whoever has waited for that may write to the others),
+// and once more when they have sent.  Not the .aligned forms, which are
+// undefined in a warp whose lanes have not met again after a branch.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// Reads 4 bytes at shared address p of block `rank` of the cluster.
-__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
+// Writes to the shared variable at `p` of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
     const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    uint32_t r, v;
+    uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
-    return v;
+    return r;
+}
+__device__ __forceinline__ void send_cluster(uint64_t* p, uint32_t rank, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_address(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void send_cluster(Soft* p, uint32_t rank, const Soft& v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_address(p, rank)),
+                 "f"(v.m), "f"(v.mz), "f"(v.s), "f"(v.a)
+                 : "memory");
+}
+constexpr int kMaxCluster = 8;
+
+// The statistics that C blocks have sent to `parts`, joined (every lane).
+template <bool ENT>
+__device__ __forceinline__ Soft soft_parts(const Soft* parts, int C) {
+    Soft o = soft_empty();
+    const int i = threadIdx.x % kMaxCluster;
+    if (i < C) o = parts[i];
+    soft_lanes<ENT, kMaxCluster>(o);
+    return o;
 }
 
 // Launch with programmatic stream serialization (see wait_prior_grids), with
