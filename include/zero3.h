@@ -561,7 +561,7 @@ zero3_status zero3_embedding_forward(const void* table, zero3_dtype table_dtype,
                                      zero3_stream stream);
 
 /* Bytes of device workspace that zero3_embedding_backward needs (about
- * 4 * vocab + 16 * n + (n / 32 + 1) * 8 * dim). */
+ * 4 * vocab + 16 * n + (n / 16 + 1) * 8 * dim). */
 zero3_status zero3_embedding_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes);
 
 /* Gradient of the lookup with respect to the table:

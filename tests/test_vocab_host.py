@@ -110,7 +110,7 @@ def test_workspace(z):
     for n, V, d in [(0, 1, 1), (1, 50257, 2048), (32768, 50257, 2048), (5, 3, 7)]:
         b = z.zero3_embedding_workspace(n, V, d)
         assert 4 * (V + 1) + 4 * n <= b
-        assert b <= 4 * (V + 600) + 16 * n + (n // 32 + 1) * (8 * (d + 3) + 4 * (d // 256 + 1)) + 80
+        assert b <= 4 * (V + 600) + 16 * n + (n // 16 + 1) * (8 * (d + 3) + 4 * (d // 256 + 1)) + 80
     out = C.c_int64()
     for bad in [(-1, 5, 5), (1, 0, 5), (1, 5, 0), (1 << 31, 5, 5), (1, 5, 1 << 42)]:
         assert z.raw_status("zero3_embedding_workspace", *bad, C.byref(out)) == z.EINVAL

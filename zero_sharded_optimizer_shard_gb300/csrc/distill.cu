@@ -518,7 +518,7 @@ bool same_phase(const DistillArgs& a) {
 // Blocks per row: more than one where rows are few and long.
 int row_blocks(int64_t n, int64_t chunks, int threads) {
     int C = 1;
-    while (C < 8 && n * C < 304 && chunks / (2 * C) >= 2 * threads) C *= 2;
+    while (C < 8 && n * C < 152 && chunks / (2 * C) >= 2 * threads) C *= 2;
     return C;
 }
 

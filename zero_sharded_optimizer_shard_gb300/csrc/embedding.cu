@@ -74,9 +74,9 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
 // ascending order, of dout[i]), in two launches: a stable counting sort of
 // the positions by token, and the rows' sums.  Sums are binary32 and their
 // order depends on the tokens alone, so the result does not depend on timing.
-constexpr int kOwn = 448;          // tokens a sorting block owns at most
-constexpr int kWarpRows = 8;       // sorted positions whose pieces a summing warp takes
-constexpr int kPiece = 32;         // shortest piece of a token that has several
+constexpr int kOwn = 512;          // tokens a sorting block owns at most
+constexpr int kList = 512;         // own positions a sorting warp lists
+constexpr int kPiece = 16;         // shortest piece of a token that has several
 constexpr int kSumThreads = 128;
 constexpr int kRing = 8192;        // bytes of rows in flight per summing warp
 constexpr int kSumWarps = kSumThreads / 32;
@@ -157,14 +157,20 @@ struct SortArgs {
 // that fills the batch) is read from the ids again.  Latency-bound: all that
 // counts is that a warp's loads are in flight together and that little is done
 // per id that is not the block's.
+template <int W>
+struct SortShared {
+    int32_t cnt[W][kOwn];
+    uint32_t list[W][kList];  // token, position from the warp's first on
+    int32_t first[kOwn], count[kOwn];
+    int32_t sh[W], scan[W];
+};
 template <int W, int J>
 __global__ void __launch_bounds__(32 * W) embed_sort_kernel(const __grid_constant__ SortArgs a) {
     constexpr int NT = 32 * W;
-    constexpr int kList = 192;
-    __shared__ int32_t cnt[W][kOwn];
-    __shared__ uint32_t list[W][kList];  // token, position from i0 on
-    __shared__ int32_t first[kOwn], count[kOwn];
-    __shared__ int32_t sh[W], sh_scan[W];
+    extern __shared__ uint4 dyn[];
+    SortShared<W>& s = *reinterpret_cast<SortShared<W>*>(dyn);
+    auto& cnt = s.cnt;
+    auto& list = s.list;
     wait_prior_grids();
     allow_next_grid();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(32 * W) embed_sort_kernel(const __grid_constan
         }
     }
     for (int o = 16; o > 0; o >>= 1) less += __shfl_xor_sync(0xffffffffu, less, o);
-    if (lane == 0) sh[warp] = less;
+    if (lane == 0) s.sh[warp] = less;
     __syncthreads();
     // exclusive scan over the own tokens' totals, kPer tokens per thread
     constexpr int kPer = (kOwn + NT - 1) / NT;
@@ -238,13 +244,13 @@ __global__ void __launch_bounds__(32 * W) embed_sort_kernel(const __grid_constan
         const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) sh_scan[warp] = incl;
+    if (lane == 31) s.scan[warp] = incl;
     __syncthreads();
     int32_t run = incl - sum;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        run += sh[w];
-        if (w < warp) run += sh_scan[w];
+        run += s.sh[w];
+        if (w < warp) run += s.scan[w];
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -252,8 +258,8 @@ __global__ void __launch_bounds__(32 * W) embed_sort_kernel(const __grid_constan
         if (k >= own) break;
         a.w.off[me * own + k] = run;
         if (me == mask && k == own - 1) a.w.off[(mask + 1) * own] = run + total[j];
-        first[k] = run;
-        count[k] = total[j];
+        s.first[k] = run;
+        s.count[k] = total[j];
         if (total[j] == 0) continue;
         for (int w = 0; w < W; ++w) {
             const int32_t c = cnt[w][k];
@@ -271,8 +277,8 @@ __global__ void __launch_bounds__(32 * W) embed_sort_kernel(const __grid_constan
             Sorted x;
             x.pos = i;
             x.token = (k << a.deal.shift) | me;
-            x.first = first[k];
-            x.count = count[k];
+            x.first = s.first[k];
+            x.count = s.count[k];
             *reinterpret_cast<int4*>(a.w.sorted + cnt[warp][k] + rank) =
                 *reinterpret_cast<const int4*>(&x);
         }
@@ -308,6 +314,7 @@ struct SumArgs {
     EmbedGradArgs a;
     Workspace w;
     Deal deal;
+    int32_t rows;   // sorted positions whose pieces a summing warp takes: 8 or 16
     int32_t slabs;
     int64_t sum_blocks;
 };
@@ -392,7 +399,7 @@ __device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t v0, int lan
     }
 }
 
-// Positions of a piece: a token with up to 1024 positions is cut every 32,
+// Positions of a piece: a token with up to 512 positions is cut every 16,
 // longer ones so that neither a piece nor the number of pieces gets long.
 __device__ __forceinline__ int32_t piece_rows(int32_t count) {
     return count <= 32 * kPiece ? kPiece
@@ -419,7 +426,7 @@ __device__ __forceinline__ void join(const SumArgs& p, int32_t v, int32_t first,
         Group<TG, VEC> old;
         if (ACC) old.load(g, at, dim);
         uint64_t acc[4] = {0, 0, 0, 0};
-        constexpr int R = 4;
+        constexpr int R = 8;
         for (int32_t b = 0; b < count; b += R * step) {
             Group<float, VEC> x[R];
 #pragma unroll
@@ -438,7 +445,7 @@ __device__ __forceinline__ void join(const SumArgs& p, int32_t v, int32_t first,
     }
 }
 
-// The pieces that a warp sums: those that start among kWarpRows consecutive
+// The pieces that a warp sums: those that start among `rows` consecutive
 // sorted positions, which together are consecutive rows [a, e) of the sorted
 // order (counted from j0).  Lane l knows position j0 + l.
 struct Pieces {
@@ -446,16 +453,16 @@ struct Pieces {
     uint32_t starts;
     int32_t j0, a, e, count;
     __device__ __forceinline__ bool last(int l) const {  // of its piece
-        return l == e - 1 || (l < kWarpRows - 1 && (starts >> (l + 1) & 1u));
+        return l == e - 1 || (l < 31 && (starts >> (l + 1) & 1u));
     }
     __device__ __forceinline__ int piece_of(int l) const {  // where row l's piece starts
-        return 31 - __clz(l >= kWarpRows ? starts : starts & ((2u << l) - 1u));
+        return 31 - __clz(l >= 31 ? starts : starts & ((2u << l) - 1u));
     }
 };
 
 // False if no piece starts there.
 __device__ __forceinline__ bool find_pieces(const SumArgs& p, int64_t tile, int lane, Pieces& q) {
-    const int64_t j = tile * kWarpRows;
+    const int64_t j = tile * p.rows;
     if (j >= p.a.n) return false;
     q.j0 = static_cast<int32_t>(j);
     q.x = Sorted{0, -1, 0, 0};
@@ -463,7 +470,7 @@ __device__ __forceinline__ bool find_pieces(const SumArgs& p, int64_t tile, int 
         *reinterpret_cast<int4*>(&q.x) = *reinterpret_cast<const int4*>(p.w.sorted + j + lane);
     q.count = p.w.off[p.deal.own << p.deal.shift];  // ignored positions are not sorted
     const int32_t size = piece_rows(q.x.count), at = q.j0 + lane;
-    q.starts = __ballot_sync(0xffffffffu, lane < kWarpRows && at < q.count &&
+    q.starts = __ballot_sync(0xffffffffu, lane < p.rows && at < q.count &&
                                               ((at - q.x.first) & (size - 1)) == 0);
     if (!q.starts) return false;
     q.a = __ffs(q.starts) - 1;
@@ -529,7 +536,7 @@ __device__ __forceinline__ void join_pieces(const SumArgs& p, const Pieces& q, u
 
 // The sums.  The sorted positions are cut into pieces (all of a token's
 // positions, or piece_rows of them), and a warp takes the pieces that start
-// among kWarpRows consecutive positions, for CU groups of columns: the work
+// among `rows` consecutive positions, for CU groups of columns: the work
 // is even however often a token occurs.  Pieces of one token are added up in
 // order by whichever warp of the token comes last.  Bound by HBM once there
 // are some thousand positions: each row is read once.
@@ -715,7 +722,8 @@ cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t 
     p.w = w;
     p.deal = deal_of(a.vocab);
     p.slabs = static_cast<int32_t>((a.dim + kGroupCols * CU - 1) / (kGroupCols * CU));
-    p.sum_blocks = ((a.n + kWarpRows - 1) / kWarpRows * p.slabs + kSumWarps - 1) / kSumWarps;
+    p.rows = a.n > 32768 ? 16 : 8;
+    p.sum_blocks = ((a.n + p.rows - 1) / p.rows * p.slabs + kSumWarps - 1) / kSumWarps;
     const int64_t each = kSumWarps * kZeroTokens;
     const int64_t grid = p.sum_blocks + (ACC ? 0 : (a.vocab + each - 1) / each);
     if constexpr (VEC)
@@ -743,6 +751,17 @@ cudaError_t sum_vec(const EmbedGradArgs& a, const Workspace& w, cudaStream_t str
                : sum_typed<TD, TG, false, false>(a, w, stream);
 }
 
+template <int W, int J>
+cudaError_t sort_launch(const SortArgs& s, int64_t grid, cudaStream_t stream) {
+    constexpr int bytes = sizeof(SortShared<W>);
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel<W, J>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_vocab(embed_sort_kernel<W, J>, grid, 32 * W, bytes, 1, s, stream);
+}
+
 }  // namespace
 
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
@@ -766,9 +785,13 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t stream) {
     s.id64 = a.id64;
     s.deal = deal_of(a.vocab);
     const int64_t grid = int64_t{1} << s.deal.shift;
-    const cudaError_t e =
-        a.n <= 1024 ? launch_vocab(embed_sort_kernel<8, 4>, grid, 256, 0, 1, s, stream)
-                    : launch_vocab(embed_sort_kernel<16, 16>, grid, 512, 0, 1, s, stream);
+    cudaError_t e;
+    if (a.n <= 1024)
+        e = sort_launch<8, 4>(s, grid, stream);
+    else if (a.n <= 4096)
+        e = sort_launch<16, 8>(s, grid, stream);
+    else
+        e = sort_launch<32, 8>(s, grid, stream);
     if (e != cudaSuccess) return e;
     if (a.dout_dtype == ZERO3_F32)
         return a.grad_dtype == ZERO3_F32 ? sum_vec<float, float>(a, s.w, stream)

@@ -465,7 +465,7 @@ cudaError_t launch_blocks(LogprobArgs a, cudaStream_t stream) {
     constexpr int U = sizeof(T) == 2 || TOP ? 4 : 2;
     const int64_t chunks = a.vocab / 8;
     int C = 1;
-    while (C < 8 && a.n * C < 304 && chunks / (2 * C) >= 2 * NT) C *= 2;
+    while (C < 8 && a.n * C < 152 && chunks / (2 * C) >= 2 * NT) C *= 2;
     a.cluster = C;
     return launch_vocab(logprob_kernel<T, NT, U, ENT, TOP>, a.n * C, NT, 0, C, a, stream);
 }
