@@ -548,8 +548,14 @@ cudaError_t launch(DistillArgs a, cudaStream_t stream) {
 
 template <typename T, Make M>
 cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
-    // short rows: more and smaller blocks
-    return a.vocab <= 8192 ? launch<T, M, 128>(a, stream) : launch<T, M, 256>(a, stream);
+    // Short rows: more and smaller blocks, to hide a row's chain of latencies
+    // (list, join, second pass) behind other rows; long rows: fewer rows at a
+    // time, whose second pass then finds them in L2.  Rows of bf16, loss with
+    // gradient, at 64 / 128 / 256 threads: 8192 of 4000 36 / 43 / - us, 8192 of 8000
+    // 59 / 64 / -, 4096 of 16000 - / 56 / 64, 4096 of 32000 - / 115 / 95.
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T));
+    if (bytes <= 16 * 1024) return launch<T, M, 64>(a, stream);
+    return bytes <= 40 * 1024 ? launch<T, M, 128>(a, stream) : launch<T, M, 256>(a, stream);
 }
 
 template <typename T>
