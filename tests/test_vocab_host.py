@@ -112,6 +112,7 @@ def test_workspace(z):
         assert 4 * (V + 1) + 4 * n <= b
         assert b <= 4 * (V + 600) + 16 * n + (n // 16 + 1) * (8 * (d + 3) + 4 * (d // 256 + 1)) + 80
     out = C.c_int64()
-    for bad in [(-1, 5, 5), (1, 0, 5), (1, 5, 0), (1 << 31, 5, 5), (1, 5, 1 << 42)]:
+    for bad in [(-1, 5, 5), (1, 0, 5), (1, 5, 0), (1 << 31, 5, 5), (1, 5, 1 << 42),
+                (1, 1, (1 << 27) + 1)]:
         assert z.raw_status("zero3_embedding_workspace", *bad, C.byref(out)) == z.EINVAL
     assert z.raw_status("zero3_embedding_workspace", 1, 1, 1, None) == z.EINVAL

@@ -8,6 +8,7 @@ namespace {
 
 constexpr int64_t kMaxVocab = int64_t{1} << 30;   // token ids and row offsets are 32-bit
 constexpr int64_t kMaxRows = int64_t{1} << 27;    // rows times blocks per row fit a grid
+constexpr int64_t kMaxDim = int64_t{1} << 27;     // embedding columns are 32-bit
 constexpr int64_t kMaxElems = int64_t{1} << 41;   // rows times columns (4 TB of bf16)
 
 zero3_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ZERO3_OK : ZERO3_ECUDA; }
@@ -38,6 +39,12 @@ bool logits_ok(int64_t n, int64_t vocab, int64_t stride) {
     return n <= kMaxRows && vocab <= kMaxVocab && rows_ok(n, vocab, stride);
 }
 
+// An embedding's two matrices.
+bool embedding_ok(int64_t vocab, int64_t dim, int64_t table_stride, int64_t n, int64_t row_stride) {
+    return vocab >= 1 && vocab <= kMaxVocab && dim <= kMaxDim && rows_ok(vocab, dim, table_stride) &&
+           rows_ok(n, dim, row_stride);
+}
+
 // Blocks of the elementwise gradients: one per 8192 elements of a row.
 bool grid_ok(int64_t n, int64_t vocab) { return n * ((vocab + 8191) / 8192) <= INT32_MAX; }
 
@@ -51,8 +58,7 @@ zero3_status zero3_embedding_forward(const void* table, zero3_dtype table_dtype,
                                      zero3_dtype out_dtype, int64_t out_stride,
                                      zero3_stream stream) {
     if (!dtype_ok(table_dtype) || !dtype_ok(out_dtype) || !itype_ok(id_type)) return ZERO3_EINVAL;
-    if (vocab < 1 || vocab > kMaxVocab || !rows_ok(vocab, dim, table_stride) ||
-        !rows_ok(n, dim, out_stride) || !std::isfinite(scale))
+    if (!embedding_ok(vocab, dim, table_stride, n, out_stride) || !std::isfinite(scale))
         return ZERO3_EINVAL;
     if (n == 0) return ZERO3_OK;
     if (!ptr_ok(table, size_of(table_dtype)) || !ptr_ok(ids, size_of(id_type)) ||
@@ -75,8 +81,7 @@ zero3_status zero3_embedding_forward(const void* table, zero3_dtype table_dtype,
 }
 
 zero3_status zero3_embedding_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes) {
-    if (!bytes || vocab < 1 || vocab > kMaxVocab || !rows_ok(vocab, dim, dim) || !rows_ok(n, dim, dim))
-        return ZERO3_EINVAL;
+    if (!bytes || !embedding_ok(vocab, dim, dim, n, dim)) return ZERO3_EINVAL;
     *bytes = z3::embed_grad_workspace(n, vocab, dim);
     return ZERO3_OK;
 }
@@ -88,8 +93,7 @@ zero3_status zero3_embedding_backward(const void* dout, zero3_dtype dout_dtype, 
                                       void* workspace, int64_t workspace_bytes,
                                       zero3_stream stream) {
     if (!dtype_ok(dout_dtype) || !dtype_ok(grad_dtype) || !itype_ok(id_type)) return ZERO3_EINVAL;
-    if (vocab < 1 || vocab > kMaxVocab || !rows_ok(vocab, dim, grad_stride) ||
-        !rows_ok(n, dim, dout_stride) || !std::isfinite(scale))
+    if (!embedding_ok(vocab, dim, grad_stride, n, dout_stride) || !std::isfinite(scale))
         return ZERO3_EINVAL;
     if (n == 0 && accumulate) return ZERO3_OK;
     if (!ptr_ok(grad, size_of(grad_dtype)) || !ptr_ok(workspace, 16) ||
