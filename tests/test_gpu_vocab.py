@@ -118,6 +118,27 @@ def test_embedding_forward(Z, n, vocab, dim, td, od, kind, pad, off):
         assert out.intact() and table.intact()
 
 
+@pytest.mark.parametrize("off", [0, 1, 2, 3, 5, 7])
+@pytest.mark.parametrize("td,od", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+def test_embedding_forward_any_alignment(Z, td, od, off):
+    """Rows that start anywhere between two 16-byte boundaries, down to tables
+    smaller than the words that a row is read by."""
+    for dim in list(range(1, 19)) + [31, 71]:
+        for vocab, pad in ((1, 0), (3, 0), (40, 5)):
+            n = 9
+            rng = np.random.default_rng(dim)
+            ids = rng.integers(0, vocab, n)
+            ids[4] = vocab
+            table = Mat(rng.normal(size=(vocab, dim)), DT[td], dim + pad, off)
+            out = Mat(np.full((n, dim), 5.0), DT[od], dim + (dim + pad) % 3, (3 * off) % 8)
+            it = ids_tensor(ids, "i64")
+            Z.zero3_embedding_forward(table.ptr, code(Z, td), vocab, dim, table.stride, it.data_ptr(),
+                                      Z.I64, n, 0.75, out.ptr, code(Z, od), out.stride, stream())
+            ref = V.embedding_forward(table.host(), ids, 0.75)
+            close(out.host(), ref, rounding(od, ref) + U * np.abs(ref))
+            assert out.intact() and table.intact()
+
+
 def grad_case(Z, n, vocab, dim, dd, gd, kind, ids, pad=0, off=0, accumulate=False, scale=1.0):
     rng = np.random.default_rng(n + dim + vocab)
     d = Mat(rng.normal(size=(n, dim)), DT[dd], dim + pad, off)

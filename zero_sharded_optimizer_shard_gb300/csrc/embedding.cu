@@ -9,17 +9,56 @@ namespace z3 {
 namespace {
 
 // ------------------------------------------------------------------ lookup
+// Elements 0 .. 7 of `p`, at any alignment, from the two or three aligned
+// 16-byte words that hold them, shifted together.  The words lie in the matrix
+// (whose rows' gaps may be read); the caller has checked it.
+__device__ __forceinline__ void load_shifted(const uint16_t* p, float* f) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint4* w = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
+    const uint32_t off = static_cast<uint32_t>(at & 15u);
+    const uint4 a = w[0], b = w[off ? 1 : 0];
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t y[6], z[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) y[i] = off & 8u ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) z[i] = off & 4u ? y[i + 1] : y[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t v = __funnelshift_r(z[i], z[i + 1], (off & 2u) * 8u);
+        f[2 * i] = bf16_lo(v);
+        f[2 * i + 1] = bf16_hi(v);
+    }
+}
+__device__ __forceinline__ void load_shifted(const float* p, float* f) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const float4* w = reinterpret_cast<const float4*>(at & ~uintptr_t{15});
+    const uint32_t off = static_cast<uint32_t>(at & 15u);
+    const float4 a = w[0], b = w[1], c = w[off ? 2 : 1];
+    const float x[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    float y[9];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) y[i] = off & 8u ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = off & 4u ? y[i + 1] : y[i];
+}
+
 // out[i] = rne(scale * table[ids[i]]), zeros where the id lies outside the
 // vocabulary.  A copy of n random rows: bound by HBM (the row reads, of
-// which repeated tokens hit L2, and the writes).  The n rows' units (chunks of
-// 8 columns, or single columns where rows are not 16-byte aligned) are
-// numbered consecutively; a block takes NT * U of them, a thread U, NT apart,
-// with all of its row loads in flight before its first store.
+// which repeated tokens hit L2, and the writes).  A row's units are 8 columns
+// each; the n rows' units are numbered consecutively, a block takes NT * U of
+// them, a thread U, NT apart, with all of its row loads in flight before its
+// first store.
+//
+// VEC: all rows start on 16-byte boundaries.  Otherwise a row's units are cut at
+// the output row's 16-byte boundaries, one more than dim / 8 rounded up, and the
+// table's elements are shifted into place; a unit that sticks out of its row, or
+// whose words would lie outside the table, goes by single elements.
 template <typename TT, typename TO, bool VEC, int NT, int U>
 __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ EmbedArgs a) {
     wait_prior_grids();
     allow_next_grid();
-    const uint32_t units = static_cast<uint32_t>(VEC ? a.dim / 8 : a.dim);  // per row
+    const uint32_t units = static_cast<uint32_t>(VEC ? a.dim / 8 : a.dim / 8 + 2);  // per row
     const uint64_t b0 = static_cast<uint64_t>(blockIdx.x) * (NT * U);
     const uint64_t row0 = b0 / units;
     const uint32_t rem = static_cast<uint32_t>(b0 - row0 * units) + threadIdx.x;
@@ -37,6 +76,7 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
     }
     const TT* table = static_cast<const TT*>(a.table);
     TO* out = static_cast<TO*>(a.out);
+    const uint64_t sc = pk2(a.scale, a.scale);
     if (VEC) {
         Chunk<TT> c[U];
 #pragma unroll
@@ -44,7 +84,6 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
             c[u].fill(0.0f);
             if (id[u] >= 0) c[u].load(table + id[u] * a.table_stride + 8ll * at[u]);
         }
-        const uint64_t sc = pk2(a.scale, a.scale);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (row[u] >= static_cast<uint64_t>(a.n)) continue;
@@ -57,15 +96,41 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
             Chunk<TO>::store(out + row[u] * a.out_stride + 8ll * at[u], f);
         }
     } else {
-        float x[U];
+        constexpr int P = Chunk<TO>::kPhase;
+        constexpr int64_t W = 16 / sizeof(TT);  // a word's elements
+        const TT* const end = table + (a.vocab - 1) * a.table_stride + a.dim;
+        float f[U][8];
+        int64_t j[U];  // the unit's first column
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            x[u] = id[u] >= 0 ? to_f32(table[id[u] * a.table_stride + at[u]]) : 0.0f;
+        for (int u = 0; u < U; ++u) {
+            const TO* o = out + row[u] * a.out_stride;
+            j[u] = 8ll * at[u] - static_cast<int64_t>((reinterpret_cast<uintptr_t>(o) / sizeof(TO)) % P);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (row[u] < static_cast<uint64_t>(a.n))
-                out[row[u] * a.out_stride + at[u]] =
-                    from_f32<TO>(id[u] >= 0 ? __fmul_rn(x[u], a.scale) : 0.0f);
+            for (int k = 0; k < 8; ++k) f[u][k] = 0.0f;
+            if (id[u] < 0 || j[u] >= a.dim) continue;
+            const TT* p = table + id[u] * a.table_stride + j[u];
+            if (p - table >= W && end - p >= 8 + W) {
+                load_shifted(p, f[u]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (j[u] + k >= 0 && j[u] + k < a.dim) f[u][k] = to_f32(p[k]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] >= static_cast<uint64_t>(a.n)) continue;
+            TO* o = out + row[u] * a.out_stride + j[u];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[u][k] = id[u] >= 0 ? __fmul_rn(f[u][k], a.scale) : 0.0f;
+            if (j[u] >= 0 && j[u] + 8 <= a.dim) {
+                Chunk<TO>::store(o, f[u]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (j[u] + k >= 0 && j[u] + k < a.dim) o[k] = from_f32<TO>(f[u][k]);
+            }
+        }
     }
 }
 
@@ -699,11 +764,13 @@ bool aligned_rows(const void* p, int64_t stride, int32_t dtype) {
 template <typename TT, typename TO, bool VEC>
 cudaError_t embed_typed(const EmbedArgs& a, cudaStream_t stream) {
     constexpr int NT = 256;
-    const int64_t items = a.n * (VEC ? a.dim / 8 : a.dim);
-    // few units: one per thread, so that they spread over the SMs
+    const int64_t items = a.n * (VEC ? a.dim / 8 : a.dim / 8 + 2);
+    // few units: one per thread, so that they spread over the SMs; many: several,
+    // for bytes in flight (8192 x 2047 bf16 at 1 / 2 / 4 shifted units per thread:
+    // 15.7 / 15.1 / 16.7 us; by single elements 40 us)
     if (items <= 152 * NT * 4)
         return launch_vocab(embed_kernel<TT, TO, VEC, NT, 1>, (items + NT - 1) / NT, NT, 0, 1, a, stream);
-    constexpr int U = VEC ? 4 : 8;
+    constexpr int U = VEC ? 4 : 2;
     return launch_vocab(embed_kernel<TT, TO, VEC, NT, U>, (items + NT * U - 1) / (NT * U), NT, 0, 1,
                         a, stream);
 }
