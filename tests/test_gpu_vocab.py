@@ -174,6 +174,18 @@ def zipf(rng, n, vocab):
     return ids
 
 
+@pytest.mark.parametrize("off", [0, 1, 3, 6])
+@pytest.mark.parametrize("dd,gd", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+def test_embedding_backward_any_alignment(Z, dd, gd, off):
+    """Rows that start anywhere between two 16-byte boundaries, next to other
+    rows, gaps and the matrix's ends, with single and repeated tokens."""
+    rng = np.random.default_rng(off)
+    for dim in [1, 2, 3, 5, 7, 9, 15, 17, 63, 71, 255, 257, 263, 521]:
+        for n, vocab, pad in ((1, 1, 0), (5, 3, 0), (90, 40, 0), (90, 4, 5)):
+            grad_case(Z, n, vocab, dim, dd, gd, "i32", rng.integers(-1, vocab, n), pad, off,
+                      (dim + n) % 2 == 0, 0.75)
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("n,vocab,dim,dd,gd,kind,pad,off", [
     (1, 1, 1, "f32", "f32", "i32", 0, 0), (1, 50257, 768, "bf16", "bf16", "i64", 0, 0),

@@ -9,38 +9,76 @@ namespace z3 {
 namespace {
 
 // ------------------------------------------------------------------ lookup
-// Elements 0 .. 7 of `p`, at any alignment, from the two or three aligned
-// 16-byte words that hold them, shifted together.  The words lie in the matrix
-// (whose rows' gaps may be read); the caller has checked it.
-__device__ __forceinline__ void load_shifted(const uint16_t* p, float* f) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const uint4* w = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
-    const uint32_t off = static_cast<uint32_t>(at & 15u);
-    const uint4 a = w[0], b = w[off ? 1 : 0];
-    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t y[6], z[5];
-#pragma unroll
-    for (int i = 0; i < 6; ++i) y[i] = off & 8u ? x[i + 2] : x[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) z[i] = off & 4u ? y[i + 1] : y[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t v = __funnelshift_r(z[i], z[i + 1], (off & 2u) * 8u);
-        f[2 * i] = bf16_lo(v);
-        f[2 * i + 1] = bf16_hi(v);
+// Eight elements at any alignment, by the two or three aligned 16-byte words that
+// hold them, shifted into place.
+template <typename T>
+struct Shifted;
+template <>
+struct Shifted<uint16_t> {
+    uint4 a, b;
+    uint32_t off;
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint4* w = reinterpret_cast<const uint4*>(at & ~uintptr_t{15});
+        off = static_cast<uint32_t>(at & 15u);
+        a = w[0];
+        b = w[off ? 1 : 0];
     }
-}
-__device__ __forceinline__ void load_shifted(const float* p, float* f) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    const float4* w = reinterpret_cast<const float4*>(at & ~uintptr_t{15});
-    const uint32_t off = static_cast<uint32_t>(at & 15u);
-    const float4 a = w[0], b = w[1], c = w[off ? 2 : 1];
-    const float x[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-    float y[9];
+    // chunk `i` of a row that starts at element `skip` of words in shared memory
+    __device__ __forceinline__ void take(const uint4* w, int i, uint32_t skip) {
+        off = 2 * skip;
+        a = w[i];
+        b = w[off ? i + 1 : i];
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t y[6], z[5];
 #pragma unroll
-    for (int i = 0; i < 9; ++i) y[i] = off & 8u ? x[i + 2] : x[i];
+        for (int i = 0; i < 6; ++i) y[i] = off & 8u ? x[i + 2] : x[i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = off & 4u ? y[i + 1] : y[i];
+        for (int i = 0; i < 5; ++i) z[i] = off & 4u ? y[i + 1] : y[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = __funnelshift_r(z[i], z[i + 1], (off & 2u) * 8u);
+            f[2 * i] = bf16_lo(v);
+            f[2 * i + 1] = bf16_hi(v);
+        }
+    }
+};
+template <>
+struct Shifted<float> {
+    float4 a, b, c;
+    uint32_t off;
+    __device__ __forceinline__ void load(const float* p) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const float4* w = reinterpret_cast<const float4*>(at & ~uintptr_t{15});
+        off = static_cast<uint32_t>(at & 15u);
+        a = w[0];
+        b = w[1];
+        c = w[off ? 2 : 1];
+    }
+    __device__ __forceinline__ void take(const uint4* m, int i, uint32_t skip) {
+        const float4* w = reinterpret_cast<const float4*>(m) + 2 * i;
+        off = 4 * skip;
+        a = w[0];
+        b = w[1];
+        c = w[off ? 2 : 1];
+    }
+    __device__ __forceinline__ void get(float* f) const {
+        const float x[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        float y[9];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) y[i] = off & 8u ? x[i + 2] : x[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = off & 4u ? y[i + 1] : y[i];
+    }
+};
+// Whether Shifted::load(p) stays within a matrix [begin, end) of rows and the
+// gaps between them.
+template <typename T>
+__device__ __forceinline__ bool inside(const T* p, const T* begin, const T* end) {
+    constexpr int64_t W = 16 / sizeof(T);  // a word's elements
+    return p - begin >= W && end - p >= 8 + W;
 }
 
 // out[i] = rne(scale * table[ids[i]]), zeros where the id lies outside the
@@ -97,7 +135,6 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
         }
     } else {
         constexpr int P = Chunk<TO>::kPhase;
-        constexpr int64_t W = 16 / sizeof(TT);  // a word's elements
         const TT* const end = table + (a.vocab - 1) * a.table_stride + a.dim;
         float f[U][8];
         int64_t j[U];  // the unit's first column
@@ -109,8 +146,10 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
             for (int k = 0; k < 8; ++k) f[u][k] = 0.0f;
             if (id[u] < 0 || j[u] >= a.dim) continue;
             const TT* p = table + id[u] * a.table_stride + j[u];
-            if (p - table >= W && end - p >= 8 + W) {
-                load_shifted(p, f[u]);
+            if (inside(p, table, end)) {
+                Shifted<TT> x;
+                x.load(p);
+                x.get(f[u]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -384,67 +423,71 @@ struct SumArgs {
     int64_t sum_blocks;
 };
 
-// A lane's columns: CU groups of 8, each a chunk (VEC) or 8 single columns,
-// 32 apart.  Group u starts at:
-template <bool VEC>
+// A lane's columns: CU groups of 8.  Group u starts at:
 __device__ __forceinline__ int32_t column(int32_t c0, int lane, int u) {
-    return c0 + kGroupCols * u + (VEC ? 8 * lane : lane);
+    return c0 + kGroupCols * u + 8 * lane;
 }
 
-// One group of a row.
-template <typename T, bool VEC>
-struct Group {
-    Chunk<T> c;
-    __device__ __forceinline__ void load(const T* row, int32_t at, int32_t dim) {
-        c.fill(0.0f);
-        if (at < dim) c.load_stream(row + at);
-    }
-    // of what another SM has written during this launch (from L2)
-    __device__ __forceinline__ void load_far(const float* row, int32_t at, int32_t dim) {
-        c.fill(0.0f);
-        if (at >= dim) return;
-        c.a = __ldcg(reinterpret_cast<const float4*>(row + at));
-        c.b = __ldcg(reinterpret_cast<const float4*>(row + at + 4));
-    }
-    __device__ __forceinline__ uint64_t pair(int k) const { return c.pair(k); }
-    static __device__ __forceinline__ void store(T* row, int32_t at, int32_t dim, const float* f) {
-        if (at < dim) Chunk<T>::store(row + at, f);
-    }
-};
-template <typename T>
-struct Group<T, false> {
-    float x[8];
-    __device__ __forceinline__ void load(const T* row, int32_t at, int32_t dim) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = at + 32 * k < dim ? to_f32(row[at + 32 * k]) : 0.0f;
-    }
-    __device__ __forceinline__ void load_far(const float* row, int32_t at, int32_t dim) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = at + 32 * k < dim ? __ldcg(row + at + 32 * k) : 0.0f;
-    }
-    __device__ __forceinline__ uint64_t pair(int k) const { return pk2(x[2 * k], x[2 * k + 1]); }
-    static __device__ __forceinline__ void store(T* row, int32_t at, int32_t dim, const float* f) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (at + 32 * k < dim) row[at + 32 * k] = from_f32<T>(f[k]);
-    }
-};
+// A group of a piece's sum, in `partial`, whose rows have room up to a
+// multiple of 4 columns.
+__device__ __forceinline__ void store_part(float* row, int32_t at, int32_t dim, const uint64_t* acc) {
+    float4 x;
+    upk2(acc[0], x.x, x.y);
+    upk2(acc[1], x.z, x.w);
+    if (at < dim) *reinterpret_cast<float4*>(row + at) = x;
+    upk2(acc[2], x.x, x.y);
+    upk2(acc[3], x.z, x.w);
+    if (at + 4 < dim) *reinterpret_cast<float4*>(row + at + 4) = x;
+}
+// (Another SM has written it during this launch: it comes from L2.)
+__device__ __forceinline__ void load_part(Chunk<float>& c, const float* row, int32_t at, int32_t dim) {
+    c.fill(0.0f);
+    if (at < dim) c.a = __ldcg(reinterpret_cast<const float4*>(row + at));
+    if (at + 4 < dim) c.b = __ldcg(reinterpret_cast<const float4*>(row + at + 4));
+}
 
+// Writes group u of token v's row.  VEC: from 16-byte boundaries on, on top of
+// `old`.  Otherwise the warp's 256 sums change places in `swap`, so that it
+// reads and writes consecutive single elements.
 template <typename TG, bool VEC, bool ACC>
-__device__ __forceinline__ void put_group(const SumArgs& p, int32_t v, int32_t at,
-                                          const uint64_t* acc, const Group<TG, VEC>& old) {
-    const uint64_t sc = pk2(p.a.scale, p.a.scale);
-    float f[8];
+__device__ __forceinline__ void put_group(const SumArgs& p, int32_t v, int32_t c0, int u, int lane,
+                                          const uint64_t* acc, const Chunk<TG>& old, float* swap) {
+    const int32_t dim = static_cast<int32_t>(p.a.dim), at = column(c0, lane, u);
+    TG* g = static_cast<TG*>(p.a.grad) + v * p.a.grad_stride;
+    if (VEC) {
+        const uint64_t sc = pk2(p.a.scale, p.a.scale);
+        float f[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        upk2(ACC ? fma2(acc[k], sc, old.pair(k)) : mul2(acc[k], sc), f[2 * k], f[2 * k + 1]);
-    Group<TG, VEC>::store(static_cast<TG*>(p.a.grad) + v * p.a.grad_stride, at,
-                          static_cast<int32_t>(p.a.dim), f);
+        for (int k = 0; k < 4; ++k)
+            upk2(ACC ? fma2(acc[k], sc, old.pair(k)) : mul2(acc[k], sc), f[2 * k], f[2 * k + 1]);
+        if (at < dim) Chunk<TG>::store(g + at, f);
+        return;
+    }
+    float4 lo, hi;
+    upk2(acc[0], lo.x, lo.y);
+    upk2(acc[1], lo.z, lo.w);
+    upk2(acc[2], hi.x, hi.y);
+    upk2(acc[3], hi.z, hi.w);
+    g += at - 7 * lane;  // the group's first column, plus the lane
+    const int32_t left = dim - (at - 7 * lane);
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = ACC && 32 * k < left ? to_f32(g[32 * k]) : 0.0f;
+    __syncwarp();
+    reinterpret_cast<float4*>(swap)[2 * lane] = lo;
+    reinterpret_cast<float4*>(swap)[2 * lane + 1] = hi;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float s = swap[32 * k + lane];
+        if (32 * k < left)
+            g[32 * k] = from_f32<TG>(ACC ? fmaf(s, p.a.scale, x[k]) : __fmul_rn(s, p.a.scale));
+    }
 }
 
 // Clears the rows of tokens without a position: a warp takes kZeroTokens
 // tokens and all columns.
-template <typename TG, bool VEC>
+template <typename TG>
 __device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t v0, int lane) {
     const int64_t v = v0 + lane;
     bool empty = false;
@@ -457,10 +500,11 @@ __device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t v0, int lan
     while (m) {
         TG* g = static_cast<TG*>(p.a.grad) + (v0 + __ffs(m) - 1) * p.a.grad_stride;
         m &= m - 1;
-        if (VEC)
-            for (int64_t c = 8 * lane; c < p.a.dim; c += 256) Chunk<TG>::store(g + c, zero);
-        else
-            for (int64_t c = lane; c < p.a.dim; c += 32) g[c] = from_f32<TG>(0.0f);
+        const RowCut<TG> cut(g, static_cast<int32_t>(p.a.dim));
+        const int32_t end = cut.head + 8 * cut.chunks;
+        for (int32_t c = cut.head + 8 * lane; c < end; c += 256) Chunk<TG>::store(g + c, zero);
+        if (lane < cut.head) g[lane] = from_f32<TG>(0.0f);
+        if (lane < cut.tail) g[end + lane] = from_f32<TG>(0.0f);
     }
 }
 
@@ -483,22 +527,23 @@ __device__ __forceinline__ int64_t piece_slot(int32_t at, bool first) {
 // Adds up a token's pieces in order and writes its row.
 template <typename TG, bool VEC, bool ACC, int CU>
 __device__ __forceinline__ void join(const SumArgs& p, int32_t v, int32_t first, int32_t count,
-                                  int32_t c0, int lane) {
+                                     int32_t c0, int lane, float* swap) {
     const int32_t step = piece_rows(count), dim = static_cast<int32_t>(p.a.dim);
     const TG* g = static_cast<const TG*>(p.a.grad) + v * p.a.grad_stride;
     for (int u = 0; u < CU; ++u) {
-        const int32_t at = column<VEC>(c0, lane, u);
-        Group<TG, VEC> old;
-        if (ACC) old.load(g, at, dim);
+        const int32_t at = column(c0, lane, u);
+        Chunk<TG> old;
+        old.fill(0.0f);
+        if (VEC && ACC && at < dim) old.load_stream(g + at);
         uint64_t acc[4] = {0, 0, 0, 0};
         constexpr int R = 8;
         for (int32_t b = 0; b < count; b += R * step) {
-            Group<float, VEC> x[R];
+            Chunk<float> x[R];
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 if (b + r * step < count)
-                    x[r].load_far(p.w.partial + piece_slot(first + b + r * step, b + r == 0) * p.w.step,
-                                  at, dim);
+                    load_part(x[r], p.w.partial + piece_slot(first + b + r * step, b + r == 0) * p.w.step,
+                              at, dim);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (b + r * step >= count) break;
@@ -506,7 +551,7 @@ __device__ __forceinline__ void join(const SumArgs& p, int32_t v, int32_t first,
                 for (int k = 0; k < 4; ++k) acc[k] = add2(acc[k], x[r].pair(k));
             }
         }
-        put_group<TG, VEC, ACC>(p, v, at, acc, old);
+        put_group<TG, VEC, ACC>(p, v, c0, u, lane, acc, old, swap);
     }
 }
 
@@ -550,7 +595,7 @@ __device__ __forceinline__ bool find_pieces(const SumArgs& p, int64_t tile, int 
 template <typename TG, bool VEC, bool ACC, int CU>
 __device__ __forceinline__ bool end_piece(const SumArgs& p, const Pieces& q, int from, int32_t slab,
                                           int lane, uint64_t (&acc)[CU][4],
-                                          const Group<TG, VEC> (&old)[CU]) {
+                                          const Chunk<TG> (&old)[CU], float* swap) {
     const int32_t c0 = slab * (kGroupCols * CU);
     const int32_t v = __shfl_sync(0xffffffffu, q.x.token, from);
     const int32_t n = __shfl_sync(0xffffffffu, q.x.count, from);
@@ -558,17 +603,13 @@ __device__ __forceinline__ bool end_piece(const SumArgs& p, const Pieces& q, int
     if (n <= kPiece) {
 #pragma unroll
         for (int u = 0; u < CU; ++u)
-            put_group<TG, VEC, ACC>(p, v, column<VEC>(c0, lane, u), acc[u], old[u]);
+            put_group<TG, VEC, ACC>(p, v, c0, u, lane, acc[u], old[u], swap);
     } else {
         const int32_t first = __shfl_sync(0xffffffffu, q.x.first, from);
         float* to = p.w.partial + piece_slot(q.j0 + from, q.j0 + from == first) * p.w.step;
 #pragma unroll
-        for (int u = 0; u < CU; ++u) {
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) upk2(acc[u][k], f[2 * k], f[2 * k + 1]);
-            Group<float, VEC>::store(to, column<VEC>(c0, lane, u), static_cast<int32_t>(p.a.dim), f);
-        }
+        for (int u = 0; u < CU; ++u)
+            store_part(to, column(c0, lane, u), static_cast<int32_t>(p.a.dim), acc[u]);
         __threadfence();
         __syncwarp();
         const int32_t step = piece_rows(n);
@@ -587,7 +628,7 @@ __device__ __forceinline__ bool end_piece(const SumArgs& p, const Pieces& q, int
 
 template <typename TG, bool VEC, bool ACC, int CU>
 __device__ __forceinline__ void join_pieces(const SumArgs& p, const Pieces& q, uint32_t joins,
-                                            int32_t slab, int lane) {
+                                            int32_t slab, int lane, float* swap) {
     while (joins) {
         __threadfence();
         const int from = __ffs(joins) - 1;
@@ -595,7 +636,7 @@ __device__ __forceinline__ void join_pieces(const SumArgs& p, const Pieces& q, u
         join<TG, VEC, ACC, CU>(p, __shfl_sync(0xffffffffu, q.x.token, from),
                                __shfl_sync(0xffffffffu, q.x.first, from),
                                __shfl_sync(0xffffffffu, q.x.count, from),
-                               slab * (kGroupCols * CU), lane);
+                               slab * (kGroupCols * CU), lane, swap);
     }
 }
 
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= p.sum_blocks) {
         const int64_t b = blockIdx.x - p.sum_blocks;
-        clear_rows<TG, true>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
+        clear_rows<TG>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
         return;
     }
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp;
@@ -634,7 +675,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
     const auto copy = [&](const void* row, int parts, int bytes, int slot) {
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-            const int32_t at = column<true>(c0, lane, u);
+            const int32_t at = column(c0, lane, u);
             if (at >= dim) continue;
             const char* from = static_cast<const char*>(row) + static_cast<int64_t>(at) * bytes;
 #pragma unroll
@@ -682,78 +723,113 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
         arrive();
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
-            Group<TD, true> row;
-            row.c.from_parts(&ring[warp][slot][u * PD][lane], 32);
+            Chunk<TD> row;
+            row.from_parts(&ring[warp][slot][u * PD][lane], 32);
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[u][k] = add2(acc[u][k], row.pair(k));
         }
         issue();
         if (!q.last(l)) continue;
-        Group<TG, true> old[CU];
+        Chunk<TG> old[CU];
         if (ACC) {
             arrive();
 #pragma unroll
-            for (int u = 0; u < CU; ++u) old[u].c.from_parts(&ring[warp][slot][u * PG][lane], 32);
+            for (int u = 0; u < CU; ++u) old[u].from_parts(&ring[warp][slot][u * PG][lane], 32);
             issue();
         }
         const int from = q.piece_of(l);
-        if (end_piece<TG, true, ACC, CU>(p, q, from, slab, lane, acc, old)) joins |= 1u << from;
+        if (end_piece<TG, true, ACC, CU>(p, q, from, slab, lane, acc, old, nullptr))
+            joins |= 1u << from;
     }
-    join_pieces<TG, true, ACC, CU>(p, q, joins, slab, lane);
+    join_pieces<TG, true, ACC, CU>(p, q, joins, slab, lane, nullptr);
 }
 
-// The same for rows at any alignment: single elements through registers, R
-// rows in flight.
+// The same for rows at any alignment: a slot holds the aligned 16-byte words
+// that a row's 256 columns touch, which the lanes shift into place; a slot whose
+// words might stick out of the matrix is copied by elements.  (Columns past the row's end
+// may hold another row's elements; their sums are not used.)
 template <typename TD, typename TG, bool ACC>
 __global__ void __launch_bounds__(kSumThreads)
-    embed_sum_scalar_kernel(const __grid_constant__ SumArgs p) {
-    constexpr int R = 8;
+    embed_sum_any_kernel(const __grid_constant__ SumArgs p) {
+    constexpr int W = kGroupCols * sizeof(TD) / 16 + 1;  // words of a slot
+    constexpr int E = 16 / sizeof(TD);                    // elements of a word
+    constexpr int D = kRing / (16 * W);
+    __shared__ __align__(16) uint4 ring[kSumWarps][D][W];
+    __shared__ __align__(16) float swap[kSumWarps][kGroupCols];
+    __shared__ uint32_t starts[kSumWarps][D];  // where in its first word a slot's row starts
     wait_prior_grids();
     allow_next_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= p.sum_blocks) {
         const int64_t b = blockIdx.x - p.sum_blocks;
-        clear_rows<TG, false>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
+        clear_rows<TG>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
         return;
     }
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp;
     const int64_t tile = w / p.slabs;
     const int32_t slab = static_cast<int32_t>(w - tile * p.slabs);
-    const int32_t at = column<false>(slab * kGroupCols, lane, 0), dim = static_cast<int32_t>(p.a.dim);
+    const int32_t c0 = slab * kGroupCols, dim = static_cast<int32_t>(p.a.dim);
+    const int32_t cols = min(kGroupCols, dim - c0);
     Pieces q;
     if (!find_pieces(p, tile, lane, q)) return;
-    const TD* dout = static_cast<const TD*>(p.a.dout);
+    const TD* const dout = static_cast<const TD*>(p.a.dout);
+    const TD* const end = dout + (p.a.n - 1) * p.a.dout_stride + dim;
+    int next = q.a, slot = 0;  // the next row to copy, and its slot
     int32_t pos = q.x.pos;
+    const auto issue = [&] {
+        if (next < q.e) {
+            if (next >= 32 && (next & 31) == 0)
+                pos = q.j0 + next + lane < q.count ? p.w.sorted[q.j0 + next + lane].pos : 0;
+            const TD* row = dout + __shfl_sync(0xffffffffu, pos, next & 31) * p.a.dout_stride + c0;
+            const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(TD));
+            if (lane == 0) starts[warp][slot] = skip;
+            uint4* const to = ring[warp][slot];
+            const TD* from = row - skip;
+            if (from - dout >= 0 && end - from >= W * E) {
+                const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to + lane));
+#pragma unroll
+                for (int k = 0; k < W; k += 32)
+                    if ((k + lane) * E < skip + cols)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * k),
+                                     "l"(from + (k + lane) * E)
+                                     : "memory");
+            } else {
+                for (int k = lane; k < skip + cols; k += 32)
+                    if (k >= skip) reinterpret_cast<TD*>(to)[k] = from[k];
+            }
+            if (ACC && q.last(next)) {  // the row that the sum is added to, soon
+                const TG* g = static_cast<const TG*>(p.a.grad) + c0 +
+                              __shfl_sync(0xffffffffu, q.x.token, q.piece_of(next)) * p.a.grad_stride;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(g + min(8 * lane, cols - 1)));
+            }
+            ++next;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        slot = slot + 1 == D ? 0 : slot + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < D; ++i) issue();
     uint64_t acc[1][4] = {{0, 0, 0, 0}};  // packed +0
     uint32_t joins = 0;
 #pragma unroll 1
-    for (int b = q.a; b < q.e; b += R) {
-        Group<TD, false> rows[R];
+    for (int l = q.a; l < q.e; ++l) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+        __syncwarp();
+        Shifted<TD> x;
+        x.take(ring[warp][slot], lane, starts[warp][slot]);
+        __syncwarp();
+        issue();
+        float f[8];
+        x.get(f);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int l = b + r;
-            if (l >= q.e) break;
-            if (l >= 32 && (l & 31) == 0)
-                pos = q.j0 + l + lane < q.count ? p.w.sorted[q.j0 + l + lane].pos : 0;
-            rows[r].load(dout + __shfl_sync(0xffffffffu, pos, l & 31) * p.a.dout_stride, at, dim);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int l = b + r;
-            if (l >= q.e) break;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[0][k] = add2(acc[0][k], rows[r].pair(k));
-            if (!q.last(l)) continue;
-            const int from = q.piece_of(l);
-            Group<TG, false> old[1];
-            if (ACC)
-                old[0].load(static_cast<const TG*>(p.a.grad) +
-                                __shfl_sync(0xffffffffu, q.x.token, from) * p.a.grad_stride,
-                            at, dim);
-            if (end_piece<TG, false, ACC, 1>(p, q, from, slab, lane, acc, old)) joins |= 1u << from;
-        }
+        for (int k = 0; k < 4; ++k) acc[0][k] = add2(acc[0][k], pk2(f[2 * k], f[2 * k + 1]));
+        if (!q.last(l)) continue;
+        const int from = q.piece_of(l);
+        Chunk<TG> none[1];
+        if (end_piece<TG, false, ACC, 1>(p, q, from, slab, lane, acc, none, swap[warp]))
+            joins |= 1u << from;
     }
-    join_pieces<TG, false, ACC, 1>(p, q, joins, slab, lane);
+    join_pieces<TG, false, ACC, 1>(p, q, joins, slab, lane, swap[warp]);
 }
 
 bool aligned_rows(const void* p, int64_t stride, int32_t dtype) {
@@ -796,7 +872,7 @@ cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t 
     if constexpr (VEC)
         return launch_vocab(embed_sum_kernel<TD, TG, ACC, CU>, grid, kSumThreads, 0, 1, p, stream);
     else
-        return launch_vocab(embed_sum_scalar_kernel<TD, TG, ACC>, grid, kSumThreads, 0, 1, p, stream);
+        return launch_vocab(embed_sum_any_kernel<TD, TG, ACC>, grid, kSumThreads, 0, 1, p, stream);
 }
 
 template <typename TD, typename TG, bool VEC, bool ACC>
