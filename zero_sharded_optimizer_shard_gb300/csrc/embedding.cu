@@ -185,7 +185,6 @@ constexpr int kSumThreads = 128;
 constexpr int kRing = 8192;        // bytes of rows in flight per summing warp
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kGroupCols = 256;    // columns of a warp: 8 per lane, times CU
-constexpr int kZeroTokens = 8;     // tokens whose untouched rows one warp clears
 
 // A sorted position: where it was, its token, the token's first sorted index
 // and number of positions.
@@ -419,7 +418,7 @@ struct SumArgs {
     Workspace w;
     Deal deal;
     int32_t rows;   // sorted positions whose pieces a summing warp takes: 8 or 16
-    int32_t slabs;
+    int32_t slabs, zero_tokens;
     int64_t sum_blocks;
 };
 
@@ -485,26 +484,27 @@ __device__ __forceinline__ void put_group(const SumArgs& p, int32_t v, int32_t c
     }
 }
 
-// Clears the rows of tokens without a position: a warp takes kZeroTokens
+// Clears the rows of tokens without a position: a warp takes p.zero_tokens
 // tokens and all columns.
 template <typename TG>
-__device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t v0, int lane) {
-    const int64_t v = v0 + lane;
+__device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t warp, int lane) {
+    constexpr int E = Chunk<TG>::kPhase;
+    const int64_t v0 = warp * p.zero_tokens, v = v0 + lane;
     bool empty = false;
-    if (lane < kZeroTokens && v < p.a.vocab) {
+    if (lane < p.zero_tokens && v < p.a.vocab) {
         const int32_t at = p.deal.place(static_cast<int32_t>(v));
         empty = p.w.off[at] == p.w.off[at + 1];
     }
     uint32_t m = __ballot_sync(0xffffffffu, empty);
-    const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     while (m) {
         TG* g = static_cast<TG*>(p.a.grad) + (v0 + __ffs(m) - 1) * p.a.grad_stride;
         m &= m - 1;
-        const RowCut<TG> cut(g, static_cast<int32_t>(p.a.dim));
-        const int32_t end = cut.head + 8 * cut.chunks;
-        for (int32_t c = cut.head + 8 * lane; c < end; c += 256) Chunk<TG>::store(g + c, zero);
-        if (lane < cut.head) g[lane] = from_f32<TG>(0.0f);
-        if (lane < cut.tail) g[end + lane] = from_f32<TG>(0.0f);
+        const int32_t head = RowCut<TG>(g, static_cast<int32_t>(p.a.dim)).head;
+        const int32_t words = (static_cast<int32_t>(p.a.dim) - head) / E, end = head + words * E;
+        for (int32_t c = lane; c < words; c += 32)
+            __stcs(reinterpret_cast<uint4*>(g + head) + c, make_uint4(0, 0, 0, 0));
+        if (lane < head) g[lane] = from_f32<TG>(0.0f);
+        if (lane < p.a.dim - end) g[end + lane] = from_f32<TG>(0.0f);
     }
 }
 
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= p.sum_blocks) {
         const int64_t b = blockIdx.x - p.sum_blocks;
-        clear_rows<TG>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
+        clear_rows<TG>(p, b * kSumWarps + warp, lane);
         return;
     }
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp;
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kSumThreads)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= p.sum_blocks) {
         const int64_t b = blockIdx.x - p.sum_blocks;
-        clear_rows<TG>(p, (b * kSumWarps + warp) * kZeroTokens, lane);
+        clear_rows<TG>(p, b * kSumWarps + warp, lane);
         return;
     }
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp;
@@ -867,7 +867,9 @@ cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t 
     p.slabs = static_cast<int32_t>((a.dim + kGroupCols * CU - 1) / (kGroupCols * CU));
     p.rows = a.n > 32768 ? 16 : 8;
     p.sum_blocks = ((a.n + p.rows - 1) / p.rows * p.slabs + kSumWarps - 1) / kSumWarps;
-    const int64_t each = kSumWarps * kZeroTokens;
+    p.zero_tokens = 8;  // fewer where that leaves SMs without a warp
+    while (p.zero_tokens > 1 && a.vocab < p.zero_tokens * kSumWarps * 304) p.zero_tokens /= 2;
+    const int64_t each = kSumWarps * p.zero_tokens;
     const int64_t grid = p.sum_blocks + (ACC ? 0 : (a.vocab + each - 1) / each);
     if constexpr (VEC)
         return launch_vocab(embed_sum_kernel<TD, TG, ACC, CU>, grid, kSumThreads, 0, 1, p, stream);
