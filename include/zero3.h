@@ -543,7 +543,7 @@ zero3_status zero3_merge_shards(const zero3_plan* plan, const char* const* shard
  *  - ZERO3_EINVAL, with nothing launched: unknown dtype or id type; NULL or
  *    misaligned pointer; vocab < 1 or above 2^30; a stride below the columns;
  *    n < 0 or above 2^27 rows of logits (2^31 - 1 tokens); dim above 2^27;
- *    rows times columns above 2^41, or n * ceil(vocab / 8192) above 2^31 - 1 in the calls that
+ *    rows times columns above 2^41, or n * ceil(vocab / 4096) above 2^31 - 1 in the calls that
  *    can write a gradient of logits; a scale that is not finite, or an
  *    inverse temperature that is not finite and positive. */
 

@@ -45,8 +45,8 @@ bool embedding_ok(int64_t vocab, int64_t dim, int64_t table_stride, int64_t n, i
            rows_ok(n, dim, row_stride);
 }
 
-// Blocks of the elementwise gradients: one per 8192 elements of a row.
-bool grid_ok(int64_t n, int64_t vocab) { return n * ((vocab + 8191) / 8192) <= INT32_MAX; }
+// Blocks of the elementwise gradients: one per 4096 elements of a row.
+bool grid_ok(int64_t n, int64_t vocab) { return n * ((vocab + 4095) / 4096) <= INT32_MAX; }
 
 }  // namespace
 
