@@ -92,6 +92,9 @@ __device__ __forceinline__ bool inside(const T* p, const T* begin, const T* end)
 // the output row's 16-byte boundaries, one more than dim / 8 rounded up, and the
 // table's elements are shifted into place; a unit that sticks out of its row, or
 // whose words would lie outside the table, goes by single elements.
+//
+// 16384 rows of 4096 bf16 take 30.4 us (182 MB, 6.0 TB/s), 8192 of 2047 15.1 us, one
+// row of 2048 1.4 us.
 template <typename TT, typename TO, bool VEC, int NT, int U>
 __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ EmbedArgs a) {
     wait_prior_grids();
@@ -178,11 +181,22 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
 // ascending order, of dout[i]), in two launches: a stable counting sort of
 // the positions by token, and the rows' sums.  Sums are binary32 and their
 // order depends on the tokens alone, so the result does not depend on timing.
+// (Adding each position's row to its token's row with atomics would neither
+// have a fixed order nor spread the frequent tokens' work.)
+//
+// Both launches: 8192 x 768 bf16 into 50257 rows, all written, 20.0 us; 32768 x 2048
+// bf16 added to bf16 49.4 us (220 MB: 4.5 TB/s), to binary32 71 us, binary32 to
+// binary32 120 us.
 constexpr int kOwn = 512;          // tokens a sorting block owns at most
 constexpr int kList = 512;         // own positions a sorting warp lists
-constexpr int kPiece = 16;         // shortest piece of a token that has several
+// Shortest piece of a token that has several.  Short ones spread frequent tokens,
+// long ones cost fewer partial sums: at 8 / 16 / 32, 2048 x 64 takes 10.3 / 11.1 / 13.8
+// us, 32768 x 2048 53.4 / 51.0 / 50.4.
+constexpr int kPiece = 16;
 constexpr int kSumThreads = 128;
-constexpr int kRing = 8192;        // bytes of rows in flight per summing warp
+// Bytes of rows in flight per summing warp (4096: 2048 x 64 10.8 us, not 11.1, but
+// binary32 rows are left with few).
+constexpr int kRing = 8192;
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kGroupCols = 256;    // columns of a warp: 8 per lane, times CU
 
@@ -259,7 +273,8 @@ struct SortArgs {
 // warp places its positions in order.  A warp's list that overflows (a token
 // that fills the batch) is read from the ids again.  Latency-bound: all that
 // counts is that a warp's loads are in flight together and that little is done
-// per id that is not the block's.
+// per id that is not the block's.  By itself 6 us for 3001 ids, 8 for 8192, 13 for
+// 32768.  (A radix sort over the grid needs a wait between its digits.)
 template <int W>
 struct SortShared {
     int32_t cnt[W][kOwn];
@@ -645,7 +660,9 @@ __device__ __forceinline__ void join_pieces(const SumArgs& p, const Pieces& q, u
 // among `rows` consecutive positions, for CU groups of columns: the work
 // is even however often a token occurs.  Pieces of one token are added up in
 // order by whichever warp of the token comes last.  Bound by HBM once there
-// are some thousand positions: each row is read once.
+// are some thousand positions: each row is read once (32768 x 2048 added to bf16:
+// 220 MB in about 37 us, 20 warps per SM; more blocks per SM by fewer registers
+// spill, 61 us for 49 in all), by latency below.
 //
 // Rows on 16-byte boundaries pass through a ring of D slots per warp in
 // shared memory, filled by asynchronous 16-byte copies (each lane reads what
@@ -746,7 +763,8 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
 
 // The same for rows at any alignment: a slot holds the aligned 16-byte words
 // that a row's 256 columns touch, which the lanes shift into place; a slot whose
-// words might stick out of the matrix is copied by elements.  (Columns past the row's end
+// words might stick out of the matrix is copied by elements.  32768 x 2047 added to
+// bf16: 76 us (131 by single elements).  (Columns past the row's end
 // may hold another row's elements; their sums are not used.)
 template <typename TD, typename TG, bool ACC>
 __global__ void __launch_bounds__(kSumThreads)
@@ -841,9 +859,10 @@ template <typename TT, typename TO, bool VEC>
 cudaError_t embed_typed(const EmbedArgs& a, cudaStream_t stream) {
     constexpr int NT = 256;
     const int64_t items = a.n * (VEC ? a.dim / 8 : a.dim / 8 + 2);
-    // few units: one per thread, so that they spread over the SMs; many: several,
-    // for bytes in flight (8192 x 2047 bf16 at 1 / 2 / 4 shifted units per thread:
-    // 15.7 / 15.1 / 16.7 us; by single elements 40 us)
+    // Few units: one per thread, so that they spread over the SMs (64 rows of
+    // 4096 bf16 1.5 us, 1.8 at four per thread); many: several, for bytes in flight
+    // (8192 x 2047 bf16 at 1 / 2 / 4 shifted units per thread: 15.7 / 15.1 / 16.7 us; by
+    // single elements 40 us).
     if (items <= 152 * NT * 4)
         return launch_vocab(embed_kernel<TT, TO, VEC, NT, 1>, (items + NT - 1) / NT, NT, 0, 1, a, stream);
     constexpr int U = VEC ? 4 : 2;
@@ -865,9 +884,13 @@ cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t 
     p.w = w;
     p.deal = deal_of(a.vocab);
     p.slabs = static_cast<int32_t>((a.dim + kGroupCols * CU - 1) / (kGroupCols * CU));
+    // More warps, or fewer with more rows of their own: 8 / 16 rows per warp, 32768 x
+    // 2048 50.1 / 51.2 us, 65536 x 768 62.6 / 54.1.
     p.rows = a.n > 32768 ? 16 : 8;
     p.sum_blocks = ((a.n + p.rows - 1) / p.rows * p.slabs + kSumWarps - 1) / kSumWarps;
-    p.zero_tokens = 8;  // fewer where that leaves SMs without a warp
+    // Fewer tokens per clearing warp where that leaves SMs without one (1483 rows of
+    // 2834 binary32: 6.4 us, 12.6 at 8).
+    p.zero_tokens = 8;
     while (p.zero_tokens > 1 && a.vocab < p.zero_tokens * kSumWarps * 304) p.zero_tokens /= 2;
     const int64_t each = kSumWarps * p.zero_tokens;
     const int64_t grid = p.sum_blocks + (ACC ? 0 : (a.vocab + each - 1) / each);
@@ -879,9 +902,13 @@ cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t 
 
 template <typename TD, typename TG, bool VEC, bool ACC>
 cudaError_t sum_typed(const EmbedGradArgs& a, const Workspace& w, cudaStream_t stream) {
-    // two groups of columns per lane where that leaves few lanes idle
-    if (VEC && (a.dim % (2 * kGroupCols) == 0 || a.dim >= 8 * kGroupCols))
-        return sum_launch<TD, TG, VEC, ACC, VEC ? 2 : 1>(a, w, stream);
+    // Two groups of columns per lane halve the warps that find pieces and make
+    // wider reads, where enough warps are left and few lanes idle: one / two groups,
+    // 32768 x 2048 59.6 / 49.4 us, 8192 x 4096 31.7 / 27.9, 8192 x 512 14.9 / 16.7.
+    // Binary32 rows are left with too short a ring: 8192 x 2048 41 / 48 us.
+    if constexpr (VEC && sizeof(TD) == 2)
+        if (a.n * a.dim >= 1 << 24 && (a.dim % (2 * kGroupCols) == 0 || a.dim >= 8 * kGroupCols))
+            return sum_launch<TD, TG, VEC, ACC, 2>(a, w, stream);
     return sum_launch<TD, TG, VEC, ACC, 1>(a, w, stream);
 }
 
@@ -931,6 +958,9 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, cudaStream_t stream) {
     s.deal = deal_of(a.vocab);
     const int64_t grid = int64_t{1} << s.deal.shift;
     cudaError_t e;
+    // Warps per block: each reads its part of all ids one batch after the other, but
+    // every warp's counts are summed up.  8 / 16 warps: 512 tokens 8.3 / 8.9 us (768
+    // columns), 4096 15.4 / 14.8 (64); 16 / 32: 2048 13.8 / 15.1 (64), 8192 22.5 / 20.7 (768).
     if (a.n <= 1024)
         e = sort_launch<8, 4>(s, grid, stream);
     else if (a.n <= 4096)

@@ -278,7 +278,10 @@ constexpr int resident() {
 
 // One row per cluster of a.cluster blocks (one block where rows abound).
 // Bound by HBM: the row is read once, each thread keeping the running
-// maximum, sum and weighted sum of its share in registers.
+// maximum, sum and weighted sum of its share in registers (8192 rows of 50257 bf16
+// with entropy: 125 us, 6.6 TB/s; with 20 alternatives 172 us; 1021 of 31999 binary32
+// with 5 alternatives 31 us).  With few rows bound by latency: 4 rows of 50257
+// take 4.0 us without alternatives and 7.7 us with 20.
 template <typename T, int NT, int U, bool ENT, bool TOP>
 __global__ void __launch_bounds__(NT, resident<T, ENT, TOP>() / NT)
     logprob_kernel(const __grid_constant__ LogprobArgs a) {
@@ -396,7 +399,7 @@ __device__ __forceinline__ void grad_chunk(const Chunk<T>& c, T* out, int32_t at
 }
 
 // A block takes 8 * NT * U consecutive elements of one row.  Elementwise and
-// bound by HBM (one read, one write); in-place is allowed, so every element
+// bound by HBM (one read, one write; 8192 x 50257 bf16 with entropy 236 us, 7.0 TB/s); in-place is allowed, so every element
 // is read by the thread that writes it.  SAME: row and gradient row start at
 // the same distance from a 16-byte boundary, so one cut serves both.
 template <typename T, bool ENT, bool SAME, int NT, int U>
@@ -471,8 +474,13 @@ __global__ void __launch_bounds__(NT)
 
 template <typename T, bool ENT, bool TOP, int NT>
 cudaError_t launch_blocks(LogprobArgs a, cudaStream_t stream) {
+    // Chunks in flight per thread: 64 bytes, but 128 of binary32 where registers
+    // limit the warps anyway.  Two / four chunks: 8192 x 31999 binary32 148 / 194 us,
+    // with alternatives 191 / 183; 8192 x 4000 bf16 19.0 / 17.6.
     constexpr int U = sizeof(T) == 2 || TOP ? 4 : 2;
     const int64_t chunks = a.vocab / 8;
+    // Blocks per row, up to the SMs' number: 4 rows of 50257 take 4.0 us (one block per
+    // row: 5.2), 64 8.0 (8.7; 12.3 with up to 304 blocks).
     int C = 1;
     while (C < 8 && a.n * C < 152 && chunks / (2 * C) >= 2 * NT) C *= 2;
     a.cluster = C;
