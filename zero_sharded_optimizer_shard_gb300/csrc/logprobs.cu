@@ -58,14 +58,12 @@ __device__ __forceinline__ void offer(TopShared& sh, uint32_t key, int32_t index
     if (at < kCandidates) sh.cand[at] = candidate(key, index);
 }
 
-// Offers the elements of chunk c whose key is at least `bound`.
+// Offers the elements of chunk c, which holds x, whose key is at least `bound`.
 template <typename T>
 __device__ __forceinline__ void offer_chunk(TopShared& sh, const Part<T>& p, int32_t c,
-                                            uint32_t bound) {
-    Chunk<T> x;
-    const int32_t at = p.cut.head + 8 * c;
-    x.load(p.row + at);
+                                            const Chunk<T>& x, uint32_t bound) {
     if (key_of(x.max()) < bound) return;
+    const int32_t at = p.cut.head + 8 * c;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const uint32_t key = key_of(chunk_value(x, e));
@@ -93,7 +91,11 @@ __device__ int offer_all(TopShared& sh, const Part<T>& p, uint32_t bound) {
     __syncthreads();
     if (threadIdx.x == 0) sh.count = 0;
     __syncthreads();
-    for (int32_t c = p.c0 + threadIdx.x; c < p.c1; c += NT) offer_chunk(sh, p, c, bound);
+    for (int32_t c = p.c0 + threadIdx.x; c < p.c1; c += NT) {
+        Chunk<T> x;
+        x.load(p.row + p.cut.head + 8 * c);
+        offer_chunk(sh, p, c, x, bound);
+    }
     offer_edges(sh, p, bound);
     __syncthreads();
     return sh.count;
@@ -195,9 +197,22 @@ __device__ int find_top(TopShared& sh, const Part<T>& p, float best, bool any, i
     const int share = (p.c1 - p.c0 + NT - 1) / NT;
     bool over = flagged > 4 * k + 32;
     if (!over) {
-        for (int i = tid; i < flagged * share; i += NT) {
-            const int32_t c = p.c0 + sh.thread[i % flagged] + (i / flagged) * NT;
-            if (c < p.c1) offer_chunk(sh, p, c, bound);
+        // Chunks whose loads are in flight together: one / four, 8192 x 50257 bf16 with
+        // 20 alternatives 172 / 163 us (4 rows 7.7 / 7.8); binary32 lacks the registers
+        // (two: 8192 x 31999 191 us, not 187).
+        constexpr int U = sizeof(T) == 2 ? 4 : 1;
+        for (int i = tid; i < flagged * share; i += U * NT) {
+            Chunk<T> x[U];
+            int32_t c[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = i + u * NT;
+                c[u] = k < flagged * share ? p.c0 + sh.thread[k % flagged] + (k / flagged) * NT : p.c1;
+                if (c[u] < p.c1) x[u].load(p.row + p.cut.head + 8 * c[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c[u] < p.c1) offer_chunk(sh, p, c[u], x[u], bound);
         }
         offer_edges(sh, p, bound);
         __syncthreads();
@@ -279,9 +294,9 @@ constexpr int resident() {
 // One row per cluster of a.cluster blocks (one block where rows abound).
 // Bound by HBM: the row is read once, each thread keeping the running
 // maximum, sum and weighted sum of its share in registers (8192 rows of 50257 bf16
-// with entropy: 125 us, 6.6 TB/s; with 20 alternatives 172 us; 1021 of 31999 binary32
+// with entropy: 125 us, 6.6 TB/s; with 20 alternatives 163 us; 1021 of 31999 binary32
 // with 5 alternatives 31 us).  With few rows bound by latency: 4 rows of 50257
-// take 4.0 us without alternatives and 7.7 us with 20.
+// take 4.0 us without alternatives and 7.8 us with 20.
 template <typename T, int NT, int U, bool ENT, bool TOP>
 __global__ void __launch_bounds__(NT, resident<T, ENT, TOP>() / NT)
     logprob_kernel(const __grid_constant__ LogprobArgs a) {
@@ -476,7 +491,7 @@ template <typename T, bool ENT, bool TOP, int NT>
 cudaError_t launch_blocks(LogprobArgs a, cudaStream_t stream) {
     // Chunks in flight per thread: 64 bytes, but 128 of binary32 where registers
     // limit the warps anyway.  Two / four chunks: 8192 x 31999 binary32 148 / 194 us,
-    // with alternatives 191 / 183; 8192 x 4000 bf16 19.0 / 17.6.
+    // with alternatives 191 / 187; 8192 x 4000 bf16 19.0 / 17.6.
     constexpr int U = sizeof(T) == 2 || TOP ? 4 : 2;
     const int64_t chunks = a.vocab / 8;
     // Blocks per row, up to the SMs' number: 4 rows of 50257 take 4.0 us (one block per
