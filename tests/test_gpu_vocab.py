@@ -221,6 +221,32 @@ def test_embedding_backward_sparse(Z, ids, accumulate):
               accumulate=accumulate)
 
 
+@pytest.mark.parametrize("dim", [24, 27])
+@pytest.mark.parametrize("n", [1024, 1025, 4096, 4097, 32768, 32769])
+def test_embedding_backward_batch_sizes(Z, n, dim):
+    """Frequent tokens in batches at the edges of the sizes that are sorted and
+    summed differently."""
+    grad_case(Z, n, 300, dim, "f32", "f32", "i32", zipf(np.random.default_rng(n), n, 300))
+
+
+@pytest.mark.parametrize("n", [8191, 8192, 32769])
+def test_embedding_backward_wide_rows(Z, n):
+    grad_case(Z, n, 700, 2048 if n < 10000 else 512, "bf16", "bf16", "i64",
+              zipf(np.random.default_rng(n), n, 700), accumulate=True, scale=0.5)
+
+
+@pytest.mark.parametrize("dim", [16, 19])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_backward_pieces(Z, dim, accumulate):
+    """Tokens with as many positions as fill pieces of every length exactly, or
+    one more or less."""
+    counts = [7, 8, 9, 15, 16, 17, 31, 32, 33, 511, 512, 513, 2047, 2048, 2049, 8191, 8192, 8193]
+    ids = np.concatenate([np.full(c, 5 * v + 2) for v, c in enumerate(counts)])
+    np.random.default_rng(1).shuffle(ids)
+    grad_case(Z, len(ids), 100, dim, "bf16", "f32", "i32", ids, accumulate=accumulate)
+
+
+
 # ------------------------------------------------------------ log probabilities
 def logits(rng, n, vocab, kind="normal"):
     x = rng.normal(size=(n, vocab)) * 3
@@ -292,6 +318,13 @@ def logprob_case(Z, n, vocab, dtype, kind, k, pad=0, off=0, ids="i64", scale=1.0
 ])
 def test_logprobs(Z, n, vocab, k, dtype):
     logprob_case(Z, n, vocab, dtype, "normal", k, scale=1.0 if n % 2 else 0.7)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,vocab,k", [(700, 1003, 0), (607, 1003, 0), (1823, 8193, 2), (1824, 8193, 2),
+                                       (1824, 8193, 0), (80, 25001, 3), (38, 12345, 7)])
+def test_logprobs_rows_per_warp_block_and_cluster(Z, n, vocab, k, dtype):
+    logprob_case(Z, n, vocab, dtype, "masked", k, ids="i32")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -503,6 +536,15 @@ def distill_case(Z, n, vocab, K, dtype, td, kind, xkind="normal", pads=(0, 0), o
 def test_distill(Z, n, vocab, K, kind, dtype):
     distill_case(Z, n, vocab, K, dtype, "f32" if K % 2 else dtype, kind,
                  scale=1.0 if n % 2 else 0.5, ids="i32" if n % 3 else "i64", tpad=n % 4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,vocab,K,kind", [
+    (3, 4096, 33, "repeated"), (3, 8192, 5, "ragged"), (37, 8193, 40, "plain"), (2, 12001, 64, "repeated"),
+    (150, 10240, 9, "ragged"), (160, 10241, 9, "plain"), (3, 20480, 31, "plain"), (2, 20481, 70, "ragged"),
+])
+def test_distill_rows_per_block_and_cluster(Z, n, vocab, K, kind, dtype):
+    distill_case(Z, n, vocab, K, dtype, dtype, kind, "masked", scale=0.9)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
