@@ -534,6 +534,8 @@ zero3_status zero3_merge_shards(const zero3_plan* plan, const char* const* shard
  *    an elementwise call, take the wide path.
  *  - dtypes: ZERO3_BF16 or ZERO3_F32 each.  Everything is computed in
  *    binary32 and rounded once, to nearest even, when it is stored.
+ *    A logit whose product with the inverse temperature overflows binary32
+ *    counts as infinite.
  *  - Token ids are int32 or int64 (zero3_itype).  An id outside [0, vocab)
  *    marks an ignored position (padding); it is never read through.
  *  - Results do not depend on timing: sums have a fixed order.

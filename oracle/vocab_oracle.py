@@ -36,6 +36,12 @@ def embedding_backward(dout, ids, scale, vocab, base=None):
     return g, mag, count
 
 
+def scaled(x, scale):
+    """x * scale; what overflows binary32 is infinite."""
+    z = np.asarray(x, np.float64) * scale
+    return np.where(np.abs(z) >= 2.0 ** 128 - 2.0 ** 103, np.copysign(np.inf, z), z)
+
+
 def _log_softmax(z):
     """(log softmax, lse); rows of -inf alone give -inf everywhere.  The
     maximum is taken off before the logarithm of the sum: at 1e38 the sum of
@@ -50,7 +56,7 @@ def _log_softmax(z):
 
 def token_logprobs(logits, targets, scale, k=0):
     x = np.asarray(logits, np.float64)
-    logp, lse = _log_softmax(x * scale)
+    logp, lse = _log_softmax(scaled(x, scale))
     n, V = x.shape
     lp = np.array([logp[i, t] if 0 <= t < V else 0.0 for i, t in enumerate(targets)])
     with np.errstate(invalid="ignore"):
@@ -67,7 +73,7 @@ def token_logprobs_backward(logits, targets, scale, dlogprob=None, dentropy=None
     x = np.asarray(logits, np.float64)
     n, V = x.shape
     out = token_logprobs(x, targets, scale)
-    logp, lse = _log_softmax(x * scale)
+    logp, lse = _log_softmax(scaled(x, scale))
     p = np.exp(logp)
     dx = np.zeros_like(x)
     for i, t in enumerate(targets):
@@ -84,7 +90,7 @@ def token_logprobs_backward(logits, targets, scale, dlogprob=None, dentropy=None
 
 def teacher_probabilities(teacher, teacher_ids, scale, vocab):
     """[n, k] probabilities; 0 for entries that do not count."""
-    t = np.asarray(teacher, np.float64) * scale
+    t = scaled(teacher, scale)
     ids = np.asarray(teacher_ids)
     t = np.where((ids >= 0) & (ids < vocab), t, NEG)
     logq, lse = _log_softmax(t)
@@ -96,7 +102,7 @@ def distill(logits, teacher, teacher_ids, scale, weight=None):
     row the sum of the loss terms' magnitudes)."""
     x = np.asarray(logits, np.float64)
     n, V = x.shape
-    logp, lse = _log_softmax(x * scale)
+    logp, lse = _log_softmax(scaled(x, scale))
     q, logq, some = teacher_probabilities(teacher, teacher_ids, scale, V)
     w = np.ones(n) if weight is None else np.asarray(weight, np.float64)
     loss, mag, dx = np.zeros(n), np.zeros(n), np.zeros_like(x)

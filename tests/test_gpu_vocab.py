@@ -382,6 +382,53 @@ def test_logprobs_not_finite(Z, vocab):
     assert torch.isfinite(lp[3]) and bool((ti[3] >= 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [30, 9001])
+def test_products_that_overflow_count_as_infinite(Z, vocab, dtype):
+    """Masks of the lowest value under a temperature below one: the masked
+    tokens have no weight, and a row of them alone is an empty one; logits that
+    overflow upwards are infinite."""
+    n, K, low = 4, 5, -3.3895313892515355e38
+    rng = np.random.default_rng(vocab)
+    x = rng.normal(size=(n, vocab))
+    x[0] = low
+    x[1, 3:] = low
+    x[2, 7] = 3e38
+    xm = Mat(x, DT[dtype])
+    t = [1, 1, 1, 1]
+    it = ids_tensor(t, "i64")
+    lp, lse, ent = (torch.empty(n, device="cuda") for _ in range(3))
+    ti, tl = torch.empty(n, 4, device="cuda", dtype=torch.int32), torch.empty(n, 4, device="cuda")
+    Z.zero3_token_logprobs(xm.ptr, code(Z, dtype), n, vocab, vocab, it.data_ptr(), Z.I64, 1.5, 4,
+                           lp.data_ptr(), lse.data_ptr(), ent.data_ptr(), ti.data_ptr(),
+                           tl.data_ptr(), stream())
+    ref = V.token_logprobs(xm.host(), t, 1.5, 4)
+    tol = sum_tol(vocab) + 64 * U
+    for got, name in ((lp, "logprob"), (lse, "lse"), (tl, "top_logprobs")):
+        close(got.cpu(), ref[name], tol)
+    h = np.where(np.isnan(ref["lse"]), np.nan, ref["entropy"])
+    close(ent.cpu(), h, tol * (2 + 2 * np.where(np.isnan(h), 0, h)))
+    assert bool((ti[2] == -1).all())
+    keep = [0, 1, 3]
+    assert np.array_equal(ti.cpu().numpy()[keep], ref["top_ids"][keep])
+
+    tt = rng.normal(size=(n, K))
+    tt[1, 1:] = low
+    tt[3] = low  # an empty list
+    ids = np.stack([rng.choice(vocab, K, replace=False) for _ in range(n)])
+    ids[1] = np.arange(K)
+    ids[1, 0] = 2  # a token that the student has not masked
+    ids[1, 2] = 0
+    tm, idt = Mat(tt, DT[dtype]), ids_tensor(ids, "i32")
+    loss, dx = torch.empty(n, device="cuda"), Mat(np.zeros((n, vocab)), DT[dtype])
+    Z.zero3_distill_loss(xm.ptr, code(Z, dtype), n, vocab, vocab, tm.ptr, code(Z, dtype), idt.data_ptr(),
+                         Z.I32, K, K, 1.5, None, loss.data_ptr(), None, dx.ptr, vocab, stream())
+    rl, rdx, _, mag = V.distill(xm.host(), tm.host(), ids, 1.5)
+    close(loss.cpu(), rl, np.where(np.isnan(rl), 0, (tol + 64 * U) * (mag + 1)))
+    close(dx.host(), rdx, np.where(np.isnan(rdx), 0, 4 * tol + rounding(dtype, rdx)))
+    assert loss[0] == 0 and loss[3] == 0 and not dx.host()[[0, 3]].any()
+
+
 def grad_tol(dtype, ref, p, d, g, h, H, scale):
     """Bound of a logit gradient's error (per element); d = log p."""
     d = np.where(np.isfinite(d), np.abs(d), 0)

@@ -100,11 +100,12 @@ __device__ __forceinline__ ListKind list_entries(const DistillArgs& a, int64_t r
         for (int u = 0; u < kEntries; ++u) {
             const int k = b + 32 * u;
             if (k >= a.k) break;
-            const bool counts = hi[u] == 0 && lo[u] < static_cast<uint32_t>(a.vocab) && v[u] != neg_inf();
+            const float z = __fmul_rn(v[u], a.scale);
+            const bool counts = hi[u] == 0 && lo[u] < static_cast<uint32_t>(a.vocab) && z != neg_inf();
             t.id[k] = counts ? static_cast<int32_t>(lo[u]) : -1;
             t.q[k] = v[u];
             some = some || counts;
-            nan = nan || (counts && !(__fmul_rn(v[u], a.scale) < -neg_inf()));
+            nan = nan || (counts && !(z < -neg_inf()));
         }
     }
     return __any_sync(0xffffffffu, nan) ? kListNan

@@ -240,9 +240,9 @@ __device__ __forceinline__ void soft_rebase(Soft& q, float to) {
 }
 
 // The maximum that lanes with weight agree on; lanes without (s = 0) do not
-// count (their mz is a placeholder).
+// count (their mz is a placeholder) unless their maximum has overflowed.
 __device__ __forceinline__ float soft_top(const Soft& q) {
-    return q.s != 0.0f ? q.mz : neg_inf();
+    return q.s != 0.0f || q.mz == -neg_inf() ? q.mz : neg_inf();
 }
 
 // Joins the statistics of `width` lanes (a power of two); every lane gets
@@ -259,6 +259,7 @@ __device__ __forceinline__ void soft_lanes(Soft& q) {
         q.s = __fadd_rn(q.s, __shfl_xor_sync(0xffffffffu, q.s, o));
         if (ENT) q.a = __fadd_rn(q.a, __shfl_xor_sync(0xffffffffu, q.a, o));
     }
+    if (top == -neg_inf()) q.s = __int_as_float(0x7fffffff);
 }
 
 // Joins the statistics of a block of NT threads; every thread gets the
