@@ -432,7 +432,7 @@ struct SumArgs {
     EmbedGradArgs a;
     Workspace w;
     Deal deal;
-    int32_t rows;   // sorted positions whose pieces a summing warp takes: 8 or 16
+    int32_t rows;   // sorted positions whose pieces a summing warp takes
     int32_t slabs, zero_tokens;
     int64_t sum_blocks;
 };
@@ -885,8 +885,9 @@ cudaError_t sum_launch(const EmbedGradArgs& a, const Workspace& w, cudaStream_t 
     p.deal = deal_of(a.vocab);
     p.slabs = static_cast<int32_t>((a.dim + kGroupCols * CU - 1) / (kGroupCols * CU));
     // More warps, or fewer with more rows of their own: 8 / 16 rows per warp, 32768 x
-    // 2048 50.1 / 51.2 us, 65536 x 768 62.6 / 54.1.
-    p.rows = a.n > 32768 ? 16 : 8;
+    // 2048 50.1 / 51.2 us, 65536 x 768 62.6 / 54.1; 2 / 8: 64 x 64 4.8 / 6.7 us, 512 x
+    // 768 8.1 / 8.2, 8192 x 768 22.9 / 20.1.
+    p.rows = a.n > 32768 ? 16 : a.n > 512 ? 8 : 2;
     p.sum_blocks = ((a.n + p.rows - 1) / p.rows * p.slabs + kSumWarps - 1) / kSumWarps;
     // Fewer tokens per clearing warp where that leaves SMs without one (1483 rows of
     // 2834 binary32: 6.4 us, 12.6 at 8).
