@@ -1,0 +1,85 @@
+"""The vocabulary operators on the GPU at the edges of their kernels: rows of
+every kind side by side, lists that overflow, sizes at the limits.  Tolerances
+as in test_gpu_vocab.py, from binary32 arithmetic.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import vocab_oracle as V  # noqa: E402
+from test_gpu_vocab import (DT, U, Mat, close, code, ids_tensor, logits, rounding,  # noqa: E402
+                            stream, sum_tol)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def Z(lib):
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from zero_sharded_optimizer_shard_gb300 import zero3
+    return zero3
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,vocab,K", [
+    (6, 500, 7), (160, 3001, 40), (40, 8193, 130), (6, 9000, 33), (160, 9001, 3), (6, 50257, 64),
+    (160, 21003, 300), (80, 40007, 5),
+])
+def test_distill_rows_of_every_kind_side_by_side(Z, n, vocab, K, dtype):
+    """Rows whose list is full, repeated or empty and rows without any student
+    token in one call: the warp of the list and the warps of the logits meet
+    wherever a row's kind leads them, in place and not, for every number of threads
+    per row and of blocks per row."""
+    rng = np.random.default_rng(n + vocab + K)
+    xs = logits(rng, n, vocab)
+    ids = np.stack([rng.choice(vocab, K, replace=False) for _ in range(n)])
+    kind = np.arange(n) % 5
+    ids[kind == 1] = ids[kind == 1] % 3  # a few tokens, again and again
+    ids[kind == 2] = -1
+    xs[kind == 3] = -np.inf
+    xs[kind == 4, : vocab // 2] = -np.inf
+    ids[kind == 4] = vocab // 2 + ids[kind == 4] % (vocab - vocab // 2)
+    x = Mat(xs, DT[dtype])
+    tm = Mat(rng.normal(size=(n, K)) * 3, DT[dtype])
+    idt = ids_tensor(ids, "i64")
+    wt = torch.as_tensor(rng.normal(size=n), dtype=torch.float32, device="cuda")
+    w, scale = wt.cpu().double().numpy(), 0.75
+    loss, lse = torch.full((n,), 9.0, device="cuda"), torch.full((n,), 9.0, device="cuda")
+    out = Mat(np.full((n, vocab), 3.0), DT[dtype])
+    head = (code(Z, dtype), n, vocab, x.stride, tm.ptr, code(Z, dtype), idt.data_ptr(), Z.I64, K, K, scale)
+    rl, rdx, rlse, mag = V.distill(x.host(), tm.host(), ids, scale, w)
+    st, qe = sum_tol(vocab), U * (2 * K + 32)
+    with np.errstate(invalid="ignore"):
+        logp, _ = V._log_softmax(x.host() * scale)
+    d, p = np.where(np.isfinite(logp), np.abs(logp), 0), np.exp(logp)
+    q = np.zeros_like(p)
+    qk = V.teacher_probabilities(tm.host(), ids, scale, vocab)[0]
+    for i in range(n):
+        np.add.at(q[i], np.where(ids[i] >= 0, ids[i], 0), qk[i])
+    big = np.where(np.isfinite(rlse), np.abs(rlse), 0)
+    ltol = (qe + st) * (mag + 1 / scale ** 2) + 16 * U * mag + 1e-30
+    wa = np.abs(w / scale)[:, None]
+    gtol = wa * (p * (2 * st + U * (16 + 6 * d)) + 2 * q * qe) + rounding(dtype, rdx) + 1e-37
+    alone = gtol + wa * p * (st + 4 * U * (1 + big))[:, None]
+
+    Z.zero3_distill_loss(x.ptr, *head, wt.data_ptr(), loss.data_ptr(), lse.data_ptr(), out.ptr, vocab,
+                         stream())
+    close(loss.cpu(), rl, ltol)
+    close(lse.cpu(), rlse, st + 2 * U * (1 + big))
+    close(out.host(), rdx, gtol)
+    both = out.t.clone()
+    out.t.fill_(4.0)
+    Z.zero3_distill_backward(x.ptr, *head, lse.data_ptr(), wt.data_ptr(), out.ptr, vocab, stream())
+    close(out.host(), rdx, alone)
+    grad, keep = out.t.clone(), x.t.clone()
+    Z.zero3_distill_backward(x.ptr, *head, lse.data_ptr(), wt.data_ptr(), x.ptr, vocab, stream())
+    assert torch.equal(x.t, grad)
+    x.t.copy_(keep)
+    Z.zero3_distill_loss(x.ptr, *head, wt.data_ptr(), loss.data_ptr(), lse.data_ptr(), x.ptr, vocab,
+                         stream())
+    assert torch.equal(x.t, both)
+    assert x.intact() and out.intact() and tm.intact()
+    quiet = (kind == 2) | (kind == 3)
+    assert not both[quiet].any() and not grad[quiet].any() and not loss[quiet].any()

@@ -9,7 +9,9 @@
 // the teacher's list meanwhile: a list costs several dependent loads (token,
 // then the student's logit there) and a softmax of its own.  The gradient's
 // elements at the teacher's tokens are written by the list's warp, after the
-// streaming threads' stores.
+// streaming threads' stores.  Both roles meet at the same barrier statements: a
+// role's work stands between them, no barrier inside a branch that only one role
+// takes.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
     wait_prior_grids();
     allow_next_grid();
     const int tid = threadIdx.x;
+    const bool lister = tid >= NT;  // the list's warp
     const int C = a.cluster;
     if (LOSS && C > 1) cluster_arrive();
     const int64_t r = blockIdx.x / C;
@@ -357,88 +360,88 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
     const RowPart<T> p(a, r, part);
     T* const out = static_cast<T*>(a.dx) + r * a.dx_stride;
     const int32_t last = p.start + 8 * p.n;
-    Sweep w;
-    w.scale = a.scale;
-    if (tid >= NT) {  // the list's warp
-        const int lane = tid - NT;
-        const Teacher t(dyn + RowRing<T, NT>::kBytes / 16, a);
-        // the loss wants the logits at all tokens, from its first part
-        const bool all = LOSS && part == 0;
-        const ListKind kind = list_entries(a, r, t);
-        if (lane == 0) sh_kind = kind;
-        // the others' writes wait for the logits only where they overwrite them
-        const bool in_place = a.dx == a.x;
-        if (!LOSS && !in_place) __syncthreads();
-        list_logits<T>(a, p.row, all ? 0 : p.lo, all ? a.vocab : p.hi, t);
-        if (!LOSS && in_place) __syncthreads();
-        const ListSums l = list_softmax(a, t);
-        if (list_repeats(a, t, p.lo, p.hi)) list_merge(a.k, t);
-        if (LOSS) __syncthreads();
-        Soft q = soft_empty();
-        if (LOSS) {
-            q = soft_all<NT / 32>(sh, sh_parts, C, part);
-            if (part == 0 && lane == 0) write_loss(a, r, q, l, kind, q.s == 0.0f ? 0.0f : logf(q.s));
-        }
-        const float lse = LOSS ? 0.0f : a.lse[r];
-        if (kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf())) return;
-        w.base = LOSS ? q.mz : lse;
-        w.c = row_coef(a, r);
-        w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
-        if (kind == kListNan) w.coef = __int_as_float(0x7fffffff);
-        __syncthreads();  // the others have written
-        write_teacher<T>(a, t, out, p.lo, p.hi, w, lane, 32);
-        return;
-    }
-    const RowRing<T, NT> ring(dyn, p.row + p.start, p.n, tid, LOSS ? 2 : 1);
-    ring.send(0);
-    ring.send(1);
-    const int32_t edge = edge_element(p.lo, p.start, last, p.hi);
+    // (the gradient alone waits for these next to the list's entries)
+    const float lse = LOSS ? 0.0f : a.lse[r], coef = LOSS ? 0.0f : row_coef(a, r);
+    const Teacher t(dyn + RowRing<T, NT>::kBytes / 16, a);
+    const RowRing<T, NT> ring(dyn, p.row + p.start, p.n, tid, LOSS ? 2 : 1);  // not the list's warp's
+    // The others' writes wait for the list's logits only where they overwrite
+    // them; the loss wants the logits at all tokens, from its first part.
+    const bool early = LOSS || a.dx == a.x;
+    const bool all = LOSS && part == 0;
+    int32_t edge = -1;
     T edge_x = from_f32<T>(0.0f);
-    if (edge >= 0) edge_x = p.row[edge];
+    ListSums l{0.0f, 0.0f};
     Soft q = soft_empty();
-    if (LOSS) {
-        if (edge >= 0) soft_element<T, false>(q, edge_x, a.scale);
-        soft_ring<T, false, NT>(q, ring, a.scale);
-        soft_lanes<false, 32>(q);
-        if ((tid & 31) == 0) sh[tid >> 5] = q;
+    if (lister) {
+        const ListKind kind = list_entries(a, r, t);
+        if (tid == NT) sh_kind = kind;
+        if (early) list_logits<T>(a, p.row, all ? 0 : p.lo, all ? a.vocab : p.hi, t);
+        if (LOSS) {
+            l = list_softmax(a, t);
+            if (list_repeats(a, t, p.lo, p.hi)) list_merge(a.k, t);
+        }
+    } else {
+        ring.send(0);
+        ring.send(1);
+        edge = edge_element(p.lo, p.start, last, p.hi);
+        if (edge >= 0) edge_x = p.row[edge];
+        if (LOSS) {
+            if (edge >= 0) soft_element<T, false>(q, edge_x, a.scale);
+            soft_ring<T, false, NT>(q, ring, a.scale);
+            soft_lanes<false, 32>(q);
+            if ((tid & 31) == 0) sh[tid >> 5] = q;
+        }
     }
     __syncthreads();
-    if (LOSS) q = soft_all<NT / 32>(sh, sh_parts, C, part);
-    const float lse = LOSS ? 0.0f : a.lse[r];
     const ListKind kind = sh_kind;
-    const bool dead = kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf());
-    w.base = LOSS ? q.mz : lse;
-    w.c = row_coef(a, r);
-    w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
-    if (kind == kListNan) w.coef = __int_as_float(0x7fffffff);
+    if (LOSS) {
+        q = soft_all<NT / 32>(sh, sh_parts, C, part);
+        if (part == 0 && tid == NT) write_loss(a, r, q, l, kind, q.s == 0.0f ? 0.0f : logf(q.s));
+    }
     T* to = out + p.start + 8 * tid;
-    if (dead) {
+    if (kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf())) {  // the same in every thread
+        if (lister) return;
         const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         drain_copies();
         for (int32_t c = tid; c < p.n; c += NT, to += 8 * NT) Chunk<T>::store(to, zero);
         if (edge >= 0) out[edge] = from_f32<T>(0.0f);
         return;
     }
-    const int b0 = LOSS ? ring.per : 0;
+    Sweep w;
+    w.scale = a.scale;
+    w.base = LOSS ? q.mz : lse;
+    w.c = LOSS ? row_coef(a, r) : coef;
+    w.coef = LOSS ? __fdiv_rn(w.c, q.s) : w.c;
+    if (kind == kListNan) w.coef = __int_as_float(0x7fffffff);
+    if (lister) {
+        if (!LOSS) {
+            if (!early) list_logits<T>(a, p.row, p.lo, p.hi, t);
+            list_softmax(a, t);
+            if (list_repeats(a, t, p.lo, p.hi)) list_merge(a.k, t);
+        }
+    } else {
+        const int b0 = LOSS ? ring.per : 0;
 #pragma unroll 1
-    for (int b = 0; b < ring.full; ++b, to += 8 * U * NT) {
-        Chunk<T> c[U];
-        ring.take(b0 + b, c);
-        ring.send(b0 + b + 2);
+        for (int b = 0; b < ring.full; ++b, to += 8 * U * NT) {
+            Chunk<T> c[U];
+            ring.take(b0 + b, c);
+            ring.send(b0 + b + 2);
 #pragma unroll
-        for (int u = 0; u < U; ++u) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
-    }
-    if (ring.full < ring.per) {
-        Chunk<T> c[U];
-        ring.take(b0 + ring.full, c);
-        ring.send(b0 + ring.full + 2);
+            for (int u = 0; u < U; ++u) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
+        }
+        if (ring.full < ring.per) {
+            Chunk<T> c[U];
+            ring.take(b0 + ring.full, c);
+            ring.send(b0 + ring.full + 2);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (ring.has(u)) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
+            for (int u = 0; u < U; ++u)
+                if (ring.has(u)) sweep_chunk<T>(c[u], to + 8 * NT * u, w);
+        }
+        if (edge >= 0) out[edge] = from_f32<T>(sweep_value(to_f32(edge_x), w));
+        drain_copies();
     }
-    if (edge >= 0) out[edge] = from_f32<T>(sweep_value(to_f32(edge_x), w));
-    drain_copies();
-    __syncthreads();
+    __syncthreads();  // the others have written, before the list's warp does
+    if (lister) write_teacher<T>(a, t, out, p.lo, p.hi, w, tid - NT, 32);
 }
 
 // The loss alone, and the gradient of rows that are not as far from a 16-byte
