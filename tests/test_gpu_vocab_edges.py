@@ -83,3 +83,28 @@ def test_distill_rows_of_every_kind_side_by_side(Z, n, vocab, K, dtype):
     assert x.intact() and out.intact() and tm.intact()
     quiet = (kind == 2) | (kind == 3)
     assert not both[quiet].any() and not grad[quiet].any() and not loss[quiet].any()
+
+
+@pytest.mark.parametrize("accumulate,tail", [(False, 0), (True, 100)])
+@pytest.mark.parametrize("dim", [1, 8])
+def test_embedding_backward_largest_batch(Z, dim, accumulate, tail):
+    """2^31 - 1 positions, all of one token but the last `tail`, of another: the
+    indices of the last pieces, and the counts, lie next to 2^31.  Every sum of
+    ones is exact: pieces hold 128 rows, and a multiple of 128 below 2^31
+    has 24 bits."""
+    n = 2 ** 31 - 1
+    ids = torch.zeros(n, device="cuda", dtype=torch.int32)
+    if tail:
+        ids[-tail:] = 1
+    dout = torch.ones(n, dim, device="cuda", dtype=torch.bfloat16)
+    grad = torch.full((3, dim), 0.5, device="cuda")
+    nb = Z.zero3_embedding_workspace(n, 3, dim)
+    ws = torch.empty(nb, device="cuda", dtype=torch.uint8)
+    Z.zero3_embedding_backward(dout.data_ptr(), Z.BF16, dim, ids.data_ptr(), Z.I32, n, 1.0,
+                               int(accumulate), grad.data_ptr(), Z.F32, 3, dim, dim, ws.data_ptr(), nb,
+                               stream())
+    base = 0.5 if accumulate else 0.0
+    want = np.float32([n - tail + base, tail + base if tail else 0.0, base])
+    assert np.array_equal(grad.cpu().numpy(), np.repeat(want[:, None], dim, 1))
+    del ids, dout, ws
+    torch.cuda.empty_cache()

@@ -552,16 +552,17 @@ __device__ __forceinline__ void join(const SumArgs& p, int32_t v, int32_t first,
         if (VEC && ACC && at < dim) old.load_stream(g + at);
         uint64_t acc[4] = {0, 0, 0, 0};
         constexpr int R = 8;
-        for (int32_t b = 0; b < count; b += R * step) {
+        // unsigned: steps past a count near 2^31 do not wrap
+        for (uint32_t b = 0; b < static_cast<uint32_t>(count); b += R * step) {
             Chunk<float> x[R];
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (b + r * step < count)
-                    load_part(x[r], p.w.partial + piece_slot(first + b + r * step, b + r == 0) * p.w.step,
-                              at, dim);
+                if (b + r * step < static_cast<uint32_t>(count))
+                    load_part(x[r], p.w.partial + piece_slot(first + static_cast<int32_t>(b + r * step),
+                                                             b + r == 0) * p.w.step, at, dim);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (b + r * step >= count) break;
+                if (b + r * step >= static_cast<uint32_t>(count)) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[k] = add2(acc[k], x[r].pair(k));
             }
@@ -594,12 +595,15 @@ __device__ __forceinline__ bool find_pieces(const SumArgs& p, int64_t tile, int 
     if (j + lane < p.a.n)  // stale beyond the count, which arrives with it
         *reinterpret_cast<int4*>(&q.x) = *reinterpret_cast<const int4*>(p.w.sorted + j + lane);
     q.count = p.w.off[p.deal.own << p.deal.shift];  // ignored positions are not sorted
-    const int32_t size = piece_rows(q.x.count), at = q.j0 + lane;
-    q.starts = __ballot_sync(0xffffffffu, lane < p.rows && at < q.count &&
-                                              ((at - q.x.first) & (size - 1)) == 0);
+    // where in its token's positions the lane's lies (from j0 on, because j0 + 32
+    // may pass 2^31)
+    const uint32_t size = piece_rows(q.x.count);
+    const uint32_t into = static_cast<uint32_t>(q.j0) + lane - static_cast<uint32_t>(q.x.first);
+    q.starts = __ballot_sync(0xffffffffu, lane < p.rows && lane < q.count - q.j0 &&
+                                              (into & (size - 1)) == 0);
     if (!q.starts) return false;
     q.a = __ffs(q.starts) - 1;
-    const int32_t end = min(at + size, q.x.first + q.x.count) - q.j0;
+    const int32_t end = lane + static_cast<int32_t>(min(size, static_cast<uint32_t>(q.x.count) - into));
     q.e = __shfl_sync(0xffffffffu, end, 31 - __clz(q.starts));
     return true;
 }
@@ -627,11 +631,10 @@ __device__ __forceinline__ bool end_piece(const SumArgs& p, const Pieces& q, int
             store_part(to, column(c0, lane, u), static_cast<int32_t>(p.a.dim), acc[u]);
         __threadfence();
         __syncwarp();
-        const int32_t step = piece_rows(n);
         int all = 0;
         if (lane == 0)
             all = atomicAdd(p.w.arrived + static_cast<int64_t>(first / kPiece) * p.slabs + slab, 1) ==
-                  (n + step - 1) / step - 1;
+                  (n - 1) / piece_rows(n);
         done = __shfl_sync(0xffffffffu, all, 0);
     }
 #pragma unroll
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
                  PG, sizeof(TG), slot);
         } else if (next < q.e) {
             if (next >= 32 && (next & 31) == 0)
-                pos = q.j0 + next + lane < q.count ? p.w.sorted[q.j0 + next + lane].pos : 0;
+                pos = next + lane < q.count - q.j0 ? (p.w.sorted + q.j0)[next + lane].pos : 0;
             copy(static_cast<const TD*>(p.a.dout) +
                      __shfl_sync(0xffffffffu, pos, next & 31) * p.a.dout_stride,
                  PD, sizeof(TD), slot);
@@ -797,7 +800,7 @@ __global__ void __launch_bounds__(kSumThreads)
     const auto issue = [&] {
         if (next < q.e) {
             if (next >= 32 && (next & 31) == 0)
-                pos = q.j0 + next + lane < q.count ? p.w.sorted[q.j0 + next + lane].pos : 0;
+                pos = next + lane < q.count - q.j0 ? (p.w.sorted + q.j0)[next + lane].pos : 0;
             const TD* row = dout + __shfl_sync(0xffffffffu, pos, next & 31) * p.a.dout_stride + c0;
             const int skip = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(TD));
             if (lane == 0) starts[warp][slot] = skip;
