@@ -605,8 +605,9 @@ zero3_status zero3_token_logprobs(const void* logits, zero3_dtype dtype, int64_t
 /* Gradient of the above: with g = dlogprob[row] (0 where the target is
  * ignored), h = dentropy[row], p = exp(z - lse):
  *   dlogits_j = inv_temperature * ([j = target] g - p_j (g + h (log p_j + entropy)))
- * and zero in a row without any token (lse = -inf).  lse and entropy are
- * what the forward call wrote.  Either of dlogprob and dentropy may be NULL
+ * and zero in a row without any token (lse = -inf), and where p_j is 0 unless
+ * j is the target (|dentropy| * inv_temperature up to 2^120; beyond it products
+ * overflow binary32).  lse and entropy are what the forward call wrote.  Either of dlogprob and dentropy may be NULL
  * (no such gradient), entropy too if dentropy is.  dlogits has the logits'
  * dtype and may be the logits themselves (same pointer and stride). */
 zero3_status zero3_token_logprobs_backward(const void* logits, zero3_dtype dtype, int64_t n,

@@ -8,8 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import vocab_oracle as V  # noqa: E402
-from test_gpu_vocab import (DT, U, Mat, close, code, ids_tensor, logits, rounding,  # noqa: E402
-                            stream, sum_tol)
+from test_gpu_vocab import (DT, U, Mat, close, code, grad_tol, ids_tensor, logits,  # noqa: E402
+                            rounding, stream, sum_tol)
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,42 @@ def test_embedding_backward_largest_batch(Z, dim, accumulate, tail):
     assert np.array_equal(grad.cpu().numpy(), np.repeat(want[:, None], dim, 1))
     del ids, dout, ws
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("weight", [1e6, -1e9, 1e20, -1e36])
+@pytest.mark.parametrize("vocab,pad", [(40, 0), (1001, 0), (1001, 1), (9001, 0)])
+def test_entropy_gradient_of_large_weights(Z, dtype, weight, vocab, pad):
+    """Masked tokens have no gradient however large the entropy's weight is, by the
+    wide path and by single elements."""
+    n, scale = 5, 0.75
+    rng = np.random.default_rng(vocab)
+    xs = logits(rng, n, vocab, "masked")
+    xs[2, 1::2] = -3.3895313892515355e38  # finite, and without weight all the same
+    x, t = Mat(xs, DT[dtype], vocab + pad), rng.integers(0, vocab, n)
+    it = ids_tensor(t, "i64")
+    lp, lse, ent = (torch.empty(n, device="cuda") for _ in range(3))
+    Z.zero3_token_logprobs(x.ptr, code(Z, dtype), n, vocab, x.stride, it.data_ptr(), Z.I64, scale, 0,
+                           lp.data_ptr(), lse.data_ptr(), ent.data_ptr(), stream=stream())
+    g = torch.as_tensor(rng.normal(size=n), dtype=torch.float32, device="cuda")
+    h = torch.as_tensor(rng.uniform(0.5, 1, size=n) * weight, dtype=torch.float32, device="cuda")
+    dx = Mat(np.full((n, vocab), 3.0), DT[dtype])
+    Z.zero3_token_logprobs_backward(x.ptr, code(Z, dtype), n, vocab, x.stride, it.data_ptr(), Z.I64,
+                                    scale, lse.data_ptr(), ent.data_ptr(), g.data_ptr(), h.data_ptr(),
+                                    dx.ptr, dx.stride, stream())
+    g, h = g.cpu().double().numpy(), h.cpu().double().numpy()
+    want = V.token_logprobs_backward(x.host(), t, scale, g, h)
+    ref = V.token_logprobs(x.host(), t, scale)
+    with np.errstate(invalid="ignore"):
+        logp, _ = V._log_softmax(V.scaled(x.host(), scale))
+    p, H = np.exp(logp), ref["entropy"]
+    eps = sum_tol(vocab) + 2 * U * (1 + np.where(np.isfinite(ref["lse"]), np.abs(ref["lse"]), 0))
+    size = np.where(p > 0, np.abs(np.where(p > 0, logp, 0)), 0)
+    w = np.abs(g)[:, None] + np.abs(h)[:, None] * (size + H[:, None] + 1)
+    tol = grad_tol(dtype, want, p, np.where(p > 0, logp, 0), g, h, H, scale) + \
+        scale * p * w * (4 + H[:, None]) * eps[:, None]
+    close(dx.host(), want, tol)
+    masked = p == 0
+    masked[np.arange(n), t] = False
+    assert not dx.host()[masked].any()
+    assert x.intact() and dx.intact()

@@ -383,7 +383,7 @@ __device__ __forceinline__ float grad_value(float x, const GradRow& g) {
     const float d = fmaf(x, g.scale, g.neg_lse);
     const float p = exp2_approx(__fmul_rn(d, kLog2e));
     if (!ENT) return __fmul_rn(p, g.c0);
-    return __fmul_rn(p, fmaf(max_nan(d, -1e30f), g.c1, g.c0));
+    return __fmul_rn(p, fmaf(max_nan(d, kNoWeight), g.c1, g.c0));
 }
 
 template <typename T, bool ENT>
@@ -400,7 +400,7 @@ __device__ __forceinline__ void grad_chunk(const Chunk<T>& c, T* out, int32_t at
         uint64_t w = c0;
         if (ENT) {  // d = -inf has weight 0: keep 0 * d finite
             upk2(d, t0, t1);
-            w = fma2(pk2(max_nan(t0, -1e30f), max_nan(t1, -1e30f)), c1, c0);
+            w = fma2(pk2(max_nan(t0, kNoWeight), max_nan(t1, kNoWeight)), c1, c0);
         }
         upk2(mul2(p, w), f[2 * k], f[2 * k + 1]);
     }

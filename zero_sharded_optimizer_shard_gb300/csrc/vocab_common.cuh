@@ -24,6 +24,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A logarithm of a weight that exp2_approx (of it, or of it times log2 e) has
+// turned into 0: what is below, -inf above all, is raised to this, so that the
+// product of the two is 0.  (Small, so that times a weight of up to 2^120 it stays
+// finite.)
+constexpr float kNoWeight = -128.0f;
 // max that keeps a NaN (fmaxf drops it).
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
@@ -188,7 +193,7 @@ __device__ __forceinline__ void soft_add(Soft& q, const Chunk<T> (&c)[U], float 
         if (q.s != 0.0f) {
             const float dt = __fmul_rn(__fsub_rn(q.mz, nzf), kLog2e);
             const float f = exp2_approx(dt);
-            if (ENT) q.a = __fmul_rn(f, fmaf(q.s, max_nan(dt, -1e30f), q.a));
+            if (ENT) q.a = __fmul_rn(f, fmaf(q.s, max_nan(dt, kNoWeight), q.a));
             q.s = __fmul_rn(q.s, f);
         }
         q.m = bm;
@@ -204,8 +209,8 @@ __device__ __forceinline__ void soft_add(Soft& q, const Chunk<T> (&c)[U], float 
             float t0, t1;
             upk2(t, t0, t1);
             if (ENT) {  // t = -inf has weight 0: keep 0 * t finite
-                t0 = max_nan(t0, -1e30f);
-                t1 = max_nan(t1, -1e30f);
+                t0 = max_nan(t0, kNoWeight);
+                t1 = max_nan(t1, kNoWeight);
                 t = pk2(t0, t1);
             }
             const uint64_t e = pk2(exp2_approx(t0), exp2_approx(t1));
@@ -233,7 +238,7 @@ __device__ __forceinline__ void soft_rebase(Soft& q, float to) {
     if (q.s != 0.0f) {
         const float dt = __fmul_rn(__fsub_rn(q.mz, to), kLog2e);
         const float f = exp2_approx(dt);
-        if (ENT) q.a = __fmul_rn(f, fmaf(q.s, max_nan(dt, -1e30f), q.a));
+        if (ENT) q.a = __fmul_rn(f, fmaf(q.s, max_nan(dt, kNoWeight), q.a));
         q.s = __fmul_rn(q.s, f);
     }
     q.mz = to;
