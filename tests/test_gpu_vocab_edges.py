@@ -2,6 +2,8 @@
 every kind side by side, lists that overflow, sizes at the limits.  Tolerances
 as in test_gpu_vocab.py, from binary32 arithmetic.
 """
+import ctypes as C
+
 import numpy as np
 import pytest
 
@@ -147,3 +149,51 @@ def test_entropy_gradient_of_large_weights(Z, dtype, weight, vocab, pad):
     masked[np.arange(n), t] = False
     assert not dx.host()[masked].any()
     assert x.intact() and dx.intact()
+
+
+def test_an_earlier_calls_error_is_not_this_calls(Z):
+    """A synchronisation refused because its stream is being captured leaves an error
+    code behind in the runtime; the launches after it succeed and do their work."""
+    from examples.tied_lm import TiedLM
+    lm = TiedLM(vocab=64, dim=16, hidden=16)
+    table = torch.randn(8, 16, device="cuda")
+    ids = torch.arange(8, device="cuda").flip(0)
+    out, grad = torch.zeros(8, 16, device="cuda"), torch.zeros(8, 16, device="cuda")
+    ws = torch.empty(Z.zero3_embedding_workspace(8, 8, 16), device="cuda", dtype=torch.uint8)
+    x, lp, loss = torch.randn(8, 8, device="cuda"), torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")
+    tl, full, s = torch.zeros(8, 1, device="cuda"), torch.zeros_like(lm.full), stream()
+    torch.cuda.synchronize()
+    rt = C.CDLL("libcudart.so.%s" % torch.version.cuda.split(".")[0])
+
+    def refused():
+        st, graph = C.c_void_p(), C.c_void_p()
+        assert rt.cudaStreamCreate(C.byref(st)) == 0
+        assert rt.cudaStreamBeginCapture(st, 2) == 0
+        assert Z.raw_status("zero3_sync", st) == Z.ECUDA
+        assert rt.cudaStreamEndCapture(st, C.byref(graph)) != 0 and not graph.value
+        assert rt.cudaStreamDestroy(st) == 0
+        rt.cudaGetLastError()  # the caller's own runtime is clean
+
+    refused()
+    Z.zero3_embedding_forward(table.data_ptr(), Z.F32, 8, 16, 16, ids.data_ptr(), Z.I64, 8, 1.0,
+                              out.data_ptr(), Z.F32, 16, s)
+    refused()
+    Z.zero3_embedding_backward(table.data_ptr(), Z.F32, 16, ids.data_ptr(), Z.I64, 8, 1.0, 0,
+                               grad.data_ptr(), Z.F32, 8, 16, 16, ws.data_ptr(), ws.numel(), s)
+    refused()
+    Z.zero3_token_logprobs(x.data_ptr(), Z.F32, 8, 8, 8, ids.data_ptr(), Z.I64, 1.0, 0, lp.data_ptr(),
+                           stream=s)
+    refused()
+    Z.zero3_distill_loss(x.data_ptr(), Z.F32, 8, 8, 8, tl.data_ptr(), Z.F32, ids.data_ptr(), Z.I64, 1, 1,
+                         1.0, None, loss.data_ptr(), stream=s)
+    refused()  # the library's other launches
+    Z.zero3_cast_params(lm.plan, lm._ptrs(lm.master), lm._ptrs(lm.sparam), full.data_ptr(), None, 0,
+                        lm.plan.info.psi_pad, s)
+    refused()
+    wte = lm.gather()[0]
+    torch.cuda.synchronize()
+    assert torch.equal(out, table[ids]) and torch.equal(grad, out)
+    assert torch.equal(full, lm.full) and torch.equal(wte.flatten(), full[:64 * 16])
+    want = torch.log_softmax(x, 1)[torch.arange(8), ids]
+    assert torch.allclose(lp, want, atol=1e-5) and torch.allclose(loss, -want, atol=1e-5)
+    lm.release()

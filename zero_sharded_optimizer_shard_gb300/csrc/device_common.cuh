@@ -64,7 +64,9 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                       pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// Launch with programmatic stream serialization (see wait_prior_grids).
+// Launch with programmatic stream serialization (see wait_prior_grids).  What the
+// launch itself returned is the call's result; the thread's last error may be an
+// earlier call's.
 template <typename Args>
 cudaError_t launch_programmatic(void (*kernel)(Args), int grid, const Args& a,
                                 cudaStream_t stream) {

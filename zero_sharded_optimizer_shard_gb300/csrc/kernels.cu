@@ -476,8 +476,7 @@ template <int MODE, int ND, int GT>
 cudaError_t launch_one(const StreamArgs& a, cudaStream_t stream) {
     const int grid = grid_for(a.total_chunks);
     if (grid <= 0) return cudaSuccess;
-    const cudaError_t e = launch_programmatic(stream_kernel<MODE, ND, GT>, grid, a, stream);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_programmatic(stream_kernel<MODE, ND, GT>, grid, a, stream);
 }
 
 template <int MODE, int GT>

@@ -379,10 +379,8 @@ cudaError_t launch_pieces(const PieceArgs<MAXP>& a, cudaStream_t stream) {
     const int grid = static_cast<int>((warps + kThreads / 32 - 1) / (kThreads / 32));
     bool phased = false;
     for (int i = 0; i < a.n; ++i) phased = phased || a.piece[i].ph != 0;
-    const cudaError_t e =
-        phased ? launch_programmatic(piece_kernel<KIND, true, MAXP>, grid, a, stream)
-               : launch_programmatic(piece_kernel<KIND, false, MAXP>, grid, a, stream);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return phased ? launch_programmatic(piece_kernel<KIND, true, MAXP>, grid, a, stream)
+                  : launch_programmatic(piece_kernel<KIND, false, MAXP>, grid, a, stream);
 }
 
 template <int MAXP>

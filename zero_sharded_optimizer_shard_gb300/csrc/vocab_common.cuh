@@ -458,7 +458,8 @@ __device__ __forceinline__ Soft soft_parts(const Soft* parts, int C) {
 }
 
 // Launch with programmatic stream serialization (see wait_prior_grids), with
-// `cluster` blocks per cluster.
+// `cluster` blocks per cluster.  Returns what the launch itself returned: the
+// thread's last error may be an earlier call's, which is not this one's failure.
 template <typename Args>
 cudaError_t launch_vocab(void (*kernel)(Args), int64_t grid, int threads, int smem, int cluster,
                          const Args& a, cudaStream_t stream) {
@@ -476,8 +477,7 @@ cudaError_t launch_vocab(void (*kernel)(Args), int64_t grid, int threads, int sm
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
