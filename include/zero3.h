@@ -626,9 +626,11 @@ zero3_status zero3_token_logprobs_backward(const void* logits, zero3_dtype dtype
  *   log p = log softmax over the vocabulary of a * logits
  *   loss = (sum q_k (log q_k - log p[id_k])) / a^2
  * A token listed more than once has the sum of its entries' q.  A row without
- * a counting entry, or without any student token (all -inf), has loss 0 and a
- * zero gradient; a NaN makes its row's loss and gradient NaN.  lse (optional)
- * is the student's log-sum-exp for zero3_distill_backward.
+ * a counting entry has loss 0 and a zero gradient.  In other rows a NaN or +inf
+ * among the entries that count makes loss and gradient NaN; without any student
+ * token (all -inf) they are 0; a NaN or +inf among the logits makes them NaN (the
+ * first of these that holds).  lse (optional) is the student's log-sum-exp for
+ * zero3_distill_backward.
  * With dlogits (optional) the gradient of sum_i row_weight[i] * loss[i] is
  * written by the same call, from one read of the logits:
  *   dlogits_j = row_weight (p_j - sum of q_k over id_k = j) / a;

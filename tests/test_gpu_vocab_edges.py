@@ -197,3 +197,47 @@ def test_an_earlier_calls_error_is_not_this_calls(Z):
     want = torch.log_softmax(x, 1)[torch.arange(8), ids]
     assert torch.allclose(lp, want, atol=1e-5) and torch.allclose(loss, -want, atol=1e-5)
     lm.release()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,vocab,pad", [(5, 300, 0), (5, 300, 1), (7, 9001, 0), (170, 50001, 0), (5, 50001, 3)])
+def test_distill_not_finite_rows(Z, dtype, n, vocab, pad):
+    """Which of an empty list, a list that is not finite, a row without any student
+    token and logits that are not finite decides: the loss and every form of
+    the gradient agree."""
+    K, rng = 6, np.random.default_rng(vocab)
+    xs, ts = rng.normal(size=(n, vocab)), rng.normal(size=(n, K))
+    ids = np.stack([rng.choice(vocab, K, replace=False) for _ in range(n)])
+    xs[0], ts[0, 3] = -np.inf, np.nan  # a NaN in the list, no student token
+    xs[1], ts[1, 0] = -np.inf, np.inf
+    xs[2, vocab // 2], ids[2] = np.nan, -1  # a NaN in the logits, no entry
+    xs[3, vocab - 1] = np.inf
+    ts[4, 1], ids[4, 1] = np.nan, vocab  # an entry that does not count
+    x, tm, it = Mat(xs, DT[dtype], vocab + pad), Mat(ts, DT[dtype]), ids_tensor(ids, "i32")
+    loss, lse = torch.full((n,), 9.0, device="cuda"), torch.full((n,), 9.0, device="cuda")
+    head = (code(Z, dtype), n, vocab, x.stride, tm.ptr, code(Z, dtype), it.data_ptr(), Z.I32, K, K, 1.0)
+    dx = Mat(np.full((n, vocab), 3.0), DT[dtype])
+
+    def check():
+        bad = torch.isnan(dx.t)
+        assert bad[[0, 1, 3]].all() and not bad[[2, 4]].any() and not bad[5:].any()
+        assert not dx.t[2].any() and dx.t[4].any()
+        assert x.intact() and dx.intact()
+        dx.t.fill_(4.0)
+    Z.zero3_distill_loss(x.ptr, *head, None, loss.data_ptr(), lse.data_ptr(), dx.ptr, dx.stride, stream())
+    check()
+    assert torch.isnan(loss[[0, 1, 3]]).all() and loss[2] == 0 and torch.isfinite(loss[4:]).all()
+    assert torch.isneginf(lse[:2]).all() and torch.isnan(lse[2:4]).all()
+    Z.zero3_distill_backward(x.ptr, *head, lse.data_ptr(), None, dx.ptr, dx.stride, stream())
+    check()
+    alone = torch.full((n,), 9.0, device="cuda")
+    Z.zero3_distill_loss(x.ptr, *head, None, alone.data_ptr(), None, None, 0, stream())
+    assert torch.isnan(alone[[0, 1, 3]]).all() and alone[2] == 0
+    keep = x.t.clone()
+    Z.zero3_distill_backward(x.ptr, *head, lse.data_ptr(), None, x.ptr, x.stride, stream())
+    dx.t.copy_(x.t)
+    check()
+    x.t.copy_(keep)
+    Z.zero3_distill_loss(x.ptr, *head, None, loss.data_ptr(), None, x.ptr, x.stride, stream())
+    dx.t.copy_(x.t)
+    check()

@@ -276,6 +276,12 @@ __device__ __forceinline__ void write_teacher(const DistillArgs& a, const Teache
     }
 }
 
+// Whether a row's gradient is zero: no entry counts, or no student token is left
+// (none).  A list with a NaN makes it NaN, as it does the loss.
+__device__ __forceinline__ bool no_gradient(ListKind kind, bool none) {
+    return kind == kListEmpty || (kind == kListPlain && none);
+}
+
 __device__ __forceinline__ float row_coef(const DistillArgs& a, int64_t r) {
     const float w = a.weight ? a.weight[r] : 1.0f;
     return __fdiv_rn(w, a.scale);
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
         if (part == 0 && tid == NT) write_loss(a, r, q, l, kind, q.s == 0.0f ? 0.0f : logf(q.s));
     }
     T* to = out + p.start + 8 * tid;
-    if (kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf())) {  // the same in every thread
+    if (no_gradient(kind, LOSS ? q.s == 0.0f : lse == neg_inf())) {  // the same in every thread
         if (lister) return;
         const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         drain_copies();
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_con
     if (!GRAD) return;
     T* out = static_cast<T*>(a.dx) + r * a.dx_stride;
     const float lse = LOSS ? 0.0f : a.lse[r];
-    if (sh_kind == kListEmpty || (LOSS ? q.s == 0.0f : lse == neg_inf())) {
+    if (no_gradient(sh_kind, LOSS ? q.s == 0.0f : lse == neg_inf())) {
         for (int32_t i = p.lo + tid; i < p.hi; i += NT + 32) out[i] = from_f32<T>(0.0f);
         return;
     }
