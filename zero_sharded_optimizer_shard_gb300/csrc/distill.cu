@@ -451,8 +451,9 @@ __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant_
 }
 
 // The loss alone, and the gradient of rows that are not as far from a 16-byte
-// boundary as the gradient's rows: one row per cluster of a.cluster blocks,
-// the gradient written by single elements.  Loss of 2047 rows of 32000 binary32,
+// boundary as the gradient's rows (never in place: equal rows are equally far):
+// one row per cluster of a.cluster blocks, the gradient written by single
+// elements.  Loss of 2047 rows of 32000 binary32,
 // 32 entries: 40 us (6.5 TB/s).
 template <typename T, Make M, int NT, int U>
 __global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_constant__ DistillArgs a) {
@@ -493,10 +494,7 @@ __global__ void __launch_bounds__(NT + 32) distill_plain_kernel(const __grid_con
     }
     __syncthreads();
     Soft q = soft_empty();
-    if (LOSS)
-        q = soft_all<NT / 32>(sh, sh_parts, C, part);
-    else if (C > 1)
-        cluster_sync();  // in place, every part's list has read the row
+    if (LOSS) q = soft_all<NT / 32>(sh, sh_parts, C, part);
     if (LOSS && part == 0 && tid == 0)
         write_loss(a, r, q, sh_list, sh_kind, q.s == 0.0f ? 0.0f : logf(q.s));
     if (!GRAD) return;
