@@ -10,8 +10,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import vocab_oracle as V  # noqa: E402
-from test_gpu_vocab import (DT, U, Mat, close, code, grad_tol, ids_tensor, logits,  # noqa: E402
-                            rounding, stream, sum_tol)
+from test_gpu_vocab import (DT, U, Mat, close, code, grad_case, grad_tol, ids_tensor,  # noqa: E402
+                            logits, rounding, stream, sum_tol, zipf)
 
 pytestmark = pytest.mark.gpu
 
@@ -241,3 +241,58 @@ def test_distill_not_finite_rows(Z, dtype, n, vocab, pad):
     Z.zero3_distill_loss(x.ptr, *head, None, loss.data_ptr(), None, x.ptr, x.stride, stream())
     dx.t.copy_(x.t)
     check()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dim", [8, 13])
+@pytest.mark.parametrize("n,vocab,share", [(20000, 50, 1.0), (33000, 3000, 0.95), (65536, 70000, 0.9)])
+def test_embedding_backward_one_token_fills_the_batch(Z, n, vocab, share, dim, accumulate):
+    """More positions of one token (padding inside the vocabulary, say) than a sorting
+    warp lists: it reads the ids again, next to warps that need not."""
+    rng = np.random.default_rng(n)
+    ids = zipf(rng, n, vocab)
+    ids[rng.random(n) < share] = 7
+    assert (ids[: n // 32] == 7).sum() > 512
+    ids[n - n // 16:] = rng.integers(0, vocab, n // 16)  # the last warps' lists do not overflow
+    grad_case(Z, n, vocab, dim, "f32", "f32", "i64", ids, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n", [700, 3001, 9000])
+@pytest.mark.parametrize("vocab", [65536, 65537, 131073, 300007])
+def test_embedding_backward_large_vocabularies(Z, vocab, n, accumulate):
+    """128 sorting blocks, 256, 512 and 1024."""
+    rng = np.random.default_rng(vocab + n)
+    ids = np.where(rng.random(n) < 0.5, zipf(rng, n, vocab), rng.integers(vocab - 600, vocab + 2, n))
+    grad_case(Z, n, vocab, 8 if n % 2 else 11, "bf16", "f32", "i32", ids, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("gd", ["bf16", "f32"])
+@pytest.mark.parametrize("n,dim", [(8192, 2048), (8192, 2056), (7300, 2312), (32769, 512), (16400, 1024)])
+def test_embedding_backward_two_groups_per_lane(Z, n, dim, gd, accumulate):
+    """Batches of at least 2^24 elements, rows of any multiple of 8 from 2048 on: the
+    last columns' second group lies in the row, partly in it, or past its end."""
+    assert n * dim >= 1 << 24
+    grad_case(Z, n, 300, dim, "bf16", gd, "i64", zipf(np.random.default_rng(dim), n, 300), accumulate=accumulate,
+              scale=0.5)
+
+
+@pytest.mark.parametrize("dim", [1, 8])
+def test_embedding_backward_long_shares(Z, dim):
+    """A sorting warp's share of more than 65536 positions, which its list cannot
+    number."""
+    n, vocab = 32 * 65536 + 77, 1009
+    rng = np.random.default_rng(dim)
+    ids = rng.integers(-1, vocab + 1, n)
+    d = Mat(rng.normal(size=(n, dim)), torch.bfloat16)
+    grad, it = torch.full((vocab, dim), 3.0, device="cuda"), ids_tensor(ids, "i32")
+    nb = Z.zero3_embedding_workspace(n, vocab, dim)
+    ws = torch.empty(nb, device="cuda", dtype=torch.uint8)
+    Z.zero3_embedding_backward(d.ptr, Z.BF16, dim, it.data_ptr(), Z.I32, n, 0.5, 0, grad.data_ptr(), Z.F32,
+                               vocab, dim, dim, ws.data_ptr(), nb, stream())
+    keep = (ids >= 0) & (ids < vocab)
+    x, t = 0.5 * d.host()[keep], ids[keep]
+    ref = np.stack([np.bincount(t, x[:, c], vocab) for c in range(dim)], 1)
+    mag = np.stack([np.bincount(t, np.abs(x[:, c]), vocab) for c in range(dim)], 1)
+    close(grad.cpu(), ref, (np.bincount(t, minlength=vocab)[:, None] + 4) * U * mag + U * np.abs(ref))
