@@ -545,9 +545,8 @@ zero3_status zero3_merge_shards(const zero3_plan* plan, const char* const* shard
  *  - ZERO3_EINVAL, with nothing launched: unknown dtype or id type; NULL or
  *    misaligned pointer; vocab < 1 or above 2^30; a stride below the columns;
  *    n < 0 or above 2^27 rows of logits (2^31 - 1 tokens); dim above 2^27;
- *    rows times columns above 2^41, or n * ceil(vocab / 4096) above 2^31 - 1 in the calls that
- *    can write a gradient of logits; a scale that is not finite, or an
- *    inverse temperature that is not finite and positive. */
+ *    rows times columns above 2^41; a scale that is not finite, or an inverse
+ *    temperature that is not finite and positive. */
 
 typedef enum zero3_itype { ZERO3_I32 = 0, ZERO3_I64 = 1 } zero3_itype;
 

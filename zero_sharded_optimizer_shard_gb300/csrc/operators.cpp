@@ -9,7 +9,9 @@ namespace {
 constexpr int64_t kMaxVocab = int64_t{1} << 30;   // token ids and row offsets are 32-bit
 constexpr int64_t kMaxRows = int64_t{1} << 27;    // rows times blocks per row fit a grid
 constexpr int64_t kMaxDim = int64_t{1} << 27;     // embedding columns are 32-bit
-constexpr int64_t kMaxElems = int64_t{1} << 41;   // rows times columns (4 TB of bf16)
+// rows times columns (4 TB of bf16); with kMaxRows this keeps the elementwise
+// gradients' blocks, one per 4096 elements of a row, below 2^29 + 2^27
+constexpr int64_t kMaxElems = int64_t{1} << 41;
 
 zero3_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ZERO3_OK : ZERO3_ECUDA; }
 
@@ -44,9 +46,6 @@ bool embedding_ok(int64_t vocab, int64_t dim, int64_t table_stride, int64_t n, i
     return vocab >= 1 && vocab <= kMaxVocab && dim <= kMaxDim && rows_ok(vocab, dim, table_stride) &&
            rows_ok(n, dim, row_stride);
 }
-
-// Blocks of the elementwise gradients: one per 4096 elements of a row.
-bool grid_ok(int64_t n, int64_t vocab) { return n * ((vocab + 4095) / 4096) <= INT32_MAX; }
 
 }  // namespace
 
@@ -159,7 +158,7 @@ zero3_status zero3_token_logprobs_backward(const void* logits, zero3_dtype dtype
                                            void* dlogits, int64_t dlogits_stride,
                                            zero3_stream stream) {
     if (!dtype_ok(dtype) || !itype_ok(id_type) || !logits_ok(n, vocab, stride) ||
-        !logits_ok(n, vocab, dlogits_stride) || !grid_ok(n, vocab) || !positive(inv_temperature))
+        !logits_ok(n, vocab, dlogits_stride) || !positive(inv_temperature))
         return ZERO3_EINVAL;
     if (n == 0) return ZERO3_OK;
     if (!ptr_ok(logits, size_of(dtype)) || !ptr_ok(targets, size_of(id_type)) || !ptr_ok(lse, 4) ||
@@ -194,7 +193,7 @@ bool distill_ok(const void* logits, zero3_dtype dtype, int64_t n, int64_t vocab,
                 zero3_dtype teacher_dtype, zero3_itype id_type, int32_t k, int64_t teacher_stride,
                 float inv_temperature, const void* dlogits, int64_t dlogits_stride) {
     if (!dtype_ok(dtype) || !dtype_ok(teacher_dtype) || !itype_ok(id_type) ||
-        !logits_ok(n, vocab, stride) || !grid_ok(n, vocab) || !positive(inv_temperature) || k < 1 ||
+        !logits_ok(n, vocab, stride) || !positive(inv_temperature) || k < 1 ||
         k > ZERO3_MAX_TEACHER || teacher_stride < k)
         return false;
     if (dlogits && !logits_ok(n, vocab, dlogits_stride)) return false;
