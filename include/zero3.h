@@ -624,14 +624,17 @@ zero3_status zero3_token_logprobs_backward(const void* logits, zero3_dtype dtype
  *   q = softmax over the entries that count of a * teacher_logits
  *   log p = log softmax over the vocabulary of a * logits
  *   loss = (sum q_k (log q_k - log p[id_k])) / a^2
- * A token listed more than once has the sum of its entries' q.  A row without
- * a counting entry has loss 0 and a zero gradient.  In other rows a NaN or +inf
- * among the entries that count makes loss and gradient NaN; without any student
- * token (all -inf) they are 0; a NaN or +inf among the logits makes them NaN (the
- * first of these that holds).  lse (optional) is the student's log-sum-exp for
- * zero3_distill_backward.
+ * The sum runs over the list's entries: a token listed more than once adds one
+ * term for each, not one of its summed q, so such a loss may be negative.  The
+ * gradient takes the sum of a token's q.
+ * A row without a counting entry has loss 0 and a zero gradient.  In other rows
+ * a NaN or +inf among the entries that count makes loss and gradient NaN;
+ * without any student token (all -inf) they are 0; a NaN or +inf among the
+ * logits makes them NaN (the first of these that holds).
+ * lse (optional) is the student's log-sum-exp for zero3_distill_backward.
  * With dlogits (optional) the gradient of sum_i row_weight[i] * loss[i] is
- * written by the same call, from one read of the logits:
+ * written by the same call, which reads a row's logits twice, the second time
+ * mostly from L2:
  *   dlogits_j = row_weight (p_j - sum of q_k over id_k = j) / a;
  * row_weight NULL: 1.  dlogits has the logits' dtype and may be the logits
  * themselves (same pointer and stride).  EINVAL also for k outside
