@@ -590,7 +590,8 @@ zero3_status zero3_embedding_backward(const void* dout, zero3_dtype dout_dtype, 
  *   entropy = -sum_j p_j log p_j       (optional)
  *   top_ids, top_logprobs [n, k]: the k largest logits in descending order,
  *     ties to the lowest index, and their log probabilities; k = 0: neither
- *     is used.
+ *     is used.  (The logits decide, also among those whose products with the
+ *     inverse temperature are equal or overflow to -inf.)
  * Masked tokens are -inf logits.  A row that a mask leaves without any token
  * has lse = -inf, entropy 0, log probabilities -inf and top_ids 0..k-1.  A row
  * with a NaN or +inf has NaN in every output that depends on it, and top_ids

@@ -346,7 +346,8 @@ struct RowPart {
 // first chunks are on their way while the block joins the row's statistics.
 // 8192 rows of 50257 bf16, 64 entries, loss and gradient: 272 us (1.65 GB, 6.1 TB/s; a
 // tenth of the second pass misses L2); gradient alone, 4096 of 32000 with 100
-// entries, 84 us (6.3 TB/s).
+// entries, 82 us (6.4 TB/s).  Where the rows in flight outgrow L2 the second pass reads
+// HBM: 4096 of 50257 binary32, loss and gradient, 530 us (floor 247).
 template <typename T, Make M, int NT>
 __global__ void __launch_bounds__(NT + 32) distill_kernel(const __grid_constant__ DistillArgs a) {
     constexpr bool LOSS = M == Make::kBoth;
@@ -528,7 +529,7 @@ bool same_phase(const DistillArgs& a) {
 }
 
 // Blocks per row: more than one where rows are few and long.  Loss and gradient of
-// 4 rows of 50257 take 5.4 us (one block per row: 7.9), 64 6.7 (8.7), 200 12.8 (two per
+// 4 rows of 50257 take 5.4 us (one block per row: 7.9), 64 6.9 (8.7), 200 12.8 (two per
 // row: 13.7).
 int row_blocks(int64_t n, int64_t chunks, int threads) {
     int C = 1;
@@ -567,8 +568,8 @@ cudaError_t launch(const DistillArgs& a, cudaStream_t stream) {
     // Short rows: more and smaller blocks, to hide a row's chain of latencies
     // (list, join, second pass) behind other rows; long rows: fewer rows at a
     // time, whose second pass then finds them in L2.  Rows of bf16, loss with
-    // gradient, at 64 / 128 / 256 threads: 8192 of 4000 36 / 43 / - us, 8192 of 8000
-    // 59 / 64 / -, 4096 of 16000 - / 56 / 64, 4096 of 32000 - / 115 / 95.
+    // gradient, at 64 / 128 / 256 threads: 8192 of 4000 38 / 45 / 73 us, 8192 of
+    // 8000 59 / 66 / 88, 4096 of 16000 60 / 57 / 67, 4096 of 32000 - / 115 / 98.
     const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T));
     if (bytes <= 16 * 1024) return launch<T, M, 64>(a, stream);
     return bytes <= 40 * 1024 ? launch<T, M, 128>(a, stream) : launch<T, M, 256>(a, stream);

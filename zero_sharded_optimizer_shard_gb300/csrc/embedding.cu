@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NT) embed_kernel(const __grid_constant__ Embed
 //
 // Both launches: 8192 x 768 bf16 into 50257 rows, all written, 20.0 us; 32768 x 2048
 // bf16 added to bf16 49.4 us (220 MB: 4.5 TB/s), to binary32 71 us, binary32 to
-// binary32 120 us.
+// binary32 123 us.
 constexpr int kOwn = 512;          // tokens a sorting block owns at most
 constexpr int kList = 512;         // own positions a sorting warp lists
 // Shortest piece of a token that has several.  Short ones spread frequent tokens,
@@ -271,10 +271,11 @@ struct SortArgs {
 // sorted index of its own) and lists, warp by warp and in order, those of its
 // own tokens; the lists are counted by token, the counts summed up, and each
 // warp places its positions in order.  A warp's list that overflows (a token
-// that fills the batch) is read from the ids again.  Latency-bound: all that
-// counts is that a warp's loads are in flight together and that little is done
-// per id that is not the block's.  By itself 6 us for 3001 ids, 8 for 8192, 13 for
-// 32768.  (A radix sort over the grid needs a wait between its digits.)
+// that fills the batch) is read from the ids again.  Small batches are bound by
+// latency: what counts is that a warp's loads are in flight together.  Large ones are
+// bound by issue, every block testing every id (32768: 64% of the issue slots): what
+// counts is that little is done per id that is not the block's.  By itself 6 us
+// for 3001 ids, 8 for 8192, 13 for 32768.  (A radix sort over the grid needs a wait between its digits.)
 template <int W>
 struct SortShared {
     int32_t cnt[W][kOwn];
@@ -523,8 +524,11 @@ __device__ __forceinline__ void clear_rows(const SumArgs& p, int64_t warp, int l
     }
 }
 
-// Positions of a piece: a token with up to 512 positions is cut every 16,
-// longer ones so that neither a piece nor the number of pieces gets long.
+// Positions of a piece: a token with up to 512 positions is cut every 16, longer
+// ones every 32 or 64, and from 8193 positions on every 128.  One warp joins a
+// token's pieces, 8 at a time, so a token that fills a large batch costs:
+// 131072 positions of 768 columns take 84 us when the tokens are spread, 249 when
+// 15 of 16 are one token's.
 __device__ __forceinline__ int32_t piece_rows(int32_t count) {
     return count <= 32 * kPiece ? kPiece
            : count <= 128 * kPiece ? 2 * kPiece
