@@ -11,8 +11,10 @@
  *  - Device buffers are owned by the caller (allocated with any CUDA
  *    allocator) and passed as raw pointers; every device pointer must be
  *    16-byte aligned (ZERO3_EINVAL otherwise), except the matrices of the
- *    vocabulary operators.  Element offsets inside
- *    buffers need no alignment: the kernels handle any phase.
+ *    vocabulary operators, the tensors of gradient lists and single numbers
+ *    (norms, coefficients, sums), which need the alignment of their elements.
+ *    Element offsets inside buffers need no alignment: the kernels handle any
+ *    phase.
  *  - Arrays of per-rank pointers (grads[], master[], ...) are HOST arrays of
  *    n_ranks device pointers.  The library reads them during the call only.
  *    A rank whose shard does not meet the requested flat range may pass NULL
@@ -25,7 +27,7 @@
  *    writes to be visible, before it touches memory.  Plain stream order
  *    therefore holds for the data, whatever kernel (this library's or
  *    another's) comes before or after.  The compute calls (steps,
- *    reduce-scatter, all-gathers, quantization) can be captured in a CUDA
+ *    reduce-scatter, all-gathers, quantization, clipping) can be captured in a CUDA
  *    graph; the fetch, release and coordinator calls keep host-side state
  *    (status, references, events) that a replay would not repeat, so they
  *    are issued directly.
@@ -520,6 +522,112 @@ zero3_status zero3_save_16bit_weights(const zero3_plan* plan, const uint16_t* fu
  * is created; ZERO3_EIO otherwise.  Memory use is one 16 MiB buffer. */
 zero3_status zero3_merge_shards(const zero3_plan* plan, const char* const* shard_paths,
                                 const char* persistent_path, const char* out_path);
+
+/* ------------------------------------------------------ gradient clipping
+ * Clipping by the global norm, between the reduction and the update:
+ *   N = sqrt(sum of the squares of every gradient)
+ *   coef = min(1, max_norm / (N + 1e-6));  1 where max_norm is infinite
+ *   g' = f32(coef * g)
+ * as one call around the sharded step (zero3_step_clipped), in parts for
+ * gradients that arrive in buckets or lie on several ranks
+ * (zero3_grad_square_sum, zero3_clip_coefficient, the scaled steps), and over
+ * plain lists of tensors (zero3_grad_norm, zero3_clip_grads).
+ *  - Norms and coefficients are device memory: nothing waits for the GPU.
+ *    Sums are kept in binary64 beyond a block's elements, in a fixed order;
+ *    squares that would overflow or vanish in binary32 do not.  N is rounded
+ *    to binary32 when it is stored (infinite above its range), coef is taken
+ *    from the unrounded N.
+ *  - A NaN gradient makes N and coef NaN (and so every clipped gradient), an
+ *    infinite one N infinite and coef 0 (clipped: NaN where it is, 0
+ *    elsewhere); with an infinite max_norm coef stays 1.
+ *  - No call allocates device memory, synchronises or keeps anything; all can
+ *    be captured in a CUDA graph.  A workspace is 16-byte aligned device
+ *    memory, free for any use once the call's work on the stream is done; calls
+ *    that may run at the same time need one each.
+ *  - EINVAL, with nothing launched: max_norm that is not positive (NaN too), a
+ *    NULL or misaligned pointer, a workspace that is too small. */
+
+/* The steps with the reduced gradient multiplied by *scale (one binary32 number
+ * in device memory, read when the kernels run): g' = f32(scale * g), one more
+ * rounding, then as zero3_step, zero3_step_stage12 and zero3_step_qwz.  A scale of
+ * 1 gives their results bit for bit. */
+zero3_status zero3_step_scaled(const zero3_plan* plan, const zero3_adamw_hparams* hp, int64_t t,
+                               const uint16_t* const* grads, int64_t grads_origin,
+                               float* const* master, float* const* m, float* const* v,
+                               uint16_t* const* sparam, uint16_t* full,
+                               const zero3_persist_state* persist, int64_t flat_lo,
+                               int64_t flat_hi, const float* scale, zero3_stream stream);
+zero3_status zero3_step_stage12_scaled(const zero3_plan* plan, const zero3_adamw_hparams* hp,
+                                       int64_t t, const uint16_t* const* grads,
+                                       int64_t grads_origin, float* const* master, float* const* m,
+                                       float* const* v, uint16_t* const* params, int64_t flat_lo,
+                                       int64_t flat_hi, const float* scale, zero3_stream stream);
+zero3_status zero3_step_qwz_scaled(const zero3_plan* plan, const zero3_adamw_hparams* hp, int64_t t,
+                                   const uint16_t* const* grads, int64_t grads_origin,
+                                   float* const* master, float* const* m, float* const* v,
+                                   uint16_t* const* sparam, int32_t bits, int8_t* const* codes,
+                                   float* const* scales, const zero3_persist_state* persist,
+                                   int64_t flat_lo, int64_t flat_hi, const float* scale,
+                                   zero3_stream stream);
+
+/* Sum of the squares of the reduced gradient (the g of zero3_reduce_scatter,
+ * binary32, never rounded further) of flat [flat_lo, flat_hi) and, with
+ * persist_grads (N_d pointers as in zero3_persist_state, or NULL), of the
+ * persistent group: *square_sum (one binary64 number in device memory) receives
+ * it, or has it added with accumulate != 0.  Ranges of buckets, or of ranks in
+ * several processes (whose sums are then added by an all-reduce), count the
+ * persistent group once. */
+zero3_status zero3_grad_square_sum_workspace(const zero3_plan* plan, int64_t flat_lo,
+                                             int64_t flat_hi, int64_t* bytes);
+zero3_status zero3_grad_square_sum(const zero3_plan* plan, const uint16_t* const* grads,
+                                   int64_t grads_origin, const uint16_t* const* persist_grads,
+                                   int64_t flat_lo, int64_t flat_hi, int32_t accumulate,
+                                   double* square_sum, void* workspace, int64_t workspace_bytes,
+                                   zero3_stream stream);
+
+/* The norm and the coefficient (one binary32 number each, either may be NULL) of
+ * a sum of squares in device memory. */
+zero3_status zero3_clip_coefficient(const double* square_sum, float max_norm, float* norm,
+                                    float* coef, zero3_stream stream);
+
+/* zero3_step with its gradients clipped by the norm over the whole range and
+ * (with persist) the persistent group; norm (one binary32 number, optional)
+ * receives the norm before clipping.  Results equal zero3_grad_square_sum +
+ * zero3_clip_coefficient + zero3_step_scaled bit for bit, with either workspace:
+ * `least` bytes re-read the ranks' gradients for the update; with `best` bytes
+ * (more for N_d above 4, by 4 bytes per element) the reduced gradient is kept
+ * there in binary32 instead, 2 * N_d + 4 + 32 bytes of traffic per element in
+ * place of 4 * N_d + 28. */
+zero3_status zero3_step_clipped_workspace(const zero3_plan* plan, int64_t flat_lo, int64_t flat_hi,
+                                          int64_t* least, int64_t* best);
+zero3_status zero3_step_clipped(const zero3_plan* plan, const zero3_adamw_hparams* hp, int64_t t,
+                                const uint16_t* const* grads, int64_t grads_origin,
+                                float* const* master, float* const* m, float* const* v,
+                                uint16_t* const* sparam, uint16_t* full,
+                                const zero3_persist_state* persist, int64_t flat_lo,
+                                int64_t flat_hi, float max_norm, float* norm, void* workspace,
+                                int64_t workspace_bytes, zero3_stream stream);
+
+/* Norms of a list of gradient tensors of one dtype (ZERO3_BF16 or ZERO3_F32):
+ * tensors[i] points to numels[i] elements with the alignment of its elements
+ * (NULL where numels[i] = 0; the arrays are host memory, read during the call).
+ * Outputs, each optional but one of them given: tensor_norms [n_tensors], the
+ * square_sum, the total norm and the coefficient.  A list of no tensor has norm
+ * 0 and coefficient 1 (for max_norm >= 1e-6).  EINVAL also for more than 2^24
+ * tensors or 2^41 elements. */
+zero3_status zero3_grad_norm_workspace(const int64_t* numels, int64_t n_tensors, int64_t* bytes);
+zero3_status zero3_grad_norm(const void* const* tensors, const int64_t* numels, int64_t n_tensors,
+                             zero3_dtype dtype, float max_norm, float* tensor_norms,
+                             double* square_sum, float* norm, float* coef, void* workspace,
+                             int64_t workspace_bytes, zero3_stream stream);
+
+/* out[i] = coef * tensors[i], rounded to binary32 and then to out_dtype; *coef is
+ * one binary32 number in device memory.  out NULL: in place (then, and where
+ * out[i] = tensors[i], the dtypes must be equal, and a coefficient of 1 writes
+ * nothing).  Otherwise no output may overlap an input. */
+zero3_status zero3_clip_grads(const void* const* tensors, const int64_t* numels, int64_t n_tensors,
+                              zero3_dtype dtype, const float* coef, void* const* out,
+                              zero3_dtype out_dtype, zero3_stream stream);
 
 /* ---------------------------------------------------- vocabulary operators
  * The two ends of a language model around the sharded step: tokens become

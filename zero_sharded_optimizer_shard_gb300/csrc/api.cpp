@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "operators.h"
 
 namespace {
 
@@ -167,12 +168,12 @@ void add_persistent_span(const zero3_plan* p, const zero3_persist_state* ps, int
 // flat gradients in one buffer per rank), returns true and the offset: the
 // group can then ride in the flat launch as one more span.
 bool common_persist_offset(const zero3_plan* p, const uint16_t* const* grads,
-                           const zero3_persist_state* ps, int64_t* gofs) {
-    if (!grads || !ps || !ps->grads) return false;
+                           const uint16_t* const* pgrads, int64_t* gofs) {
+    if (!grads || !pgrads) return false;
     int64_t d0 = 0;
     for (int q = 0; q < p->n_ranks; ++q) {
-        if (!grads[q] || !ps->grads[q]) return false;
-        const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(ps->grads[q]) -
+        if (!grads[q] || !pgrads[q]) return false;
+        const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(pgrads[q]) -
                                                reinterpret_cast<uintptr_t>(grads[q]));
         if (d % 2 != 0 || (q > 0 && d != d0)) return false;
         d0 = d;
@@ -182,13 +183,15 @@ bool common_persist_offset(const zero3_plan* p, const uint16_t* const* grads,
 }
 
 zero3_status persistent_launch(const zero3_plan* p, const z3::Scalars& sc,
-                               const zero3_persist_state* ps, cudaStream_t stream) {
+                               const zero3_persist_state* ps, const float* scale,
+                               cudaStream_t stream) {
     if (p->psi_s == 0) return ZERO3_OK;
     if (!persist_ok(p, ps)) return ZERO3_EINVAL;
     StreamArgs a;
     std::memset(&a, 0, sizeof(a));
     a.nd = p->n_ranks;
     a.sc = sc;
+    a.scale = scale;
     for (int q = 0; q < p->n_ranks; ++q) a.grads[q] = ps->grads[q];
     add_persistent_span(p, ps, 0, a);
     return cuda_status(z3::launch_stream(z3::kFused, a, stream));
@@ -433,17 +436,22 @@ zero3_status zero3_allgather(const zero3_plan* p, const uint16_t* const* sparam,
     return L.flush();
 }
 
-zero3_status zero3_step(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
-                        const uint16_t* const* grads, int64_t grads_origin, float* const* master,
-                        float* const* m, float* const* v, uint16_t* const* sparam,
-                        uint16_t* full, const zero3_persist_state* persist, int64_t lo,
-                        int64_t hi, zero3_stream stream) {
+}  // extern "C"
+
+namespace {
+
+// The steps; `scale`: a factor of the reduced gradient on the device, or null.
+zero3_status step(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                  const uint16_t* const* grads, int64_t grads_origin, float* const* master,
+                  float* const* m, float* const* v, uint16_t* const* sparam, uint16_t* full,
+                  const zero3_persist_state* persist, int64_t lo, int64_t hi, const float* scale,
+                  zero3_stream stream) {
     if (!p || !range_ok(p, lo, hi) || !hparams_ok(hp, t) || grads_origin > lo)
         return ZERO3_EINVAL;
     const z3::Scalars sc = step_scalars(p, hp, t);
     const bool with_persist = persist && p->psi_s > 0;
     int64_t pofs = 0;
-    const bool fold = with_persist && lo < hi && common_persist_offset(p, grads, persist, &pofs);
+    const bool fold = with_persist && lo < hi && common_persist_offset(p, grads, persist->grads, &pofs);
     // validate the persistent group before the first launch so that an
     // error launches nothing
     if (with_persist) {
@@ -466,21 +474,21 @@ zero3_status zero3_step(const zero3_plan* p, const zero3_adamw_hparams* hp, int6
         rp.full = full;
         StreamArgs a;
         zero3_status st = build_args(p, z3::kFused, rp, lo, hi, &sc, 0, a);
+        a.scale = scale;
         if (st != ZERO3_OK) return st;
         // the persistent group rides in the same launch as one more span
         if (fold) add_persistent_span(p, persist, pofs, a);
         st = cuda_status(z3::launch_stream(z3::kFused, a, stream));
         if (st != ZERO3_OK || fold) return st;
     }
-    if (with_persist) return persistent_launch(p, sc, persist, stream);
+    if (with_persist) return persistent_launch(p, sc, persist, scale, stream);
     return ZERO3_OK;
 }
 
-zero3_status zero3_step_stage12(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
-                                const uint16_t* const* grads, int64_t grads_origin,
-                                float* const* master, float* const* m, float* const* v,
-                                uint16_t* const* params, int64_t lo, int64_t hi,
-                                zero3_stream stream) {
+zero3_status step_stage12(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                          const uint16_t* const* grads, int64_t grads_origin, float* const* master,
+                          float* const* m, float* const* v, uint16_t* const* params, int64_t lo,
+                          int64_t hi, const float* scale, zero3_stream stream) {
     if (!p || !range_ok(p, lo, hi) || !hparams_ok(hp, t) || grads_origin > lo)
         return ZERO3_EINVAL;
     if (lo == hi) return ZERO3_OK;
@@ -500,15 +508,15 @@ zero3_status zero3_step_stage12(const zero3_plan* p, const zero3_adamw_hparams* 
     zero3_status st = build_args(p, z3::kFusedRep, rp, lo, hi, &sc, 0, a);
     if (st != ZERO3_OK) return st;
     for (int q = 0; q < p->n_ranks; ++q) a.reps[q] = params[q];
+    a.scale = scale;
     return cuda_status(z3::launch_stream(z3::kFusedRep, a, stream));
 }
 
-zero3_status zero3_step_qwz(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
-                            const uint16_t* const* grads, int64_t grads_origin,
-                            float* const* master, float* const* m, float* const* v,
-                            uint16_t* const* sparam, int32_t bits, int8_t* const* codes,
-                            float* const* scales, const zero3_persist_state* persist,
-                            int64_t lo, int64_t hi, zero3_stream stream) {
+zero3_status step_qwz(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                      const uint16_t* const* grads, int64_t grads_origin, float* const* master,
+                      float* const* m, float* const* v, uint16_t* const* sparam, int32_t bits,
+                      int8_t* const* codes, float* const* scales, const zero3_persist_state* persist,
+                      int64_t lo, int64_t hi, const float* scale, zero3_stream stream) {
     if (!p || !range_ok(p, lo, hi) || !hparams_ok(hp, t) || grads_origin > lo)
         return ZERO3_EINVAL;
     if (bits != 8 && bits != 4) return ZERO3_EINVAL;
@@ -528,13 +536,295 @@ zero3_status zero3_step_qwz(const zero3_plan* p, const zero3_adamw_hparams* hp, 
         rp.warp_blocks = true;
         StreamArgs a;
         zero3_status st = build_args(p, z3::kFusedQ, rp, lo, hi, &sc, bits, a);
+        a.scale = scale;
         if (st != ZERO3_OK) return st;
         if (persist && !persist_ok(p, persist)) return ZERO3_EINVAL;
         st = cuda_status(z3::launch_stream(z3::kFusedQ, a, stream));
         if (st != ZERO3_OK) return st;
     }
-    if (persist) return persistent_launch(p, sc, persist, stream);
+    if (persist) return persistent_launch(p, sc, persist, scale, stream);
     return ZERO3_OK;
+}
+
+// ------------------------------------------------------------------ clipping
+
+bool scale_ok(const float* scale) {
+    return scale && reinterpret_cast<uintptr_t>(scale) % 4 == 0;
+}
+
+// Upper bounds for a norm over flat [lo, hi) and the persistent group: blocks
+// of its launches, and elements of the kept reduced gradient.
+int64_t norm_blocks(const zero3_plan* p, int64_t lo, int64_t hi) {
+    const int64_t chunks = (hi - lo) / 8 + 2 * p->n_ranks + p->psi_s / 8 + 2;
+    return z3::stream_blocks(chunks) + 1;  // one more where the group is a launch of its own
+}
+int64_t kept_elements(const zero3_plan* p, int64_t lo, int64_t hi) {
+    return hi - lo + 16 * (p->n_ranks + 1) + p->psi_s;
+}
+// One sum per block fits a grid.
+bool norm_range_ok(const zero3_plan* p, int64_t lo, int64_t hi) {
+    return (hi - lo) / 8 + p->psi_s / 8 < int64_t{1} << 38;
+}
+
+struct NormSpace {
+    double* partial;
+    double* folded;
+    double* square_sum;
+    float* coef;
+    float* kept;
+};
+constexpr int64_t kNormScalars = 16;  // bytes: the square sum, the coefficient
+int64_t norm_space(const zero3_plan* p, int64_t lo, int64_t hi) {
+    return ((norm_blocks(p, lo, hi) + z3::kFoldBlocks) * 8 + kNormScalars + 15) / 16 * 16;
+}
+NormSpace cut_space(const zero3_plan* p, int64_t lo, int64_t hi, void* workspace) {
+    NormSpace s;
+    s.partial = static_cast<double*>(workspace);
+    s.folded = s.partial + norm_blocks(p, lo, hi);
+    s.square_sum = s.folded + z3::kFoldBlocks;
+    s.coef = reinterpret_cast<float*>(s.square_sum + 1);
+    s.kept = reinterpret_cast<float*>(static_cast<char*>(workspace) + norm_space(p, lo, hi));
+    return s;
+}
+
+// Where a span's part of the kept gradient lies: local index i at out[i], the
+// first multiple of 8 on 16 bytes.
+void keep_span(Span& s, float** at) {
+    const int64_t first = s.lo & ~static_cast<int64_t>(7);
+    s.out = reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(*at) -
+                                    static_cast<uintptr_t>(first) * sizeof(float));
+    *at += (s.hi - first + 7) / 8 * 8;
+}
+
+// Sums of squares of the reduced gradient of [lo, hi) and, with pgrads, of the
+// persistent group: one per block of one or two launches into s.partial, their
+// number into *n.  keep: the reduced gradient stays in s.kept, spans in order.
+zero3_status norm_launches(const zero3_plan* p, const uint16_t* const* grads, int64_t grads_origin,
+                           const uint16_t* const* pgrads, int64_t lo, int64_t hi, bool keep,
+                           const NormSpace& s, int64_t* n, cudaStream_t stream) {
+    z3::Scalars sc;
+    std::memset(&sc, 0, sizeof(sc));
+    sc.inv_nd = static_cast<float>(1.0 / static_cast<double>(p->n_ranks));
+    const int mode = keep ? z3::kReduceNorm : z3::kNorm;
+    int64_t pofs = 0;
+    const bool with_persist = pgrads && p->psi_s > 0;
+    const bool fold = with_persist && lo < hi && common_persist_offset(p, grads, pgrads, &pofs);
+    Span ps;
+    std::memset(&ps, 0, sizeof(ps));
+    ps.hi = p->psi_s;
+    ps.fofs = -1;
+    float* at = s.kept;
+    *n = 0;
+    if (lo < hi) {
+        RankPtrs rp;
+        rp.grads = grads;
+        rp.grads_origin = grads_origin;
+        StreamArgs a;
+        zero3_status st = build_args(p, mode, rp, lo, hi, &sc, 0, a);
+        if (st != ZERO3_OK) return st;
+        if (fold) {
+            ps.gofs = pofs;
+            ps.gphase = static_cast<int32_t>(pofs & 7);
+            add_span(a, ps);
+        }
+        if (keep)
+            for (int i = 0; i < a.n_spans; ++i) keep_span(a.span[i], &at);
+        a.partial = s.partial;
+        st = cuda_status(z3::launch_stream(mode, a, stream));
+        if (st != ZERO3_OK) return st;
+        *n = z3::stream_blocks(a.total_chunks);
+    }
+    if (with_persist && !fold) {
+        StreamArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.nd = p->n_ranks;
+        a.sc = sc;
+        for (int q = 0; q < p->n_ranks; ++q) a.grads[q] = pgrads[q];
+        add_span(a, ps);
+        if (keep) keep_span(a.span[0], &at);
+        a.partial = s.partial + *n;
+        const zero3_status st = cuda_status(z3::launch_stream(mode, a, stream));
+        if (st != ZERO3_OK) return st;
+        *n += z3::stream_blocks(a.total_chunks);
+    }
+    return ZERO3_OK;
+}
+
+z3::NormArgs norm_args(const NormSpace& s, int64_t n) {
+    z3::NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.partial = s.partial;
+    a.n = n;
+    a.max_norm = 1.0f;
+    return a;
+}
+
+// Gradients of the persistent group that a norm may read: any alignment of
+// their elements where they ride in the flat launch, 16 bytes otherwise.
+bool persist_grads_ok(const zero3_plan* p, const uint16_t* const* grads,
+                      const uint16_t* const* pgrads, int64_t lo, int64_t hi) {
+    int64_t ofs;
+    if (!pgrads || p->psi_s == 0) return true;
+    if (lo < hi && common_persist_offset(p, grads, pgrads, &ofs)) return true;
+    return grads_ok(p, pgrads);
+}
+
+}  // namespace
+
+extern "C" {
+
+zero3_status zero3_step(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                        const uint16_t* const* grads, int64_t grads_origin, float* const* master,
+                        float* const* m, float* const* v, uint16_t* const* sparam,
+                        uint16_t* full, const zero3_persist_state* persist, int64_t lo,
+                        int64_t hi, zero3_stream stream) {
+    return step(p, hp, t, grads, grads_origin, master, m, v, sparam, full, persist, lo, hi, nullptr,
+                stream);
+}
+
+zero3_status zero3_step_scaled(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                               const uint16_t* const* grads, int64_t grads_origin,
+                               float* const* master, float* const* m, float* const* v,
+                               uint16_t* const* sparam, uint16_t* full,
+                               const zero3_persist_state* persist, int64_t lo, int64_t hi,
+                               const float* scale, zero3_stream stream) {
+    if (!scale_ok(scale)) return ZERO3_EINVAL;
+    return step(p, hp, t, grads, grads_origin, master, m, v, sparam, full, persist, lo, hi, scale,
+                stream);
+}
+
+zero3_status zero3_step_stage12(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                                const uint16_t* const* grads, int64_t grads_origin,
+                                float* const* master, float* const* m, float* const* v,
+                                uint16_t* const* params, int64_t lo, int64_t hi,
+                                zero3_stream stream) {
+    return step_stage12(p, hp, t, grads, grads_origin, master, m, v, params, lo, hi, nullptr, stream);
+}
+
+zero3_status zero3_step_stage12_scaled(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                                       const uint16_t* const* grads, int64_t grads_origin,
+                                       float* const* master, float* const* m, float* const* v,
+                                       uint16_t* const* params, int64_t lo, int64_t hi,
+                                       const float* scale, zero3_stream stream) {
+    if (!scale_ok(scale)) return ZERO3_EINVAL;
+    return step_stage12(p, hp, t, grads, grads_origin, master, m, v, params, lo, hi, scale, stream);
+}
+
+zero3_status zero3_step_qwz(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                            const uint16_t* const* grads, int64_t grads_origin,
+                            float* const* master, float* const* m, float* const* v,
+                            uint16_t* const* sparam, int32_t bits, int8_t* const* codes,
+                            float* const* scales, const zero3_persist_state* persist,
+                            int64_t lo, int64_t hi, zero3_stream stream) {
+    return step_qwz(p, hp, t, grads, grads_origin, master, m, v, sparam, bits, codes, scales, persist,
+                    lo, hi, nullptr, stream);
+}
+
+zero3_status zero3_step_qwz_scaled(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                                   const uint16_t* const* grads, int64_t grads_origin,
+                                   float* const* master, float* const* m, float* const* v,
+                                   uint16_t* const* sparam, int32_t bits, int8_t* const* codes,
+                                   float* const* scales, const zero3_persist_state* persist,
+                                   int64_t lo, int64_t hi, const float* scale, zero3_stream stream) {
+    if (!scale_ok(scale)) return ZERO3_EINVAL;
+    return step_qwz(p, hp, t, grads, grads_origin, master, m, v, sparam, bits, codes, scales, persist,
+                    lo, hi, scale, stream);
+}
+
+zero3_status zero3_grad_square_sum_workspace(const zero3_plan* p, int64_t lo, int64_t hi,
+                                             int64_t* bytes) {
+    if (!p || !bytes || !range_ok(p, lo, hi) || !norm_range_ok(p, lo, hi)) return ZERO3_EINVAL;
+    *bytes = norm_space(p, lo, hi);
+    return ZERO3_OK;
+}
+
+zero3_status zero3_grad_square_sum(const zero3_plan* p, const uint16_t* const* grads,
+                                   int64_t grads_origin, const uint16_t* const* persist_grads,
+                                   int64_t lo, int64_t hi, int32_t accumulate, double* square_sum,
+                                   void* workspace, int64_t bytes, zero3_stream stream) {
+    if (!p || !range_ok(p, lo, hi) || !norm_range_ok(p, lo, hi) || grads_origin > lo || !square_sum ||
+        reinterpret_cast<uintptr_t>(square_sum) % 8 != 0)
+        return ZERO3_EINVAL;
+    if (!workspace || !aligned16(workspace) || bytes < norm_space(p, lo, hi)) return ZERO3_EINVAL;
+    if (lo < hi && !grads_ok(p, grads)) return ZERO3_EINVAL;
+    if (!persist_grads_ok(p, grads, persist_grads, lo, hi)) return ZERO3_EINVAL;
+    const NormSpace s = cut_space(p, lo, hi, workspace);
+    int64_t n;
+    const zero3_status st = norm_launches(p, grads, grads_origin, persist_grads, lo, hi, false, s, &n,
+                                          stream);
+    if (st != ZERO3_OK) return st;
+    z3::NormArgs a = norm_args(s, n);
+    a.square_sum = square_sum;
+    a.accumulate = accumulate ? 1 : 0;
+    return cuda_status(z3::launch_norms(a, s.folded, stream));
+}
+
+zero3_status zero3_step_clipped_workspace(const zero3_plan* p, int64_t lo, int64_t hi, int64_t* least,
+                                          int64_t* best) {
+    if (!p || !least || !best || !range_ok(p, lo, hi) || !norm_range_ok(p, lo, hi)) return ZERO3_EINVAL;
+    *least = norm_space(p, lo, hi);
+    // The update needs the reduced gradient again: N_d bf16 numbers read once
+    // more, or one binary32 number written and read.
+    *best = *least + (p->n_ranks > 4 ? 4 * kept_elements(p, lo, hi) : 0);
+    return ZERO3_OK;
+}
+
+zero3_status zero3_step_clipped(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
+                                const uint16_t* const* grads, int64_t grads_origin,
+                                float* const* master, float* const* m, float* const* v,
+                                uint16_t* const* sparam, uint16_t* full,
+                                const zero3_persist_state* persist, int64_t lo, int64_t hi,
+                                float max_norm, float* norm, void* workspace, int64_t bytes,
+                                zero3_stream stream) {
+    int64_t least, best;
+    if (zero3_step_clipped_workspace(p, lo, hi, &least, &best) != ZERO3_OK || !hparams_ok(hp, t) ||
+        grads_origin > lo || !(max_norm > 0.0f) || reinterpret_cast<uintptr_t>(norm) % 4 != 0)
+        return ZERO3_EINVAL;
+    if (!workspace || !aligned16(workspace) || bytes < least) return ZERO3_EINVAL;
+    const bool with_persist = persist && p->psi_s > 0;
+    const uint16_t* const* pgrads = with_persist ? persist->grads : nullptr;
+    // everything is checked before the first launch
+    if (with_persist &&
+        (!persist->grads || !persist->master || !persist->m || !persist->v || !persist->param ||
+         !aligned16(persist->master) || !aligned16(persist->m) || !aligned16(persist->v) ||
+         !aligned16(persist->param) || !persist_grads_ok(p, grads, pgrads, lo, hi)))
+        return ZERO3_EINVAL;
+    const z3::Scalars sc = step_scalars(p, hp, t);
+    RankPtrs rp;
+    rp.master = master;
+    rp.m = m;
+    rp.v = v;
+    rp.need_state = true;
+    rp.out = reinterpret_cast<void* const*>(sparam);
+    rp.full = full;
+    StreamArgs a;
+    if (lo < hi && (!grads_ok(p, grads) || !sparam || !full || !aligned16(full))) return ZERO3_EINVAL;
+    const zero3_status ok = build_args(p, z3::kAdamFull, rp, lo, hi, &sc, 0, a);
+    if (ok != ZERO3_OK) return ok;
+    if (lo == hi && !with_persist && !norm) return ZERO3_OK;
+    const bool keep = best > least && bytes >= best;
+    const NormSpace s = cut_space(p, lo, hi, workspace);
+    int64_t n;
+    zero3_status st = norm_launches(p, grads, grads_origin, pgrads, lo, hi, keep, s, &n, stream);
+    if (st != ZERO3_OK) return st;
+    z3::NormArgs na = norm_args(s, n);
+    na.norm = norm;
+    na.coef = s.coef;
+    na.max_norm = max_norm;
+    st = cuda_status(z3::launch_norms(na, s.folded, stream));
+    if (st != ZERO3_OK) return st;
+    if (!keep)
+        return step(p, hp, t, grads, grads_origin, master, m, v, sparam, full, persist, lo, hi, s.coef,
+                    stream);
+    if (with_persist) add_persistent_span(p, persist, 0, a);
+    float* at = s.kept;
+    for (int i = 0; i < a.n_spans; ++i) {
+        Span kept = a.span[i];
+        keep_span(kept, &at);
+        a.span[i].in = kept.out;
+    }
+    a.scale = s.coef;
+    return cuda_status(z3::launch_stream(z3::kAdamFull, a, stream));
 }
 
 zero3_status zero3_quantize_shards(const zero3_plan* p, const uint16_t* const* sparam,
@@ -585,7 +875,7 @@ zero3_status zero3_allgather_qwz(const zero3_plan* p, int32_t bits, const int8_t
 zero3_status zero3_persistent_step(const zero3_plan* p, const zero3_adamw_hparams* hp, int64_t t,
                                    const zero3_persist_state* persist, zero3_stream stream) {
     if (!p || !hparams_ok(hp, t) || !persist) return ZERO3_EINVAL;
-    return persistent_launch(p, step_scalars(p, hp, t), persist, stream);
+    return persistent_launch(p, step_scalars(p, hp, t), persist, nullptr, stream);
 }
 
 zero3_status zero3_cast_params(const zero3_plan* p, const float* const* master,

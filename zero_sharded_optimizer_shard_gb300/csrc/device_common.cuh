@@ -64,6 +64,35 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
                       pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+// The 8 bf16 values at elements ph..ph+7 (1 <= ph <= 7) of the 16-element
+// window formed by two consecutive aligned 16-byte blocks b0, b1 (window
+// words w0..w7).  Branch-free, so the compiler keeps every rank's loads
+// ahead of the first realignment: result word m is the funnel shift of
+// words k+m and k+m+1 (k = ph / 2) right by 16 * (ph & 1) bits, the words
+// picked by two rounds of selects (by 2 words, then by 1).
+__device__ __forceinline__ uint4 realign8(const uint4& b0, const uint4& b1, int ph) {
+    const bool by2 = (ph & 4) != 0, by1 = (ph & 2) != 0;
+    const uint32_t sh = static_cast<uint32_t>(ph & 1) * 16u;
+    const uint32_t t0 = by2 ? b0.z : b0.x, t1 = by2 ? b0.w : b0.y, t2 = by2 ? b1.x : b0.z;
+    const uint32_t t3 = by2 ? b1.y : b0.w, t4 = by2 ? b1.z : b1.x, t5 = by2 ? b1.w : b1.y;
+    const uint32_t v0 = by1 ? t1 : t0, v1 = by1 ? t2 : t1, v2 = by1 ? t3 : t2;
+    const uint32_t v3 = by1 ? t4 : t3, v4 = by1 ? t5 : t4;
+    return make_uint4(__funnelshift_r(v0, v1, sh), __funnelshift_r(v1, v2, sh),
+                      __funnelshift_r(v2, v3, sh), __funnelshift_r(v3, v4, sh));
+}
+
+// 8 consecutive bf16 values at p, element phase ph != 0, read as the two
+// aligned 16-byte blocks around them (through the read-only path, so the
+// block a neighbouring thread also reads is served from L1).  The caller
+// guarantees that both blocks lie inside the valid range: the 8 elements
+// before p and the 16 from p on.
+__device__ __forceinline__ uint4 ld8_window(const uint16_t* p, int ph) {
+    const uint16_t* a = p - ph;
+    const uint4 b0 = __ldg(reinterpret_cast<const uint4*>(a));
+    const uint4 b1 = __ldg(reinterpret_cast<const uint4*>(a + 8));
+    return realign8(b0, b1, ph);
+}
+
 // Launch with programmatic stream serialization (see wait_prior_grids).  What the
 // launch itself returned is the call's result; the thread's last error may be an
 // earlier call's.

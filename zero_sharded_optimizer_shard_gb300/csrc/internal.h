@@ -49,6 +49,9 @@ enum Mode : int {
     kFusedRep = 5, // grads -> reduce -> AdamW -> every rank's full copy (ZeRO-1/2)
     kFusedQ = 6,   // grads -> reduce -> AdamW -> sparam + int8 codes/scales (qwZ)
     kQuant = 7,    // sparam -> int8 codes/scales (qwZ)
+    kNorm = 8,       // grads -> reduce -> sums of squares
+    kReduceNorm = 9, // grads -> reduce -> f32 shard grad + sums of squares
+    kAdamFull = 10,  // f32 shard grad -> AdamW -> sparam (+ full)
 };
 
 // qwZ block: one warp's 32 chunks of 8 elements.
@@ -66,8 +69,8 @@ struct Span {
     float* master;
     float* m;
     float* v;
-    void* out;           // sparam (bf16) or shard grad (kReduce)
-    const void* in;      // shard grad (kAdam) or sparam (kQuant) or master (kCast)
+    void* out;           // sparam (bf16) or shard grad (kReduce, kReduceNorm)
+    const void* in;      // shard grad (kAdam, kAdamFull) or sparam (kQuant) or master (kCast)
     int8_t* codes;       // qwZ codes of the shard (kFusedQ, kQuant out)
     float* scales;       // qwZ block scales of the shard
     // Element phase (address / 2 mod 8) of the gradient and all-gather
@@ -88,6 +91,8 @@ struct StreamArgs {
     int32_t nd;
     int32_t dtype;       // zero3_dtype of the shard grad (kReduce out / kAdam in); qwZ bits
     int32_t pad_;
+    const float* scale;  // factor of the reduced gradient, on the device (null: none)
+    double* partial;     // kNorm, kReduceNorm: a block's sum of squares
     Scalars sc;
 };
 
@@ -159,6 +164,8 @@ class PieceLauncher {
 };
 
 cudaError_t launch_stream(int mode, const StreamArgs& a, cudaStream_t stream);
+// Blocks of a streaming launch, each of which writes one sum in the norm modes.
+int64_t stream_blocks(int64_t total_chunks);
 cudaError_t launch_pieces_small(int kind, const PieceArgs<kSmallPieces>& a, cudaStream_t stream);
 cudaError_t launch_pieces_large(int kind, const PieceArgs<kLargePieces>& a, cudaStream_t stream);
 

@@ -27,6 +27,8 @@
 //   g = (sum_q f32(grad_q)) * inv_nd            (q ascending, from +0)
 //   p = p*decay; m = b1*m + omb1*g; v = b2*v + omb2*(g*g)
 //   d = sqrt(v)*inv_sqrt_bc2 + eps; p = p - step_size*(m/d); sparam = bf16(p)
+// The scaled forms of the steps multiply g by one more factor, which lies in
+// device memory (the clipping coefficient): one more rounding per element.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -79,35 +81,6 @@ __device__ __forceinline__ uint4 ld8_phase(const uint16_t* p, int ph) {
         w[k] = static_cast<uint32_t>(__ldg(q + 2 * k)) |
                (static_cast<uint32_t>(__ldg(q + 2 * k + 1)) << 16);
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The 8 bf16 values at elements ph..ph+7 (1 <= ph <= 7) of the 16-element
-// window formed by two consecutive aligned 16-byte blocks b0, b1 (window
-// words w0..w7).  Branch-free, so the compiler keeps every rank's loads
-// ahead of the first realignment: result word m is the funnel shift of
-// words k+m and k+m+1 (k = ph / 2) right by 16 * (ph & 1) bits, the words
-// picked by two rounds of selects (by 2 words, then by 1).
-__device__ __forceinline__ uint4 realign8(const uint4& b0, const uint4& b1, int ph) {
-    const bool by2 = (ph & 4) != 0, by1 = (ph & 2) != 0;
-    const uint32_t sh = static_cast<uint32_t>(ph & 1) * 16u;
-    const uint32_t t0 = by2 ? b0.z : b0.x, t1 = by2 ? b0.w : b0.y, t2 = by2 ? b1.x : b0.z;
-    const uint32_t t3 = by2 ? b1.y : b0.w, t4 = by2 ? b1.z : b1.x, t5 = by2 ? b1.w : b1.y;
-    const uint32_t v0 = by1 ? t1 : t0, v1 = by1 ? t2 : t1, v2 = by1 ? t3 : t2;
-    const uint32_t v3 = by1 ? t4 : t3, v4 = by1 ? t5 : t4;
-    return make_uint4(__funnelshift_r(v0, v1, sh), __funnelshift_r(v1, v2, sh),
-                      __funnelshift_r(v2, v3, sh), __funnelshift_r(v3, v4, sh));
-}
-
-// 8 consecutive bf16 values at p, element phase ph != 0, read as the two
-// aligned 16-byte blocks around them (through the read-only path, so the
-// block a neighbouring thread also reads is served from L1).  The caller
-// guarantees that both blocks lie inside the valid range: the 8 elements
-// before p and the 16 from p on.
-__device__ __forceinline__ uint4 ld8_window(const uint16_t* p, int ph) {
-    const uint16_t* a = p - ph;
-    const uint4 b0 = __ldg(reinterpret_cast<const uint4*>(a));
-    const uint4 b1 = __ldg(reinterpret_cast<const uint4*>(a + 8));
-    return realign8(b0, b1, ph);
 }
 
 // 8 consecutive bf16 values stored at an address of element phase ph.
@@ -225,11 +198,29 @@ __device__ __forceinline__ float reduce1(const StreamArgs& a, int64_t off) {
     return __fmul_rn(s, a.sc.inv_nd);
 }
 
-template <int MODE, int ND, int GT>
+// The modes that reduce the ranks' gradients.
+template <int MODE>
+__host__ __device__ constexpr bool reduces() {
+    return MODE == kFused || MODE == kFusedRep || MODE == kFusedQ || MODE == kReduce ||
+           MODE == kNorm || MODE == kReduceNorm;
+}
+template <int MODE>
+__host__ __device__ constexpr bool sums_squares() {
+    return MODE == kNorm || MODE == kReduceNorm;
+}
+
+// The factor of the scaled steps, read where it is used: held from the kernel's
+// start on, its register makes the fused step of eight ranks spill.
+__device__ __forceinline__ float gradient_scale(const StreamArgs& a) {
+    return *static_cast<const volatile float*>(a.scale);
+}
+
+template <int MODE, int ND, int GT, bool SCALED>
 __device__ __forceinline__ void vector_chunk(const StreamArgs& a, const Span& sp, int64_t i0,
                                              float* hq, bool warp_store) {
-    float g[8];
-    if constexpr (MODE == kFused || MODE == kFusedRep || MODE == kFusedQ || MODE == kReduce) {
+    float own[8];
+    float* g = sums_squares<MODE>() ? hq : own;
+    if constexpr (reduces<MODE>()) {
         // blocks of a phased chunk: local [i0 - ph, i0 - ph + 16) within [i0 - 8, i0 + 16)
         const bool window = i0 - 8 >= sp.lo && i0 + 16 <= sp.hi;
         reduce8<ND>(a, sp.gofs + i0, sp.gphase, window, g);
@@ -238,7 +229,8 @@ __device__ __forceinline__ void vector_chunk(const StreamArgs& a, const Span& sp
         unpack8(ldcs16(static_cast<const uint16_t*>(sp.in) + i0), hq);
         return;
     }
-    if constexpr (MODE == kReduce) {
+    if constexpr (MODE == kNorm) return;
+    if constexpr (MODE == kReduce || MODE == kReduceNorm) {
         if constexpr (GT == ZERO3_BF16) {
             stcs16(static_cast<uint16_t*>(sp.out) + i0, pack8(g));
         } else {
@@ -248,7 +240,7 @@ __device__ __forceinline__ void vector_chunk(const StreamArgs& a, const Span& sp
         }
         return;
     }
-    if constexpr (MODE == kAdam) {
+    if constexpr (MODE == kAdam || MODE == kAdamFull) {
         if constexpr (GT == ZERO3_BF16) {
             unpack8(ldcs16(static_cast<const uint16_t*>(sp.in) + i0), g);
         } else {
@@ -257,6 +249,11 @@ __device__ __forceinline__ void vector_chunk(const StreamArgs& a, const Span& sp
             g[0] = g0.x; g[1] = g0.y; g[2] = g0.z; g[3] = g0.w;
             g[4] = g1.x; g[5] = g1.y; g[6] = g1.z; g[7] = g1.w;
         }
+    }
+    if constexpr (SCALED) {
+        const float scale = gradient_scale(a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = __fmul_rn(g[e], scale);
     }
     float p[8];
     if constexpr (MODE == kCast) {
@@ -308,33 +305,35 @@ __device__ __forceinline__ void vector_chunk(const StreamArgs& a, const Span& sp
     }
 }
 
-template <int MODE, int ND, int GT>
+template <int MODE, int ND, int GT, bool SCALED>
 __device__ __forceinline__ void scalar_chunk(const StreamArgs& a, const Span& sp, int64_t i0,
                                              float* hq) {
     for (int e = 0; e < 8; ++e) {
         const int64_t i = i0 + e;
-        if constexpr (MODE == kFusedQ || MODE == kQuant) hq[e] = 0.0f;
+        if constexpr (MODE == kFusedQ || MODE == kQuant || sums_squares<MODE>()) hq[e] = 0.0f;
         if (i < sp.lo || i >= sp.hi) continue;
         if constexpr (MODE == kQuant) {
             hq[e] = bf16_f32(static_cast<const uint16_t*>(sp.in)[i]);
             continue;
         }
         float g = 0.0f;
-        if constexpr (MODE == kFused || MODE == kFusedRep || MODE == kFusedQ || MODE == kReduce)
-            g = reduce1<ND>(a, sp.gofs + i);
-        if constexpr (MODE == kReduce) {
+        if constexpr (reduces<MODE>()) g = reduce1<ND>(a, sp.gofs + i);
+        if constexpr (sums_squares<MODE>()) hq[e] = g;
+        if constexpr (MODE == kNorm) continue;
+        if constexpr (MODE == kReduce || MODE == kReduceNorm) {
             if constexpr (GT == ZERO3_BF16)
                 static_cast<uint16_t*>(sp.out)[i] = to_bf16(g);
             else
                 static_cast<float*>(sp.out)[i] = g;
             continue;
         }
-        if constexpr (MODE == kAdam) {
+        if constexpr (MODE == kAdam || MODE == kAdamFull) {
             if constexpr (GT == ZERO3_BF16)
                 g = bf16_f32(static_cast<const uint16_t*>(sp.in)[i]);
             else
                 g = static_cast<const float*>(sp.in)[i];
         }
+        if constexpr (SCALED) g = __fmul_rn(g, gradient_scale(a));
         float p;
         if constexpr (MODE == kCast) {
             p = static_cast<const float*>(sp.in)[i];
@@ -404,6 +403,39 @@ __device__ __forceinline__ void qwz_block(const Span& sp, int64_t i0, const floa
     }
 }
 
+// Epilogue of the norm modes: the sum of squares of the block's reduced
+// gradients.  A warp takes its largest magnitude to [1, 2) by a power of two
+// before it squares, so no square overflows, and those that vanish are 2^-126 of
+// the largest one; the eight warps are joined in binary64, in their order.
+// Every thread of the block calls it.
+__device__ __forceinline__ void block_squares(const float* g, double* partial) {
+    __shared__ double sh[kThreads / 32];
+    float mx = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(g[e]));  // drops a NaN: its square stays
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(mx)) >> 23;
+    const int sb = top > 253u ? 1 : (top < 1u ? 253 : 254 - static_cast<int>(top));
+    const float up = __uint_as_float(static_cast<uint32_t>(sb) << 23);  // 2^(sb - 127)
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = __fmul_rn(g[e], up);
+        s = fmaf(x, x, s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+    if ((threadIdx.x & 31) == 0)
+        sh[threadIdx.x >> 5] = static_cast<double>(s) *
+            __hiloint2double((1023 + 2 * (127 - sb)) << 20, 0);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double d = sh[0];
+#pragma unroll
+        for (int w = 1; w < kThreads / 32; ++w) d += sh[w];
+        partial[blockIdx.x] = d;
+    }
+}
+
 // Resident blocks of 256 threads per SM that the register allocation must
 // allow.  The modes that reduce gradients with a compile-time rank count keep
 // 4 (at most 64 registers a thread): the ZeRO-1/2 step at N_d = 8 otherwise
@@ -411,17 +443,19 @@ __device__ __forceinline__ void qwz_block(const Span& sp, int64_t i0, const floa
 // them spills.
 template <int MODE, int ND>
 __host__ __device__ constexpr int min_blocks_per_sm() {
-    return (ND > 0 && (MODE == kFused || MODE == kFusedRep || MODE == kFusedQ ||
-                       MODE == kReduce))
-               ? 4
-               : 1;
+    return (ND > 0 && reduces<MODE>()) ? 4 : 1;
 }
 
-template <int MODE, int ND, int GT>
+template <int MODE, int ND, int GT, bool SCALED>
 __global__ void __launch_bounds__(kThreads, min_blocks_per_sm<MODE, ND>())
     stream_kernel(const __grid_constant__ StreamArgs a) {
     wait_prior_grids();
     allow_next_grid();
+    float sq[8];  // norm modes: the thread's chunk
+    if constexpr (sums_squares<MODE>()) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq[e] = 0.0f;
+    }
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     int s = 0;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -435,14 +469,16 @@ __global__ void __launch_bounds__(kThreads, min_blocks_per_sm<MODE, ND>())
             while (s + 1 < a.n_spans && c >= a.span[s + 1].chunk0) ++s;
             const Span& sp = a.span[s];
             const int64_t i0 = (sp.lo & ~static_cast<int64_t>(7)) + ((c - sp.chunk0) << 3);
-            float hq[8];
+            float own[8];
+            float* hq = sums_squares<MODE>() ? sq : own;
             const bool vec = i0 >= sp.lo && i0 + 8 <= sp.hi;
             // A phased all-gather stream is stored by the whole warp at once
             // when its 32 lanes hold vector chunks of one span (a
             // warp-uniform decision: every active lane takes part in it, and
             // a partial or diverged warp keeps the per-lane stores).
             bool warp_store = false;
-            if constexpr (MODE == kFused || MODE == kFusedRep || MODE == kFusedQ) {
+            if constexpr (MODE == kFused || MODE == kFusedRep || MODE == kFusedQ ||
+                          MODE == kAdamFull) {
                 const unsigned active = __activemask();
                 if (active == 0xffffffffu) {
                     const int s0 = __shfl_sync(0xffffffffu, s, 0);
@@ -451,13 +487,16 @@ __global__ void __launch_bounds__(kThreads, min_blocks_per_sm<MODE, ND>())
                 }
             }
             if (vec)
-                vector_chunk<MODE, ND, GT>(a, sp, i0, hq, warp_store);
+                vector_chunk<MODE, ND, GT, SCALED>(a, sp, i0, hq, warp_store);
             else
-                scalar_chunk<MODE, ND, GT>(a, sp, i0, hq);
+                scalar_chunk<MODE, ND, GT, SCALED>(a, sp, i0, hq);
             if constexpr (MODE == kFusedQ || MODE == kQuant)
                 qwz_block<GT == 4 ? 4 : 8>(sp, i0, hq);
         }
+        // one sum per block: the caller keeps such a launch within one grid
+        if constexpr (sums_squares<MODE>()) break;
     }
+    if constexpr (sums_squares<MODE>()) block_squares(sq, a.partial);
 }
 
 // The grid covers every chunk once (the grid-stride loop in the kernels only
@@ -472,47 +511,60 @@ int grid_for(int64_t total_chunks, int chunks_per_thread = 1) {
     return static_cast<int>(need < cap ? need : cap);
 }
 
-template <int MODE, int ND, int GT>
+template <int MODE, int ND, int GT, bool SCALED = false>
 cudaError_t launch_one(const StreamArgs& a, cudaStream_t stream) {
     const int grid = grid_for(a.total_chunks);
     if (grid <= 0) return cudaSuccess;
-    return launch_programmatic(stream_kernel<MODE, ND, GT>, grid, a, stream);
+    return launch_programmatic(stream_kernel<MODE, ND, GT, SCALED>, grid, a, stream);
 }
 
-template <int MODE, int GT>
+template <int MODE, int GT, bool SCALED = false>
 cudaError_t launch_nd(const StreamArgs& a, cudaStream_t stream) {
     switch (a.nd) {
-        case 1: return launch_one<MODE, 1, GT>(a, stream);
-        case 2: return launch_one<MODE, 2, GT>(a, stream);
-        case 3: return launch_one<MODE, 3, GT>(a, stream);
-        case 4: return launch_one<MODE, 4, GT>(a, stream);
-        case 5: return launch_one<MODE, 5, GT>(a, stream);
-        case 6: return launch_one<MODE, 6, GT>(a, stream);
-        case 7: return launch_one<MODE, 7, GT>(a, stream);
-        case 8: return launch_one<MODE, 8, GT>(a, stream);
-        default: return launch_one<MODE, 0, GT>(a, stream);
+        case 1: return launch_one<MODE, 1, GT, SCALED>(a, stream);
+        case 2: return launch_one<MODE, 2, GT, SCALED>(a, stream);
+        case 3: return launch_one<MODE, 3, GT, SCALED>(a, stream);
+        case 4: return launch_one<MODE, 4, GT, SCALED>(a, stream);
+        case 5: return launch_one<MODE, 5, GT, SCALED>(a, stream);
+        case 6: return launch_one<MODE, 6, GT, SCALED>(a, stream);
+        case 7: return launch_one<MODE, 7, GT, SCALED>(a, stream);
+        case 8: return launch_one<MODE, 8, GT, SCALED>(a, stream);
+        default: return launch_one<MODE, 0, GT, SCALED>(a, stream);
     }
+}
+
+template <bool SCALED>
+cudaError_t launch_step(int mode, const StreamArgs& a, cudaStream_t stream) {
+    if (mode == kFused) return launch_nd<kFused, 0, SCALED>(a, stream);
+    if (mode == kFusedRep) return launch_nd<kFusedRep, 0, SCALED>(a, stream);
+    // qwZ: the template's GT carries the code width (8 or 4 bits)
+    return a.dtype == 4 ? launch_nd<kFusedQ, 4, SCALED>(a, stream)
+                        : launch_nd<kFusedQ, 8, SCALED>(a, stream);
 }
 
 }  // namespace
 
+int64_t stream_blocks(int64_t total_chunks) { return grid_for(total_chunks); }
+
 cudaError_t launch_stream(int mode, const StreamArgs& a, cudaStream_t stream) {
     if (a.total_chunks <= 0) return cudaSuccess;
     switch (mode) {
-        case kFused: return launch_nd<kFused, 0>(a, stream);
-        case kFusedRep: return launch_nd<kFusedRep, 0>(a, stream);
-        // qwZ modes: the template's GT carries the code width (8 or 4 bits)
+        case kFused:
+        case kFusedRep:
         case kFusedQ:
-            return a.dtype == 4 ? launch_nd<kFusedQ, 4>(a, stream) : launch_nd<kFusedQ, 8>(a, stream);
+            return a.scale ? launch_step<true>(mode, a, stream) : launch_step<false>(mode, a, stream);
         case kQuant:
             return a.dtype == 4 ? launch_one<kQuant, 1, 4>(a, stream)
                                 : launch_one<kQuant, 1, 8>(a, stream);
         case kReduce:
             return a.dtype == ZERO3_BF16 ? launch_nd<kReduce, ZERO3_BF16>(a, stream)
                                          : launch_nd<kReduce, ZERO3_F32>(a, stream);
+        case kNorm: return launch_nd<kNorm, ZERO3_F32>(a, stream);
+        case kReduceNorm: return launch_nd<kReduceNorm, ZERO3_F32>(a, stream);
         case kAdam:
             return a.dtype == ZERO3_BF16 ? launch_one<kAdam, 1, ZERO3_BF16>(a, stream)
                                          : launch_one<kAdam, 1, ZERO3_F32>(a, stream);
+        case kAdamFull: return launch_one<kAdamFull, 1, ZERO3_F32, true>(a, stream);
         case kCast: return launch_one<kCast, 1, 0>(a, stream);
     }
     return cudaErrorInvalidValue;

@@ -77,6 +77,49 @@ struct DistillArgs {
     int32_t map_bytes;     // of the map of listed tokens (set by the launch)
 };
 
+// Gradient tensors, cut into blocks of `per` 8-element chunks; a launch takes
+// up to MAXT of them.  Every tensor has a block at least, so that its norm is
+// written; block0[i] is the first block of tensor i in the launch.
+constexpr int kSmallList = 64, kLargeList = 1024;
+template <int MAXT>
+struct ListArgs {
+    const void* x[MAXT];
+    void* out[MAXT];       // clipping only
+    int64_t numel[MAXT];
+    uint32_t block0[MAXT + 1];
+    int32_t count;
+    int64_t per;
+    double* partial;       // norms: a sum of squares per block, from this launch's first block on
+    int32_t* start;        // norms: number of the first block of each tensor
+    int32_t first;         // of this launch's blocks
+    const float* scale;    // clipping: the factor
+};
+
+// Sums of squares -> norms and the clipping coefficient.
+struct NormArgs {
+    const double* partial;  // n sums of blocks
+    int64_t n;
+    const double* folded;   // the same in fewer numbers
+    int64_t n_folded;
+    const int32_t* start;   // first block of each tensor
+    int64_t n_tensors;
+    float* tensor_norms;
+    double* square_sum;
+    float* norm;
+    float* coef;
+    float max_norm;
+    int32_t accumulate;     // *square_sum is added to
+};
+// Sums of more blocks than this are folded by a kernel of their own first.
+constexpr int64_t kFoldAbove = 16384;
+constexpr int kFoldBlocks = 1024;
+
+// Blocks of one gradient tensor.
+inline int64_t list_blocks(int64_t numel, int64_t per) {
+    const int64_t b = (numel / 8 + per - 1) / per;
+    return b < 1 ? 1 : b;
+}
+
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t stream);
@@ -85,5 +128,12 @@ cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t stream);
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, cudaStream_t stream);
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
 cudaError_t launch_distill_grad(const DistillArgs& a, cudaStream_t stream);
+cudaError_t launch_list_norm(const ListArgs<kSmallList>& a, int dtype, cudaStream_t stream);
+cudaError_t launch_list_norm(const ListArgs<kLargeList>& a, int dtype, cudaStream_t stream);
+cudaError_t launch_list_scale(const ListArgs<kSmallList>& a, int dtype, int out_dtype, cudaStream_t stream);
+cudaError_t launch_list_scale(const ListArgs<kLargeList>& a, int dtype, int out_dtype, cudaStream_t stream);
+// Folds a.partial into `to` (kFoldBlocks numbers) if there are many, then
+// writes the norms.
+cudaError_t launch_norms(NormArgs a, double* to, cudaStream_t stream);
 
 }  // namespace z3

@@ -155,6 +155,32 @@ _SIGS = [
     ("zero3_distill_backward", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, _vp,
                                          C.c_int, _vp, C.c_int, C.c_int32, C.c_int64, C.c_float,
                                          _vp, _vp, _vp, C.c_int64, _vp]),
+    ("zero3_step_scaled", C.c_int, [_vp, C.POINTER(AdamWHparams), C.c_int64, C.POINTER(_vp),
+                                    C.c_int64, C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp),
+                                    C.POINTER(_vp), _vp, C.POINTER(PersistState), C.c_int64,
+                                    C.c_int64, _vp, _vp]),
+    ("zero3_step_stage12_scaled", C.c_int, [_vp, C.POINTER(AdamWHparams), C.c_int64,
+                                            C.POINTER(_vp), C.c_int64, C.POINTER(_vp),
+                                            C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp),
+                                            C.c_int64, C.c_int64, _vp, _vp]),
+    ("zero3_step_qwz_scaled", C.c_int, [_vp, C.POINTER(AdamWHparams), C.c_int64, C.POINTER(_vp),
+                                        C.c_int64, C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp),
+                                        C.POINTER(_vp), C.c_int32, C.POINTER(_vp), C.POINTER(_vp),
+                                        C.POINTER(PersistState), C.c_int64, C.c_int64, _vp, _vp]),
+    ("zero3_grad_square_sum_workspace", C.c_int, [_vp, C.c_int64, C.c_int64, _c_i64_p]),
+    ("zero3_grad_square_sum", C.c_int, [_vp, C.POINTER(_vp), C.c_int64, C.POINTER(_vp), C.c_int64,
+                                        C.c_int64, C.c_int32, _vp, _vp, C.c_int64, _vp]),
+    ("zero3_clip_coefficient", C.c_int, [_vp, C.c_float, _vp, _vp, _vp]),
+    ("zero3_step_clipped_workspace", C.c_int, [_vp, C.c_int64, C.c_int64, _c_i64_p, _c_i64_p]),
+    ("zero3_step_clipped", C.c_int, [_vp, C.POINTER(AdamWHparams), C.c_int64, C.POINTER(_vp),
+                                     C.c_int64, C.POINTER(_vp), C.POINTER(_vp), C.POINTER(_vp),
+                                     C.POINTER(_vp), _vp, C.POINTER(PersistState), C.c_int64,
+                                     C.c_int64, C.c_float, _vp, _vp, C.c_int64, _vp]),
+    ("zero3_grad_norm_workspace", C.c_int, [_c_i64_p, C.c_int64, _c_i64_p]),
+    ("zero3_grad_norm", C.c_int, [C.POINTER(_vp), _c_i64_p, C.c_int64, C.c_int, C.c_float, _vp, _vp,
+                                  _vp, _vp, _vp, C.c_int64, _vp]),
+    ("zero3_clip_grads", C.c_int, [C.POINTER(_vp), _c_i64_p, C.c_int64, C.c_int, _vp,
+                                   C.POINTER(_vp), C.c_int, _vp]),
     ("zero3_plan_memory_bytes", C.c_int, [_vp, C.c_int32, C.POINTER(C.c_double)]),
     ("zero3_memory_bytes", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.POINTER(C.c_double)]),
     ("zero3_comm_elems", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.POINTER(C.c_double)]),
@@ -503,6 +529,102 @@ def zero3_distill_backward(logits, dtype, n, vocab, stride, teacher_logits, teac
                                          teacher_dtype, teacher_ids, id_type, k, teacher_stride,
                                          inv_temperature, lse, dloss, dlogits, dlogits_stride,
                                          stream), "zero3_distill_backward")
+
+
+class TensorList:
+    """The device pointers and element counts of gradient tensors of one dtype, as
+    host arrays that calls read."""
+
+    def __init__(self, pointers: Sequence[int], numels: Sequence[int], dtype: int):
+        if len(pointers) != len(numels):
+            raise ValueError("one pointer per tensor")
+        self.n, self.dtype = len(numels), dtype
+        self.pointers = _ptrs(pointers)
+        self.numels = (C.c_int64 * self.n)(*numels)
+
+
+def zero3_grad_norm_workspace(tensors: TensorList) -> int:
+    out = C.c_int64()
+    _check(load().zero3_grad_norm_workspace(tensors.numels, tensors.n, C.byref(out)),
+           "zero3_grad_norm_workspace")
+    return out.value
+
+
+def zero3_grad_norm(tensors: TensorList, max_norm, tensor_norms, square_sum, norm, coef, workspace,
+                    workspace_bytes, stream=0):
+    _check(load().zero3_grad_norm(tensors.pointers, tensors.numels, tensors.n, tensors.dtype, max_norm,
+                                  tensor_norms, square_sum, norm, coef, workspace, workspace_bytes,
+                                  stream), "zero3_grad_norm")
+
+
+def zero3_clip_grads(tensors: TensorList, coef, out: Optional[TensorList] = None, stream=0):
+    """out: tensors of the same sizes; None: in place."""
+    if out is not None and (out.n != tensors.n or bytes(out.numels) != bytes(tensors.numels)):
+        raise ValueError("the outputs' sizes are not the tensors'")
+    _check(load().zero3_clip_grads(tensors.pointers, tensors.numels, tensors.n, tensors.dtype, coef,
+                                   out.pointers if out is not None else None,
+                                   out.dtype if out is not None else tensors.dtype, stream),
+           "zero3_clip_grads")
+
+
+def zero3_grad_square_sum_workspace(plan: Plan, lo, hi) -> int:
+    out = C.c_int64()
+    _check(plan._lib.zero3_grad_square_sum_workspace(plan.handle, lo, hi, C.byref(out)),
+           "zero3_grad_square_sum_workspace")
+    return out.value
+
+
+def zero3_grad_square_sum(plan: Plan, grads, grads_origin, persist_grads, lo, hi, accumulate,
+                          square_sum, workspace, workspace_bytes, stream=0):
+    _check(plan._lib.zero3_grad_square_sum(plan.handle, _ptrs(grads), grads_origin,
+                                           _ptrs(persist_grads), lo, hi, accumulate, square_sum,
+                                           workspace, workspace_bytes, stream),
+           "zero3_grad_square_sum")
+
+
+def zero3_clip_coefficient(square_sum, max_norm, norm, coef, stream=0):
+    _check(load().zero3_clip_coefficient(square_sum, max_norm, norm, coef, stream),
+           "zero3_clip_coefficient")
+
+
+def zero3_step_clipped_workspace(plan: Plan, lo, hi) -> tuple:
+    """(least, best) bytes."""
+    least, best = C.c_int64(), C.c_int64()
+    _check(plan._lib.zero3_step_clipped_workspace(plan.handle, lo, hi, C.byref(least),
+                                                  C.byref(best)), "zero3_step_clipped_workspace")
+    return least.value, best.value
+
+
+def zero3_step_clipped(plan: Plan, hp, t, grads, grads_origin, master, m, v, sparam, full, persist,
+                       flat_lo, flat_hi, max_norm, norm, workspace, workspace_bytes, stream=0):
+    _check(plan._lib.zero3_step_clipped(plan.handle, C.byref(hp), t, _ptrs(grads), grads_origin,
+                                        _ptrs(master), _ptrs(m), _ptrs(v), _ptrs(sparam), full,
+                                        _ps_ref(persist), flat_lo, flat_hi, max_norm, norm,
+                                        workspace, workspace_bytes, stream), "zero3_step_clipped")
+
+
+def zero3_step_scaled(plan: Plan, hp, t, grads, grads_origin, master, m, v, sparam, full, persist,
+                      flat_lo, flat_hi, scale, stream=0):
+    _check(plan._lib.zero3_step_scaled(plan.handle, C.byref(hp), t, _ptrs(grads), grads_origin,
+                                       _ptrs(master), _ptrs(m), _ptrs(v), _ptrs(sparam), full,
+                                       _ps_ref(persist), flat_lo, flat_hi, scale, stream),
+           "zero3_step_scaled")
+
+
+def zero3_step_stage12_scaled(plan: Plan, hp, t, grads, grads_origin, master, m, v, params, flat_lo,
+                              flat_hi, scale, stream=0):
+    _check(plan._lib.zero3_step_stage12_scaled(plan.handle, C.byref(hp), t, _ptrs(grads),
+                                               grads_origin, _ptrs(master), _ptrs(m), _ptrs(v),
+                                               _ptrs(params), flat_lo, flat_hi, scale, stream),
+           "zero3_step_stage12_scaled")
+
+
+def zero3_step_qwz_scaled(plan: Plan, hp, t, grads, grads_origin, master, m, v, sparam, codes,
+                          scales, persist, flat_lo, flat_hi, scale, stream=0, bits=8):
+    _check(plan._lib.zero3_step_qwz_scaled(plan.handle, C.byref(hp), t, _ptrs(grads), grads_origin,
+                                           _ptrs(master), _ptrs(m), _ptrs(v), _ptrs(sparam), bits,
+                                           _ptrs(codes), _ptrs(scales), _ps_ref(persist), flat_lo,
+                                           flat_hi, scale, stream), "zero3_step_qwz_scaled")
 
 
 def zero3_plan_memory_bytes(plan: Plan, stage) -> float:
