@@ -660,6 +660,7 @@ typedef enum zero3_itype { ZERO3_I32 = 0, ZERO3_I64 = 1 } zero3_itype;
 
 #define ZERO3_MAX_TOP 64
 #define ZERO3_MAX_TEACHER 1024
+#define ZERO3_MAX_DRAFT 256
 
 /* Embedding lookup with scaling: out[i, :] = scale * table[ids[i], :] for
  * i < n, `dim` columns; an ignored position's row is zero. */
@@ -764,6 +765,44 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
                                     zero3_itype id_type, int32_t k, int64_t teacher_stride,
                                     float inv_temperature, const float* lse, const float* dloss,
                                     void* dlogits, int64_t dlogits_stride, zero3_stream stream);
+
+/* Verification of drafted tokens, or with k = 0 sampling.  Sequence s has up to k
+ * drafted tokens draft_ids[s, 0..k-1]; the first ignored id ends its draft (length
+ * L).  Its target logits are rows s * (k + 1) + j of `logits`, j = 0..k (row j
+ * follows j drafted tokens), those of the draft model rows s * k + j of
+ * draft_logits.  With p_j = softmax(inv_temperature * logits), q_j =
+ * softmax(draft_inv_temperature * draft_logits), or q_j = 1 at the drafted token
+ * alone where draft_logits is NULL (tokens proposed without probabilities):
+ *   token j is accepted iff log u + log q_j(d_j) < log p_j(d_j), u = uniform[s, j]
+ *     in [0, 1), and every one before it was; A = the number accepted;
+ *   the next token is drawn from the residual max(p_A - q_A, 0) after a refusal,
+ *     from p_A after a whole draft (A = L): the token with the largest
+ *     residual / e, e = noise[s, token], ties to the lowest index.  With e drawn
+ *     from the exponential distribution (mean 1) that is a draw in proportion to the
+ *     residual, and the emitted tokens are distributed as the target's.
+ * accepted [n]: A.  tokens [n, k + 1]: the accepted tokens, the drawn one, then -1.
+ * logprobs [n, k + 1] (optional): log p_j of those tokens, 0 behind them.
+ * The answer is that of exact arithmetic on the given numbers: binary32 decides where
+ * it is certain, closer decisions are taken again with weights of 31 bits or more.
+ *  - Tokens whose e is negative or NaN, or whose probability is below 2^-126 of
+ *    the row's largest, are not drawn; e = 0 wins over every e > 0 where the
+ *    residual is positive.  Where no token has a positive residual the draw is
+ *    from p_A.
+ *  - Masked tokens are -inf logits.  A target row without any token accepts
+ *    nothing and draws -1 (log probability -inf), a draft row without any has
+ *    q = 0.  A NaN or +inf logit in a target row, or in a draft row that refuses,
+ *    makes the drawn token -1 with a NaN log probability; in a draft row it refuses
+ *    the token.
+ * uniform [n, k], noise [n, vocab] with noise_stride; logits and draft_logits with
+ * their strides.  draft_ids and uniform may be NULL when k = 0.  EINVAL also for k
+ * outside [0, ZERO3_MAX_DRAFT] and n * (k + 1) above 2^27. */
+zero3_status zero3_verify_draft(const void* logits, zero3_dtype dtype, int64_t n, int32_t k,
+                                int64_t vocab, int64_t stride, const void* draft_logits,
+                                zero3_dtype draft_dtype, int64_t draft_stride,
+                                const void* draft_ids, zero3_itype id_type, float inv_temperature,
+                                float draft_inv_temperature, const float* uniform,
+                                const float* noise, int64_t noise_stride, int32_t* accepted,
+                                int32_t* tokens, float* logprobs, zero3_stream stream);
 
 /* ------------------------------------------------------------- accounting */
 

@@ -30,7 +30,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC"
 LIBS = {
     "libzero3.so": ["plan.cpp", "api.cpp", "checkpoint.cpp", "coordinator.cpp", "kernels.cu",
                     "pieces.cu", "operators.cpp", "embedding.cu", "logprobs.cu", "distill.cu",
-                    "clip.cpp", "clip.cu"],
+                    "clip.cpp", "clip.cu", "verify.cu"],
     "libzero3_synth.so": ["synth.cu"],
 }
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "device_common.cuh"),

@@ -274,4 +274,50 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
     return cuda_status(z3::launch_distill_grad(a, stream));
 }
 
+zero3_status zero3_verify_draft(const void* logits, zero3_dtype dtype, int64_t n, int32_t k,
+                                int64_t vocab, int64_t stride, const void* draft_logits,
+                                zero3_dtype draft_dtype, int64_t draft_stride,
+                                const void* draft_ids, zero3_itype id_type, float inv_temperature,
+                                float draft_inv_temperature, const float* uniform,
+                                const float* noise, int64_t noise_stride, int32_t* accepted,
+                                int32_t* tokens, float* logprobs, zero3_stream stream) {
+    if (!dtype_ok(dtype) || !itype_ok(id_type) || k < 0 || k > ZERO3_MAX_DRAFT || n < 0 ||
+        n > kMaxRows / (k + 1) || !logits_ok(n * (k + 1), vocab, stride) ||
+        !positive(inv_temperature) || noise_stride < vocab)
+        return ZERO3_EINVAL;
+    const bool draft = k > 0 && draft_logits;
+    if (draft && (!dtype_ok(draft_dtype) || !logits_ok(n * k, vocab, draft_stride) ||
+                  !positive(draft_inv_temperature)))
+        return ZERO3_EINVAL;
+    if (n == 0) return ZERO3_OK;
+    if (!ptr_ok(logits, size_of(dtype)) || !ptr_ok(noise, 4) || !ptr_ok(accepted, 4) ||
+        !ptr_ok(tokens, 4) || !opt_ok(logprobs, 4))
+        return ZERO3_EINVAL;
+    if (draft && !ptr_ok(draft_logits, size_of(draft_dtype))) return ZERO3_EINVAL;
+    if (k > 0 && (!ptr_ok(draft_ids, size_of(id_type)) || !ptr_ok(uniform, 4))) return ZERO3_EINVAL;
+    z3::VerifyArgs a;
+    a.x = logits;
+    a.y = draft ? draft_logits : nullptr;
+    a.ids = draft_ids;
+    a.uniform = uniform;
+    a.noise = noise;
+    a.accepted = accepted;
+    a.tokens = tokens;
+    a.logprobs = logprobs;
+    a.n = n;
+    a.stride = stride;
+    a.y_stride = draft_stride;
+    a.noise_stride = noise_stride;
+    a.vocab = static_cast<int32_t>(vocab);
+    a.k = k;
+    a.scale = inv_temperature;
+    a.y_scale = draft ? draft_inv_temperature : 1.0f;
+    a.dtype = dtype;
+    a.y_dtype = draft ? draft_dtype : dtype;
+    a.id64 = id_type == ZERO3_I64;
+    a.cluster = 1;
+    a.ahead = 1;
+    return cuda_status(z3::launch_verify(a, stream));
+}
+
 }  // extern "C"

@@ -120,6 +120,22 @@ inline int64_t list_blocks(int64_t numel, int64_t per) {
     return b < 1 ? 1 : b;
 }
 
+struct VerifyArgs {
+    const void* x;
+    const void* y;          // draft logits, or null: the draft is certain of its tokens
+    const void* ids;
+    const float* uniform;
+    const float* noise;
+    int32_t* accepted;
+    int32_t* tokens;
+    float* logprobs;
+    int64_t n, stride, y_stride, noise_stride;
+    int32_t vocab, k;
+    float scale, y_scale;
+    int32_t dtype, y_dtype, id64;
+    int32_t cluster, ahead;  // blocks per sequence, positions per round (set by the launch)
+};
+
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t stream);
@@ -135,5 +151,6 @@ cudaError_t launch_list_scale(const ListArgs<kLargeList>& a, int dtype, int out_
 // Folds a.partial into `to` (kFoldBlocks numbers) if there are many, then
 // writes the norms.
 cudaError_t launch_norms(NormArgs a, double* to, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 
 }  // namespace z3

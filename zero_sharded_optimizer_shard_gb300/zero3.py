@@ -23,6 +23,7 @@ NOT_AVAILABLE, INFLIGHT, AVAILABLE = 0, 1, 2
 MAX_RANKS = 64
 MAX_TOP = 64
 MAX_TEACHER = 1024
+MAX_DRAFT = 256
 
 _c_i64_p = C.POINTER(C.c_int64)
 _c_i32_p = C.POINTER(C.c_int32)
@@ -181,6 +182,9 @@ _SIGS = [
                                   _vp, _vp, _vp, C.c_int64, _vp]),
     ("zero3_clip_grads", C.c_int, [C.POINTER(_vp), _c_i64_p, C.c_int64, C.c_int, _vp,
                                    C.POINTER(_vp), C.c_int, _vp]),
+    ("zero3_verify_draft", C.c_int, [_vp, C.c_int, C.c_int64, C.c_int32, C.c_int64, C.c_int64, _vp,
+                                     C.c_int, C.c_int64, _vp, C.c_int, C.c_float, C.c_float, _vp,
+                                     _vp, C.c_int64, _vp, _vp, _vp, _vp]),
     ("zero3_plan_memory_bytes", C.c_int, [_vp, C.c_int32, C.POINTER(C.c_double)]),
     ("zero3_memory_bytes", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.POINTER(C.c_double)]),
     ("zero3_comm_elems", C.c_int, [C.c_int32, C.c_double, C.c_int32, C.POINTER(C.c_double)]),
@@ -625,6 +629,15 @@ def zero3_step_qwz_scaled(plan: Plan, hp, t, grads, grads_origin, master, m, v, 
                                            _ptrs(master), _ptrs(m), _ptrs(v), _ptrs(sparam), bits,
                                            _ptrs(codes), _ptrs(scales), _ps_ref(persist), flat_lo,
                                            flat_hi, scale, stream), "zero3_step_qwz_scaled")
+
+
+def zero3_verify_draft(logits, dtype, n, k, vocab, stride, draft_logits, draft_dtype, draft_stride,
+                       draft_ids, id_type, inv_temperature, draft_inv_temperature, uniform, noise,
+                       noise_stride, accepted, tokens, logprobs=0, stream=0):
+    _check(load().zero3_verify_draft(logits, dtype, n, k, vocab, stride, draft_logits, draft_dtype,
+                                     draft_stride, draft_ids, id_type, inv_temperature,
+                                     draft_inv_temperature, uniform, noise, noise_stride, accepted,
+                                     tokens, logprobs, stream), "zero3_verify_draft")
 
 
 def zero3_plan_memory_bytes(plan: Plan, stage) -> float:
