@@ -784,10 +784,12 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
  * logprobs [n, k + 1] (optional): log p_j of those tokens, 0 behind them.
  * The answer is that of exact arithmetic on the given numbers: binary32 decides where
  * it is certain, closer decisions are taken again with weights of 31 bits or more.
- *  - Tokens whose e is negative or NaN, or whose probability is below 2^-126 of
- *    the row's largest, are not drawn; e = 0 wins over every e > 0 where the
- *    residual is positive.  Where no token has a positive residual the draw is
- *    from p_A.
+ *  - Tokens whose e is negative (-0 too), NaN or infinite, or whose probability is
+ *    below 2^-126 of the row's largest, are not drawn; e = 0 wins over every
+ *    e > 0 where the residual is positive.  Where no token has a positive
+ *    residual the draw is from p_A.  A NaN or negative u refuses.
+ *  - Log probabilities are exact to about 2^-22 of themselves plus 2^-22 (a nearly
+ *    certain token's keeps fewer digits).
  *  - Masked tokens are -inf logits.  A target row without any token accepts
  *    nothing and draws -1 (log probability -inf), a draft row without any has
  *    q = 0.  A NaN or +inf logit in a target row, or in a draft row that refuses,

@@ -134,6 +134,8 @@ struct VerifyArgs {
     float scale, y_scale;
     int32_t dtype, y_dtype, id64;
     int32_t cluster, ahead;  // blocks per sequence, positions per round (set by the launch)
+    int32_t pd, pr;
+    float sum_error;         // relative, of a row's sum (set by the launch)
 };
 
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);

@@ -6,11 +6,10 @@
 // after a whole draft of p(i) / e_i (an exponential race: a draw from
 // the normalised residual).
 //
-// Bound by HBM where there are many sequences: rows behind the first refusal are
-// not needed, so a sequence's blocks (a cluster of 1 to 8) take its positions in
-// rounds of `ahead` and stop there; the race reads the last round's two rows again
-// from L2, and the noise.  With few sequences the chain of latencies bounds it, and
-// all positions go in one round.
+// Rows behind the first refusal are not needed, so a sequence's blocks (a cluster of
+// 1 to 8, as many as are resident) take its positions in rounds of `ahead` and stop
+// there; in a round each warp has a share of one row.  The race reads the target's
+// row again, mostly from L2, and the noise; of the draft's row only what may win.
 //
 // Decisions.  Weights are binary32, with errors that are bounded as they are
 // formed.  A test or a race closer than its bound is taken again by the same
@@ -25,9 +24,6 @@
 namespace z3 {
 namespace {
 
-constexpr int kNT = 512;
-constexpr int kWarps = kNT / 32;
-
 __device__ __forceinline__ float pos_inf() { return __int_as_float(0x7f800000); }
 
 // 16 bytes to the shared variable at `p` of block `rank` of the cluster.
@@ -36,45 +32,46 @@ __device__ __forceinline__ void send16(uint4* p, uint32_t rank, const uint4& v) 
                  "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
-__device__ __forceinline__ uint4 pack(const Soft& s) {
-    return make_uint4(__float_as_uint(s.m), __float_as_uint(s.mz), __float_as_uint(s.s), 0u);
-}
-__device__ __forceinline__ Soft unpack(const uint4& v) {
-    return Soft{__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), 0.0f};
-}
+
+constexpr int kNT = 256, kWarps = kNT / 32;
 
 // What decides about a drafted token.
 enum Verdict : int { kAccept = 0, kRefuse = 1, kClose = 2, kBroken = 3, kEnd = 4 };
 
 struct Position {
-    Soft p, q;       // statistics of the two rows
+    float pm, ps, qm, qs;  // the two rows' mz and s (Soft)
     float xd, yd;    // the drafted token's logits
     float u;
     int32_t token;
     int32_t verdict;
 };
 
-constexpr int kMaxRows = 16;  // rows per round
+// The 4-byte word of global memory that holds *p, on its way to shared memory,
+// and *p from there.
+template <typename T>
+__device__ __forceinline__ void send_word(uint32_t* to, const T* p) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(at)
+                 : "memory");
+}
+__device__ __forceinline__ float from_word(uint32_t w, const float*) { return __uint_as_float(w); }
+__device__ __forceinline__ float from_word(uint32_t w, const uint16_t* p) {
+    return reinterpret_cast<uintptr_t>(p) & 2 ? bf16_hi(w) : bf16_lo(w);
+}
+// Brings the line at p to L2.
+__device__ __forceinline__ void prefetch_line(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
-struct Shared {
-    uint4 parts[2][kWarps][kMaxCluster];  // what the cluster's warps have sent, by turns
-    Position pos[kMaxRows];
-    int32_t ids[ZERO3_MAX_DRAFT];
-    float lp[ZERO3_MAX_DRAFT];
-};
+constexpr int kMaxPositions = kWarps;  // per round: a warp each
 
-// All of a cluster's warps send 16 bytes to all of its blocks; `turn` numbers the
-// exchanges.  Whoever has come back from exchange t has read what exchange t - 1
-// brought, so two sets of places are enough.
-__device__ __forceinline__ void exchange(Shared& sh, int turn, int C, uint32_t rank, const uint4& v) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (C == 1) {
-        if (lane == 0) sh.parts[turn & 1][warp][0] = v;
-        __syncthreads();
-    } else {
-        if (lane < C) send16(&sh.parts[turn & 1][warp][rank], lane, v);
-        cluster_sync();
-    }
+__device__ __forceinline__ uint4 pack(const Soft& s) {
+    return make_uint4(__float_as_uint(s.mz), __float_as_uint(s.s), 0u, 0u);
+}
+__device__ __forceinline__ Soft unpack(const uint4& v) {
+    return Soft{neg_inf(), __uint_as_float(v.x), __uint_as_float(v.y), 0.0f};
 }
 
 // Thread `tid`'s share, of `nt` threads in each of C blocks, of a row.
@@ -90,10 +87,18 @@ __device__ __forceinline__ void stream_row(Soft& q, const T* row, int32_t V, int
     const bool tail = tid == nt - 1 && rank == C - 1 && cut.tail;
     const T* p = row + cut.head;
     int32_t i = c0 + tid;
-    for (; i + (U - 1) * nt < c1; i += U * nt) {
+    if (i + (U - 1) * nt < c1) {  // the next batch is on its way while one is added
         Chunk<T> c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) c[u].load(p + 8 * static_cast<int64_t>(i + u * nt));
+        for (i += U * nt; i + (U - 1) * nt < c1; i += U * nt) {
+            Chunk<T> d[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) d[u].load(p + 8 * static_cast<int64_t>(i + u * nt));
+            soft_add<T, false, U>(q, c, scale);
+#pragma unroll
+            for (int u = 0; u < U; ++u) c[u] = d[u];
+        }
         soft_add<T, false, U>(q, c, scale);
     }
     for (; i < c1; i += nt) {
@@ -113,28 +118,10 @@ __device__ __forceinline__ void stream_row(Soft& q, const T* row, int32_t V, int
     }
 }
 
-// Joins the parts that warps [w0, w0 + nw) of all blocks have sent; every lane of
-// the calling warp gets the result.
-__device__ __forceinline__ Soft join_rows(const Shared& sh, int turn, int w0, int nw, int C) {
-    const int lane = threadIdx.x & 31;
-    Soft o = soft_empty();
-    for (int i = lane; i < nw * C; i += 32) {
-        Soft s = unpack(sh.parts[turn & 1][w0 + i / C][i % C]);
-        float top = fmaxf(soft_top(o), soft_top(s));
-        if (top == neg_inf()) top = 0.0f;
-        soft_rebase<false>(o, top);
-        soft_rebase<false>(s, top);
-        o.s = __fadd_rn(o.s, s.s);
-        if (top == pos_inf()) o.s = __int_as_float(0x7fffffff);
-    }
-    soft_lanes<false, 32>(o);
-    return o;
-}
-
 // ------------------------------------------------- 31-bit weights, exact sums
-// 2^F for F = n + f / 2^31: y / 2^31 with 0.70 < y / 2^31 < 1.42, from the Taylor
-// series of 2^f = e^(f ln 2), terms (ln 2)^k / k!, k <= 9 (the next is below 8e-12 for
-// |f| <= 1/2), in 31-bit fixed point.
+// 2^(n + f), |f| <= 1/2, as y / 2^31 * 2^n with 0.70 < y / 2^31 < 1.42, from the Taylor
+// series of 2^f = e^(f ln 2), terms (f ln 2)^k / k!, k <= 9 (the next is below 8e-12),
+// in fixed point.
 struct Weight {
     uint32_t y;
     int32_t n;  // below -1000: no weight
@@ -161,13 +148,14 @@ __device__ __forceinline__ Weight weight31(T x, float scale, float mz) {
         return w;
     }
     const float r = rintf(t);
-    const int32_t F = __float2int_rn((t - r) * 2147483648.0f) + __float2int_rn(tl * 2147483648.0f);
-    constexpr int64_t c[10] = {2147483648ll, 1488522236ll, 515882496ll, 119194166ll, 20654775ll,
-                               2863360ll,    330788ll,     32755ll,     2838ll,      219ll};
-    int64_t a = c[9];
+    const int32_t h = __float2int_rn((t - r) * 2147483648.0f) + __float2int_rn(tl * 2147483648.0f);
+    // f = h / 2^31; a high product brings f / 2, so the coefficients are those of
+    // powers of f / 2, in 2^-30: (2 ln 2)^k / k!
+    constexpr int32_t c[10] = {0, 1488522236, 1031764991, 476776663, 165238200, 45813757, 10585225, 2096320, 363265, 55955};
+    int32_t a = c[9];
 #pragma unroll
-    for (int k = 8; k >= 0; --k) a = c[k] + ((a * F) >> 31);
-    w.y = static_cast<uint32_t>(a);
+    for (int k = 8; k >= 1; --k) a = c[k] + __mulhi(a, h);
+    w.y = 0x80000000u + static_cast<uint32_t>((static_cast<int64_t>(a) * h) >> 31);
     w.n = static_cast<int32_t>(r);
     return w;
 }
@@ -180,26 +168,233 @@ __device__ __forceinline__ double weight64(const Weight& w) {
 // Bits behind the point of a row's integer sum: V weights below 4 fit 64 bits.
 __device__ __forceinline__ int sum_bits(int32_t V) { return 61 - (32 - __clz(V)); }
 
+// Sums of the target's and the draft's rows, in every thread of the cluster.
+struct Sums {
+    double p, q;
+};
+// ------------------------------------------------------------------ the race
+// Scores with bounds: the best lower bound, the two best upper bounds and the
+// token of the best one.
+struct Race {
+    float low, up, second;
+    int32_t token;
+};
+__device__ __forceinline__ void race_add(Race& r, float low, float up, int32_t token) {
+    r.low = fmaxf(r.low, low);
+    r.second = fmaxf(r.second, fminf(r.up, up));
+    if (up > r.up) {
+        r.up = up;
+        r.token = token;
+    }
+}
+__device__ __forceinline__ void race_join(Race& r, const Race& o) {
+    r.low = fmaxf(r.low, o.low);
+    r.second = fmaxf(fmaxf(r.second, o.second), fminf(r.up, o.up));
+    if (o.up > r.up) {
+        r.up = o.up;
+        r.token = o.token;
+    }
+}
+// Joins a warp's (the numbers are not negative: their bits are in their order).
+__device__ __forceinline__ Race race_lanes(const Race& r) {
+    const uint32_t up = __float_as_uint(r.up);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, up);
+    const int who = __ffs(__ballot_sync(0xffffffffu, up == most)) - 1;
+    const bool me = static_cast<int>(threadIdx.x & 31) == who;
+    Race o;
+    o.low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r.low)));
+    o.second = __uint_as_float(__reduce_max_sync(0xffffffffu, me ? __float_as_uint(r.second) : up));
+    o.up = __uint_as_float(most);
+    o.token = __shfl_sync(0xffffffffu, r.token, who);
+    return o;
+}
+
+// A weight 2^t, t = (x scale - mz) log2(e), and its relative error: the unit's two
+// ulp, and three roundings of t.  Without weight below 2^-126.
+template <typename T>
+__device__ __forceinline__ float weight(T x, float scale, float mz, float& rel) {
+    const float t = __fmul_rn(fmaf(to_f32(x), scale, -mz), kLog2e);
+    rel = fmaf(fabsf(fmaxf(t, -128.0f)), 0x1p-23f, 0x1p-21f);
+    return exp2_approx(t);
+}
+
+// 1 / e of the hardware's unit (1 ulp; infinite for subnormal e, 0 above 2^126).
+__device__ __forceinline__ float reciprocal(float e) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ int phase_of(const T* p) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % Chunk<T>::kPhase);
+}
+
+// What one pass needs to know of its two rows.
+template <typename TX, typename TY>
+struct Rows {
+    const TX* x;
+    const TY* y;       // the draft's row, or null
+    const float* e;
+    float xs, ys, pm, qm;  // scales and mz
+    float ratio;       // sum of the target's weights over the draft's
+    float ratio_error; // relative
+    int32_t without;   // this token is not drawn (a refused token without probabilities)
+};
+
+// Score of token i: (wp - ratio wq) / e, and how far it may be off.
+template <typename TX, typename TY>
+__device__ __forceinline__ void score(const Rows<TX, TY>& r, TX x, TY y, float e, int32_t i, float& s,
+                                      float& off) {
+    float rel;
+    const float wp = weight(x, r.xs, r.pm, rel);
+    float v = wp;
+    off = wp * rel;
+    if (r.y) {
+        const float wq = weight(y, r.ys, r.qm, rel) * r.ratio;
+        v = wp - wq;
+        off = fmaf(wq, rel + r.ratio_error, off);
+    }
+    const float inv = reciprocal(e);
+    // rounding of the difference, of 1 / e and of the product
+    off = fmaf(fabsf(v), 0x1p-21f, off) * inv;
+    s = v * inv;
+    if (!(e > 0.0f)) {  // nothing is drawn at e < 0 or NaN; 0 wins, and is decided in 64 bits
+        s = 0.0f;
+        off = e == 0.0f && wp > 0.0f ? pos_inf() : 0.0f;
+    } else if (inv == pos_inf()) {
+        s = 0.0f;
+        off = wp > 0.0f ? pos_inf() : 0.0f;
+    }
+    if (i == r.without) s = off = 0.0f;
+}
+
+// How the race passes over tokens.  No score exceeds wp / e, whose logarithm has a
+// bound without a special function: log2(1 / e) is at most what the bits of e say
+// (a line between powers of two lies below log2, by 0.086 at most), and t with 14
+// bits behind the point is the integer part of one multiply-add on 2^23.  In
+// 2^-23:  bound = 512 T - bits(e) + bits(1).
+struct Sieve {
+    float a, c;
+    int32_t margin;
+    static constexpr float kFloor = 8388608.0f + 27.0f * 16384.0f;  // t = -100, masked tokens too
+    __device__ __forceinline__ Sieve(float scale, float mz) {
+        a = scale * kLog2e * 16384.0f;
+        c = 8388608.0f + 127.0f * 16384.0f - mz * kLog2e * 16384.0f;
+        // T is off by half a unit, and by the roundings of a and c; where they
+        // overflow nothing is passed over
+        const float m = 0x1p-13f + (fabsf(mz) + 150.0f) * 0x1p-21f;
+        margin = m < 64.0f ? static_cast<int32_t>(m * 8388608.0f) : 0x7fffffff;
+    }
+    // bits(e) - 512 T - bits(1): the bound with its sign turned.  Negative e are
+    // never drawn and may come out anyhow.
+    __device__ __forceinline__ int32_t of(float x, float e) const {
+        const float f = fmaxf(fmaf(x, a, c), kFloor);
+        return __float_as_int(e) - (__float_as_int(f) << 9);
+    }
+    // What is above this cannot reach a score of `low`.
+    __device__ __forceinline__ int32_t limit(uint32_t low) const {
+        return low == 0u || margin == 0x7fffffff ? 0x7fffffff
+                                                 : 0x3f800000 - static_cast<int32_t>(low) + margin;
+    }
+};
+
+// 8 elements of noise from an address whose place on 16 bytes is `ph`, by the aligned
+// blocks that hold them (each of which holds one of them at least).
+struct Noise8 {
+    float4 a, b, c;
+    __device__ __forceinline__ void load(const float* p, int ph) {
+        const float4* q = reinterpret_cast<const float4*>(p - ph);
+        a = __ldg(q);
+        b = __ldg(q + 1);
+        c = b;
+        if (ph) c = __ldg(q + 2);
+    }
+    template <int PH>
+    __device__ __forceinline__ float get(int k) const {
+        const float f[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        return f[k + PH];
+    }
+};
+template <typename T>
+__device__ __forceinline__ float chunk_element(const Chunk<T>& c, int k) {
+    float lo, hi;
+    upk2(c.pair(k >> 1), lo, hi);
+    return k & 1 ? hi : lo;
+}
+template <typename T, int PH>
+__device__ __forceinline__ int32_t sieve_chunk(const Sieve& sieve, const Chunk<T>& x, const Noise8& e) {
+    int32_t least = 0x7fffffff;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) least = min(least, sieve.of(chunk_element(x, k), e.get<PH>(k)));
+    return least;
+}
+
+struct Shared {
+    uint4 parts[2][kWarps][kMaxCluster];  // 16 bytes of each warp of all blocks, by turns
+    Position pos[kMaxPositions];
+    uint32_t words[kMaxPositions][4];  // words that hold a position's two logits, and its uniform number
+    int32_t ids[ZERO3_MAX_DRAFT];
+    float z[ZERO3_MAX_DRAFT], sum[ZERO3_MAX_DRAFT];  // an accepted token's z - mz, its row's s
+    uint32_t low[2];   // bits of the race's best lower bound, first and second pass
+};
+
+// All of a cluster's warps send 16 bytes to all of its blocks; `turn` numbers the
+// exchanges.  Whoever has come back from exchange t has read what exchange t - 1
+// brought, so two sets of places are enough.
+__device__ __forceinline__ void exchange(Shared& sh, int turn, int C, uint32_t rank, const uint4& v) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (C == 1) {
+        if (lane == 0) sh.parts[turn & 1][warp][0] = v;
+        __syncthreads();
+    } else {
+        if (lane < C) send16(&sh.parts[turn & 1][warp][rank], lane, v);
+        cluster_sync();
+    }
+}
+
+// Joins what the warps `row`, `row` + R, ... of all blocks have sent, each half of
+// the calling warp for a row of its own; every lane of the half gets the result.
+__device__ __forceinline__ Soft join_rows(const Shared& sh, int turn, int row, int R, int C) {
+    Soft o = soft_empty();
+    const int n = (kWarps - row + R - 1) / R * C;
+    int i = threadIdx.x & 15;
+    if (i < n) o = unpack(sh.parts[turn & 1][row + i / C * R][i % C]);
+    for (i += 16; i < n; i += 16) {
+        Soft s = unpack(sh.parts[turn & 1][row + i / C * R][i % C]);
+        float top = fmaxf(soft_top(o), soft_top(s));
+        if (top == neg_inf()) top = 0.0f;
+        soft_rebase<false>(o, top);
+        soft_rebase<false>(s, top);
+        o.s = __fadd_rn(o.s, s.s);
+        if (top == pos_inf()) o.s = __int_as_float(0x7fffffff);
+    }
+    soft_lanes<false, 16>(o);
+    return o;
+}
+
 // This thread's share of the integer sum of a row's weights.
 template <typename T>
 __device__ __forceinline__ uint64_t exact_share(const T* row, int32_t V, float scale, float mz, int rank,
                                                 int C, int bits) {
     uint64_t s = 0;
-    for (int64_t i = rank * kNT + threadIdx.x; i < V; i += static_cast<int64_t>(C) * kNT) {
-        const Weight w = weight31(row[i], scale, mz);
-        const int shift = bits - 31 + w.n;  // y * 2^shift
-        if (shift >= 0)
-            s += static_cast<uint64_t>(w.y) << (shift < 32 ? shift : 32);
-        else if (shift > -34)  // rounded: the errors of many small weights cancel
-            s += (w.y + (uint64_t{1} << (-shift - 1))) >> -shift;
+    const int64_t step = static_cast<int64_t>(C) * kNT;
+    for (int64_t i = rank * kNT + threadIdx.x; i < V; i += 4 * step) {
+        Weight w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            w[u] = i + u * step < V ? weight31(row[i + u * step], scale, mz) : Weight{0, 0};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int shift = bits - 31 + w[u].n;  // y * 2^shift
+            if (shift >= 0)
+                s += static_cast<uint64_t>(w[u].y) << (shift < 32 ? shift : 32);
+            else if (shift > -34)  // rounded: the errors of many small weights cancel
+                s += (w[u].y + (uint64_t{1} << (-shift - 1))) >> -shift;
+        }
     }
     return s;
 }
 
-// Sums of the target's and the draft's rows, in every thread of the cluster.
-struct Sums {
-    double p, q;
-};
 template <typename TX, typename TY>
 __device__ __noinline__ Sums exact_sums(Shared& sh, int turn, const TX* xr, const TY* yr, int32_t V,
                                         float xs, float ys, float mzp, float mzq, int rank, int C) {
@@ -225,116 +420,81 @@ __device__ __noinline__ Sums exact_sums(Shared& sh, int turn, const TX* xr, cons
     return Sums{static_cast<double>(s) * unit, static_cast<double>(t) * unit};
 }
 
-// ------------------------------------------------------------------ the race
-// Scores with bounds: the best lower bound, the two best upper bounds and the
-// token of the best one.
-struct Race {
-    float low, up, second;
-    int32_t token;
-};
-__device__ __forceinline__ void race_add(Race& r, float low, float up, int32_t token) {
-    r.low = fmaxf(r.low, low);
-    r.second = fmaxf(r.second, fminf(r.up, up));
-    if (up > r.up) {
-        r.up = up;
-        r.token = token;
-    }
-}
-__device__ __forceinline__ void race_join(Race& r, const Race& o) {
-    r.low = fmaxf(r.low, o.low);
-    r.second = fmaxf(fmaxf(r.second, o.second), fminf(r.up, o.up));
-    if (o.up > r.up) {
-        r.up = o.up;
-        r.token = o.token;
-    }
-}
-
-// A weight 2^t, t = (x scale - mz) log2(e), and its relative error: the unit's two
-// ulp, and three roundings of t.  Without weight below 2^-126.
-template <typename T>
-__device__ __forceinline__ float weight(T x, float scale, float mz, float& rel) {
-    const float t = __fmul_rn(fmaf(to_f32(x), scale, -mz), kLog2e);
-    rel = fmaf(fabsf(fmaxf(t, -128.0f)), 0x1p-23f, 0x1p-21f);
-    return exp2_approx(t);
-}
-
-// What one pass needs to know of its two rows.
-template <typename TX, typename TY>
-struct Rows {
-    const TX* x;
-    const TY* y;       // the draft's row, or null
-    const float* e;
-    float xs, ys, mzp, mzq;
-    float ratio;       // sum of the target's weights over the draft's
-    float ratio_error; // relative
-    int32_t without;   // this token is not drawn (a refused token without probabilities)
-};
-
-// Score of token i: (wp - ratio wq) / e, and how far it may be off.
-template <typename TX, typename TY>
-__device__ __forceinline__ void score(const Rows<TX, TY>& r, TX x, TY y, float e, int32_t i, float& s,
-                                      float& off) {
-    float rel;
-    const float wp = weight(x, r.xs, r.mzp, rel);
-    float v = wp;
-    off = wp * rel;
-    if (r.y) {
-        const float wq = weight(y, r.ys, r.mzq, rel) * r.ratio;
-        v = wp - wq;
-        off = fmaf(wq, rel + r.ratio_error, off);
-    }
-    const float inv = __fdividef(1.0f, e);
-    // rounding of the difference, of 1 / e and of the product
-    off = fmaf(fabsf(v), 0x1p-21f, off) * inv;
-    s = v * inv;
-    if (!(e > 0.0f)) {  // nothing is drawn at e < 0 or NaN; 0 wins, and is decided in 64 bits
-        s = 0.0f;
-        off = e == 0.0f && wp > 0.0f ? pos_inf() : 0.0f;
-    } else if (inv == pos_inf()) {
-        s = 0.0f;
-        off = wp > 0.0f ? pos_inf() : 0.0f;
-    }
-    if (i == r.without) s = off = 0.0f;
-}
-
+// One pass over the rows.  Only tokens that the sieve lets through are scored, and
+// only for them the draft's row is read.  (The best lower bound of the block, by
+// which it sieves, depends on the warps' timing; the winner does not: what is
+// passed over lies below a lower bound of another token's score.)
 template <typename TX, typename TY>
 __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, TY>& r, int32_t V,
-                                          int rank, int C) {
-    constexpr int U = 4;
+                                          int rank, int C, volatile uint32_t* shared_low) {
     Race b{0.0f, 0.0f, 0.0f, -1};
-    const int64_t step = static_cast<int64_t>(C) * kNT;
-    int64_t i = rank * kNT + threadIdx.x;
-    for (; i + (U - 1) * step < V; i += U * step) {
-        TX x[U];
-        TY y[U];
-        float e[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            x[u] = r.x[i + u * step];
-            y[u] = r.y ? r.y[i + u * step] : TY(0);
-            e[u] = __ldcs(r.e + i + u * step);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float s, off;
-            score(r, x[u], y[u], e[u], static_cast<int32_t>(i + u * step), s, off);
-            race_add(b, s - off, s + off, static_cast<int32_t>(i + u * step));
-        }
-    }
-    for (; i < V; i += step) {
+    const RowCut<TX> cut(r.x, V);
+    const int step = C * kNT, lane = threadIdx.x & 31;
+    const TX* xs = r.x + cut.head;
+    const float* es = r.e + cut.head;
+    const int ep = phase_of(es);
+    const Sieve sieve(r.xs, r.pm);
+    const auto look = [&](TX x, float e, int32_t i) {
         float s, off;
-        score(r, r.x[i], r.y ? r.y[i] : TY(0), __ldcs(r.e + i), static_cast<int32_t>(i), s, off);
-        race_add(b, s - off, s + off, static_cast<int32_t>(i));
+        score(r, x, r.y ? r.y[i] : TY(0), e, i, s, off);
+        race_add(b, s - off, s + off, i);
+    };
+    // a warp takes 32 chunks at a time, and loads the next ones meanwhile
+    Chunk<TX> nx;
+    Noise8 ne;
+    int c = rank * kNT + static_cast<int>(threadIdx.x);
+    if (c < cut.chunks) {
+        nx.load(xs + 8 * c);
+        ne.load(es + 8 * c, ep);
     }
+    for (; c - lane < cut.chunks; c += step) {
+        const Chunk<TX> x = nx;
+        const Noise8 e = ne;
+        if (c + step < cut.chunks) {
+            nx.load(xs + 8 * (c + step));
+            ne.load(es + 8 * (c + step), ep);
+        }
+        const uint32_t low = *shared_low;
+        int32_t least = 0x7fffffff;
+        switch (ep) {
+            case 0: least = sieve_chunk<TX, 0>(sieve, x, e); break;
+            case 1: least = sieve_chunk<TX, 1>(sieve, x, e); break;
+            case 2: least = sieve_chunk<TX, 2>(sieve, x, e); break;
+            default: least = sieve_chunk<TX, 3>(sieve, x, e); break;
+        }
+        unsigned let = __ballot_sync(0xffffffffu, c < cut.chunks && least <= sieve.limit(low));
+        if (let == 0) continue;
+        if (__popc(let) > 4) {  // the first chunks, mostly: all of them whole
+            if (let >> lane & 1) {
+                const int32_t i = cut.head + 8 * c;
+#pragma unroll 4
+                for (int k = 0; k < 8; ++k) look(r.x[i + k], r.e[i + k], i + k);
+            }
+        } else {  // eight lanes for each chunk
+            int from = 0;
+            bool any = false;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Race t;
-        t.low = __shfl_xor_sync(0xffffffffu, b.low, o);
-        t.up = __shfl_xor_sync(0xffffffffu, b.up, o);
-        t.second = __shfl_xor_sync(0xffffffffu, b.second, o);
-        t.token = __shfl_xor_sync(0xffffffffu, b.token, o);
-        race_join(b, t);
+            for (int k = 0; k < 4; ++k) {
+                if (k == lane >> 3 && let) {
+                    from = __ffs(let) - 1;
+                    any = true;
+                }
+                let &= let - 1;
+            }
+            const int32_t i = __shfl_sync(0xffffffffu, cut.head + 8 * c, from) + (lane & 7);
+            if (any) look(r.x[i], r.e[i], i);
+        }
+        __syncwarp();
+        const uint32_t found = __reduce_max_sync(0xffffffffu, __float_as_uint(b.low));
+        if (lane == 0 && found > low) atomicMax(const_cast<uint32_t*>(shared_low), found);
     }
+    // the ends of the row
+    if (rank == 0 && threadIdx.x < 16) {
+        const int32_t i = edge_element(0, cut.head, cut.head + 8 * cut.chunks, V);
+        if (i >= 0) look(r.x[i], r.e[i], i);
+    }
+    __syncwarp();
+    b = race_lanes(b);
     exchange(sh, turn, C, rank,
              make_uint4(__float_as_uint(b.low), __float_as_uint(b.up), __float_as_uint(b.second),
                         static_cast<uint32_t>(b.token)));
@@ -344,16 +504,7 @@ __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, T
         race_join(best, Race{__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                              static_cast<int32_t>(v.w)});
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Race t;
-        t.low = __shfl_xor_sync(0xffffffffu, best.low, o);
-        t.up = __shfl_xor_sync(0xffffffffu, best.up, o);
-        t.second = __shfl_xor_sync(0xffffffffu, best.second, o);
-        t.token = __shfl_xor_sync(0xffffffffu, best.token, o);
-        race_join(best, t);
-    }
-    return best;
+    return race_lanes(best);
 }
 
 // The race among the tokens whose upper bound reaches `low`, with 31-bit weights
@@ -370,8 +521,8 @@ __device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Rows<TX, 
         float s, off;
         score(r, x, y, e, static_cast<int32_t>(i), s, off);
         if (!(s + off >= low) || !(e >= 0.0f) || i == r.without) continue;
-        double v = weight64(weight31(x, r.xs, r.mzp));
-        if (r.y) v = v / sums.p - weight64(weight31(y, r.ys, r.mzq)) / sums.q;
+        double v = weight64(weight31(x, r.xs, r.pm));
+        if (r.y) v = v / sums.p - weight64(weight31(y, r.ys, r.qm)) / sums.q;
         v = v / static_cast<double>(e);
         if (v > best) {  // tokens come in ascending order
             best = v;
@@ -407,8 +558,130 @@ __device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Rows<TX, 
 }
 
 // ---------------------------------------------------------------- the kernel
+// Exact decision about a close position.
 template <typename TX, typename TY, bool DRAFT>
-__global__ void __launch_bounds__(kNT, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__device__ __noinline__ int decide(Shared& sh, int turn, const VerifyArgs& a, const Position& o, const TX* xr,
+                                   const TY* yr, int rank) {
+    const Sums m = exact_sums<TX, TY>(sh, turn, xr, yr, a.vocab, a.scale, a.y_scale, o.pm, o.qm, rank,
+                                      a.cluster);
+    const double wp = weight64(weight31(xr[o.token], a.scale, o.pm));
+    double wq = 1.0, sq = 1.0;
+    if (DRAFT) {
+        wq = weight64(weight31(yr[o.token], a.y_scale, o.qm));
+        sq = m.q;
+    }
+    bool less = static_cast<double>(o.u) * wq * m.p < wp * sq;
+    if (wp == 0.0 || wq == 0.0) {  // below 2^-1000: by their logarithms
+        const double lp = static_cast<double>(o.xd) * a.scale - o.pm - log(m.p);
+        const double lq = DRAFT ? static_cast<double>(o.yd) * a.y_scale - o.qm - log(m.q) : 0.0;
+        less = log(static_cast<double>(o.u)) + lq < lp;
+    }
+    return less ? kAccept : kRefuse;
+}
+
+// Position j, number g of the round, from the rows' sums (one warp).
+template <typename TX, typename TY, bool DRAFT>
+__device__ __forceinline__ void judge(Shared& sh, int turn, const VerifyArgs& a, int R, int g, int j, bool drafted,
+                                      const TX* xr, const TY* yr) {
+    const int lane = threadIdx.x & 31;
+    const int row = (DRAFT ? 2 * g : g) + (DRAFT && lane >= 16 && drafted);
+    const Soft h = join_rows(sh, turn, row, R, a.cluster);
+    Position o;
+    o.pm = __shfl_sync(0xffffffffu, h.mz, 0);
+    o.ps = __shfl_sync(0xffffffffu, h.s, 0);
+    o.qm = __shfl_sync(0xffffffffu, h.mz, 16);
+    o.qs = __shfl_sync(0xffffffffu, h.s, 16);
+    o.verdict = o.ps != o.ps ? kBroken : kEnd;
+    o.xd = o.yd = o.u = 0.0f;
+    o.token = -1;
+    if (drafted) {
+        o.token = sh.ids[j];
+        o.xd = from_word(sh.words[g][0], xr + o.token);
+        o.u = __uint_as_float(sh.words[g][2]);
+        bool q_nan = false, in_q = true;
+        float rel, rel_q = 0.0f, wq = 1.0f, sq = 1.0f;
+        const float wp = weight(o.xd, a.scale, o.pm, rel);
+        if (DRAFT) {
+            o.yd = from_word(sh.words[g][1], yr + o.token);
+            q_nan = o.qs != o.qs;
+            in_q = o.qs != 0.0f && __fmul_rn(o.yd, a.y_scale) != neg_inf();
+            wq = weight(o.yd, a.y_scale, o.qm, rel_q);
+            sq = o.qs;
+        }
+        if (lane == 0) {
+            sh.z[j] = fmaf(o.xd, a.scale, -o.pm);
+            sh.sum[j] = o.ps;
+        }
+        if (o.ps != o.ps || q_nan) {
+            o.verdict = kBroken;
+        } else if (!(o.u >= 0.0f) || o.ps == 0.0f || __fmul_rn(o.xd, a.scale) == neg_inf()) {
+            o.verdict = kRefuse;
+        } else if (!in_q || o.u == 0.0f) {
+            o.verdict = kAccept;
+        } else {
+            // u q < p: u wq sp < wp sq, off by the sums' and the weights' errors and
+            // a few roundings; what is small for binary32 is close
+            const float l = o.u * (wq * o.ps), r = wp * sq;
+            const float off = fmaf(2.0f, a.sum_error, rel + rel_q + 0x1p-21f) * (l + r);
+            o.verdict = kClose;
+            if (l + r > 0x1p-60f) {
+                if (r - l > off) o.verdict = kAccept;
+                if (l - r > off) o.verdict = kRefuse;
+            }
+        }
+    }
+    if (lane == 0) sh.pos[g] = o;
+}
+
+// The token after position o: the row of the target, the draft's, the noise.
+template <typename TX, typename TY, bool DRAFT>
+__device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const VerifyArgs& a, const Position& o,
+                                        int verdict, const TX* xr, const TY* yr, const float* noise, int rank) {
+    const int C = a.cluster;
+    Rows<TX, TY> r;
+    r.x = xr;
+    r.y = nullptr;
+    r.e = noise;
+    r.xs = a.scale;
+    r.ys = a.y_scale;
+    r.pm = o.pm;
+    r.qm = o.qm;
+    r.ratio = 0.0f;
+    r.ratio_error = 0.0f;
+    r.without = -1;
+    if (verdict == kRefuse) {
+        if (!DRAFT) {
+            r.without = o.token;
+        } else if (o.qs != 0.0f) {
+            r.y = yr;
+            r.ratio = __fmul_rn(o.ps, reciprocal(o.qs));
+            r.ratio_error = 2.0f * a.sum_error + 0x1p-22f;
+        }
+    }
+    int32_t token = -1;
+    for (int pass = 0; pass < 2; ++pass) {
+        const Race b = race_pass<TX, TY>(sh, turn, r, a.vocab, rank, C, &sh.low[pass]);
+        ++turn;
+        if (b.low > 0.0f && b.second < b.low) {
+            token = b.token;
+        } else {
+            Sums m{1.0, 1.0};
+            if (r.y) {
+                m = exact_sums<TX, TY>(sh, turn, r.x, r.y, a.vocab, r.xs, r.ys, r.pm, r.qm, rank, C);
+                ++turn;
+            }
+            token = exact_race<TX, TY>(sh, turn, r, m, b.low, a.vocab, rank, C);
+            ++turn;
+        }
+        if (token >= 0 || (!r.y && r.without < 0)) break;
+        r.y = nullptr;  // no residual: from the target itself
+        r.without = -1;
+    }
+    return token;
+}
+
+template <typename TX, typename TY, bool DRAFT>
+__global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ Shared sh;
     const int C = a.cluster;
     const uint32_t rank = C > 1 ? cluster_rank() : 0u;
@@ -420,8 +693,21 @@ __global__ void __launch_bounds__(kNT, 2) verify_kernel(const __grid_constant__ 
     const TX* x = static_cast<const TX*>(a.x) + s * (K + 1) * a.stride;
     const TY* y = DRAFT ? static_cast<const TY*>(a.y) + s * K * a.y_stride : nullptr;
     const float* noise = a.noise + s * a.noise_stride;
+    int32_t* tokens = a.tokens + s * (K + 1);
     wait_prior_grids();
     allow_next_grid();
+    if (tid < 2) sh.low[tid] = 0;  // seen by all after the first barrier
+    // The block's part of the noise goes to L2: at once where all sequences' fits
+    // there beside the rows, else when it is needed.
+    const auto prefetch_noise = [&]() {
+        const int per = (V + C - 1) / C;
+        const int lo = rank * per, hi = lo + per < V ? lo + per : V;
+        for (int i = lo + 32 * tid; i < hi; i += 32 * kNT) prefetch_line(noise + i);
+    };
+    const bool early = a.n * V <= (int64_t{1} << 22);  // 16 MB
+    const int ahead = a.ahead;  // its rows and one more are kWarps at most
+    if (early) prefetch_noise();
+    int turn = 0, verdict = kAccept;
     // the draft's length: ids up to the first ignored one (every warp by itself)
     int L = K;
     for (int j = lane; j - lane < K; j += 32) {
@@ -433,174 +719,83 @@ __global__ void __launch_bounds__(kNT, 2) verify_kernel(const __grid_constant__ 
             break;
         }
     }
-    if (C > 1) cluster_wait();  // the others' shared memory is there
-    // relative error of a row's sum: terms off by less than 2^-18 on average, the
-    // longest chain of additions
-    const int G = a.ahead;
-    const int R = DRAFT ? 2 * G : G;
-    const int WR = kWarps / R;          // warps per row
-    const float sum_error = 0x1p-17f + static_cast<float>(V / (8 * C * WR * 32) + 16) * 0x1p-24f;
-    int turn = 0;
-    int A = 0;
-    int32_t token = -1;
-    float token_lp = 0.0f;
-    for (int j0 = 0;; j0 += G) {
-        // ---- the round's rows
-        {
-            const int row = warp / WR, g = DRAFT ? row >> 1 : row;
-            const bool of_draft = DRAFT && (row & 1);
-            Soft q = soft_empty();
-            const int j = j0 + g;
-            const int tr = (warp % WR) * 32 + lane;
-            if (of_draft) {
-                if (j < L)
-                    stream_row<TY>(q, y + j * a.y_stride, V, rank, C, a.y_scale, tr, WR * 32);
-            } else if (j <= L) {
-                stream_row<TX>(q, x + j * a.stride, V, rank, C, a.scale, tr, WR * 32);
+    __syncwarp();  // warp 0 reads the ids that its lanes have written
+    if (C > 1) cluster_wait();     // the others' shared memory is there
+    int at = -1, j0 = 0;
+    for (;; j0 += ahead) {
+        // ---- the round's rows, and what the verdicts need beside them.  The row behind
+        // the draft comes along with the last position.
+        const int G = ahead < L - j0 ? ahead : L - j0;
+        const bool whole = j0 + G == L;
+        const int R = (DRAFT ? 2 * G : G) + whole;
+        if (warp == 0) {
+            if (lane < G) {
+                const int j = j0 + lane, d = sh.ids[j];
+                send_word(&sh.words[lane][0], x + j * a.stride + d);
+                if (DRAFT) send_word(&sh.words[lane][1], y + j * a.y_stride + d);
+                send_word(&sh.words[lane][2], a.uniform + s * K + j);
             }
+        }
+        {
+            const int row = warp % R, nt = (kWarps - row + R - 1) / R * 32;
+            const int tr = warp / R * 32 + lane;
+            const int j = j0 + (DRAFT ? row >> 1 : row);
+            Soft q = soft_empty();
+            if (DRAFT && (row & 1))
+                stream_row<TY>(q, y + j * a.y_stride, V, rank, C, a.y_scale, tr, nt);
+            else
+                stream_row<TX>(q, x + j * a.stride, V, rank, C, a.scale, tr, nt);
+            __syncwarp();
             soft_lanes<false, 32>(q);
+            if (warp == 0) drain_copies();
             exchange(sh, turn, C, rank, pack(q));
         }
-        // ---- verdicts, a warp each
-        if (warp < G && j0 + warp <= L) {
-            const int g = warp, j = j0 + g;
-            Position o;
-            o.p = join_rows(sh, turn, (DRAFT ? 2 * g : g) * WR, WR, C);
-            o.q = DRAFT && j < L ? join_rows(sh, turn, (2 * g + 1) * WR, WR, C) : soft_empty();
-            o.verdict = kEnd;
-            o.token = -1;
-            o.xd = o.yd = o.u = 0.0f;
-            if (j < L) {
-                o.token = sh.ids[j];
-                const TX xd = x[j * a.stride + o.token];
-                o.xd = to_f32(xd);
-                o.u = a.uniform[s * K + j];
-                // log2 p = tp - lsp, log2 q = tq - lq; a token that is there keeps its
-                // place among the smallest where t leaves binary32's range
-                float tq = 0.0f, lq = 0.0f;
-                bool q_nan = false, in_q = true;
-                if (DRAFT) {
-                    const TY yd = y[j * a.y_stride + o.token];
-                    o.yd = to_f32(yd);
-                    tq = fmaxf(__fmul_rn(fmaf(o.yd, a.y_scale, -o.q.mz), kLog2e), -0x1p126f);
-                    lq = log2f(o.q.s);
-                    q_nan = o.q.s != o.q.s;
-                    in_q = o.q.s != 0.0f && __fmul_rn(o.yd, a.y_scale) != neg_inf();
-                }
-                const float tp = fmaxf(__fmul_rn(fmaf(o.xd, a.scale, -o.p.mz), kLog2e), -0x1p126f);
-                const float lsp = log2f(o.p.s);
-                const float lu = log2f(o.u);
-                if (lane == 0) sh.lp[j] = __fsub_rn(fmaf(o.xd, a.scale, -o.p.mz), logf(o.p.s));
-                if (o.p.s != o.p.s || q_nan || o.u != o.u) {
-                    o.verdict = o.u != o.u && o.p.s == o.p.s && !q_nan ? kRefuse : kBroken;
-                } else if (o.p.s == 0.0f || __fmul_rn(o.xd, a.scale) == neg_inf()) {
-                    o.verdict = kRefuse;
-                } else if (!in_q || lu == neg_inf()) {
-                    o.verdict = kAccept;
-                } else {
-                    const float diff = (tp - lsp) - (tq - lq) - lu;
-                    const float off = 3.0f * sum_error +
-                                      (fabsf(tp) + fabsf(tq) + fabsf(lsp) + fabsf(lq) + fabsf(lu)) * 0x1p-21f;
-                    o.verdict = diff > off ? kAccept : diff < -off ? kRefuse : kClose;
-                }
-            } else if (o.p.s != o.p.s) {
-                o.verdict = kBroken;
-            }
-            if (lane == 0) sh.pos[g] = o;
+        if (warp < G + whole) {
+            const int j = j0 + warp;
+            judge<TX, TY, DRAFT>(sh, turn, a, R, warp, j, warp < G, x + j * a.stride,
+                                 DRAFT ? y + j * a.y_stride : nullptr);
         }
         ++turn;
         __syncthreads();
         // ---- the first position that does not accept
-        int at = -1, verdict = kAccept;
-        for (int g = 0; g < G && j0 + g <= L; ++g) {
+        for (int g = 0; g < G + whole; ++g) {
             verdict = sh.pos[g].verdict;
             if (verdict == kClose) {
-                const Position o = sh.pos[g];
                 const int j = j0 + g;
-                const TX* xr = x + j * a.stride;
-                const TY* yr = DRAFT ? y + j * a.y_stride : nullptr;
-                const Sums m = exact_sums<TX, TY>(sh, turn, xr, yr, V, a.scale, a.y_scale, o.p.mz, o.q.mz,
-                                                  rank, C);
+                verdict = decide<TX, TY, DRAFT>(sh, turn, a, sh.pos[g], x + j * a.stride,
+                                                DRAFT ? y + j * a.y_stride : nullptr, rank);
                 ++turn;
-                const double wp = weight64(weight31(xr[o.token], a.scale, o.p.mz));
-                double wq = 1.0, sq = 1.0;
-                if (DRAFT) {
-                    wq = weight64(weight31(yr[o.token], a.y_scale, o.q.mz));
-                    sq = m.q;
-                }
-                bool less = static_cast<double>(o.u) * wq * m.p < wp * sq;
-                if (wp == 0.0 || wq == 0.0) {  // both below 2^-1000: by their logarithms
-                    const double lp = static_cast<double>(o.xd) * a.scale - o.p.mz - log(m.p);
-                    const double lq = DRAFT ? static_cast<double>(o.yd) * a.y_scale - o.q.mz - log(m.q) : 0.0;
-                    less = log(static_cast<double>(o.u)) + lq < lp;
-                }
-                verdict = less ? kAccept : kRefuse;
             }
             if (verdict != kAccept) {
                 at = g;
                 break;
             }
         }
-        if (at < 0) continue;  // the next exchange's barrier lies before the positions' next writing
-        // ---- the draw
-        A = j0 + at;
-        const Position o = sh.pos[at];
-        if (verdict == kBroken) {
-            token_lp = __int_as_float(0x7fffffff);
-            break;
+        if (at >= 0) break;
+        // (the next round's barrier lies before the positions' next writing)
+    }
+    const int A = j0 + at;
+    const Position o = sh.pos[at];
+    int32_t token = -1;
+    float lp = __int_as_float(0x7fffffff);
+    if (verdict != kBroken) {
+        lp = neg_inf();
+        if (o.ps != 0.0f) {
+            if (!early) prefetch_noise();
+            const TX* xr = x + A * a.stride;
+            token = draw<TX, TY, DRAFT>(sh, turn, a, o, verdict, xr, DRAFT ? y + A * a.y_stride : nullptr, noise,
+                                        rank);
+            if (token >= 0 && rank == 0)
+                lp = __fsub_rn(fmaf(to_f32(xr[token]), a.scale, -o.pm), logf(o.ps));
         }
-        if (o.p.s == 0.0f) {
-            token_lp = neg_inf();
-            break;
-        }
-        Rows<TX, TY> r;
-        r.x = x + A * a.stride;
-        r.y = nullptr;
-        r.e = noise;
-        r.xs = a.scale;
-        r.ys = a.y_scale;
-        r.mzp = o.p.mz;
-        r.mzq = o.q.mz;
-        r.ratio = 0.0f;
-        r.ratio_error = 0.0f;
-        r.without = -1;
-        if (verdict == kRefuse) {
-            if (!DRAFT) {
-                r.without = o.token;
-            } else if (o.q.s != 0.0f) {
-                r.y = y + A * a.y_stride;
-                r.ratio = __fdiv_rn(o.p.s, o.q.s);
-                r.ratio_error = 2.5f * sum_error;
-            }
-        }
-        for (int pass = 0; pass < 2; ++pass) {
-            const Race b = race_pass(sh, turn, r, V, rank, C);
-            ++turn;
-            if (b.low > 0.0f && b.second < b.low) {
-                token = b.token;
-            } else {
-                Sums m{1.0, 1.0};
-                if (r.y) {
-                    m = exact_sums<TX, TY>(sh, turn, r.x, r.y, V, r.xs, r.ys, r.mzp, r.mzq, rank, C);
-                    ++turn;
-                }
-                token = exact_race(sh, turn, r, m, b.low, V, rank, C);
-                ++turn;
-            }
-            if (token >= 0 || (!r.y && r.without < 0)) break;
-            r.y = nullptr;  // no residual: from the target itself
-            r.without = -1;
-        }
-        token_lp = neg_inf();
-        if (token >= 0)
-            token_lp = __fsub_rn(fmaf(to_f32(r.x[token]), a.scale, -o.p.mz), logf(o.p.s));
-        break;
     }
     if (rank == 0) {
         if (tid == 0) a.accepted[s] = A;
         for (int j = tid; j <= K; j += kNT) {
-            a.tokens[s * (K + 1) + j] = j < A ? sh.ids[j] : j == A ? token : -1;
-            if (a.logprobs) a.logprobs[s * (K + 1) + j] = j < A ? sh.lp[j] : j == A ? token_lp : 0.0f;
+            tokens[j] = j < A ? sh.ids[j] : j == A ? token : -1;
+            if (a.logprobs)
+                a.logprobs[s * (K + 1) + j] =
+                    j < A ? __fsub_rn(sh.z[j], logf(sh.sum[j])) : j == A ? lp : 0.0f;
         }
     }
 }
@@ -616,19 +811,23 @@ cudaError_t launch_types(const VerifyArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_verify(const VerifyArgs& args, cudaStream_t stream) {
     VerifyArgs a = args;
+    // as many blocks per sequence as are resident at once (four on each of 152 SMs)
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && a.n * a.cluster * 2 <= 304) a.cluster *= 2;
-    const int most = a.y ? kMaxRows / 2 : kMaxRows;
-    a.ahead = 1;
-    // few sequences: their rows in one round, while latency costs more than rows
-    // that turn out not to be needed
-    if (a.n <= 19)
-        while (a.ahead < most && a.ahead < a.k + 1) a.ahead *= 2;
+    while (a.cluster < kMaxCluster && a.n * a.cluster * 2 <= 608) a.cluster *= 2;
+    a.ahead = a.y ? (a.n <= 100 ? 3 : 2) : (a.n <= 200 ? 7 : 3);
+    const int g = a.ahead < a.k ? a.ahead : a.k, rows = (a.y ? 2 * g : g) + 1;
+    // Relative error of a row's sum.  Its terms: the unit's two ulp (2^-22), three
+    // roundings of t, 1.2 * 2^-23 |t| on their average |t|, which is at most log2(V); a
+    // thread's chain of additions and the joins (its batches, then at most 32
+    // more); five changes of the reference, 2^-22 each.
+    int bits = 1;
+    while (a.vocab >> bits) ++bits;
+    const int chain = a.vocab / (16 * 32 * a.cluster * (kWarps / rows)) + 32;
+    a.sum_error = 6 * 0x1p-22f + 1.2f * 0x1p-23f * static_cast<float>(bits) + static_cast<float>(chain) * 0x1p-24f;
     if (a.dtype == ZERO3_BF16)
         return a.y_dtype == ZERO3_BF16 ? launch_types<uint16_t, uint16_t>(a, stream)
                                        : launch_types<uint16_t, float>(a, stream);
-    return a.y_dtype == ZERO3_BF16 ? launch_types<float, uint16_t>(a, stream)
-                                   : launch_types<float, float>(a, stream);
+    return a.y_dtype == ZERO3_BF16 ? launch_types<float, uint16_t>(a, stream) : launch_types<float, float>(a, stream);
 }
 
 }  // namespace z3
