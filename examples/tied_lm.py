@@ -1,6 +1,7 @@
 """A small tied language model trained under ZeRO-3 with the vocabulary
-operators: distillation from a teacher's top logits, a policy step on log
-probabilities and entropy, and decoding.
+operators: distillation from a teacher's top logits, policy steps with clipped
+gradients on tokens that the model has drawn itself (from a smaller model's drafts),
+and decoding.
 
 The model is wte [vocab, dim] (embedding and output head), w1 [dim, hidden] and
 w2 [hidden, dim]: h = x + gelu(x w1) w2, logits = h wte^T.  Its parameters live
@@ -54,6 +55,8 @@ class TiedLM:
         self.gathered = [torch.empty(self.plan.submodule(k)[1], dtype=BF, device=device) for k in (0, 1)]
         self.scale = dim ** 0.5
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
+        self.norm = torch.zeros(1, device=device)  # of the last clipped step's gradients
+        self.clip_workspace = torch.empty(0, dtype=torch.uint8, device=device)
         Z.zero3_cast_params(self.plan, self._ptrs(self.master), self._ptrs(self.sparam),
                             self.full.data_ptr(), None, 0, info.psi_pad, self.stream)
 
@@ -113,11 +116,22 @@ class TiedLM:
                                    self.workspace.numel(), self.stream)
         self.release()
 
-    def step(self):
+    def step(self, max_norm=None):
+        """One optimizer step; with max_norm the gradients are clipped by their
+        global norm, which self.norm receives."""
         self.t += 1
-        Z.zero3_step(self.plan, self.hp, self.t, self._ptrs(self.grads), 0, self._ptrs(self.master),
-                     self._ptrs(self.m), self._ptrs(self.v), self._ptrs(self.sparam),
-                     self.full.data_ptr(), None, 0, self.plan.info.psi_pad, self.stream)
+        end = self.plan.info.psi_pad
+        args = (self.plan, self.hp, self.t, self._ptrs(self.grads), 0, self._ptrs(self.master),
+                self._ptrs(self.m), self._ptrs(self.v), self._ptrs(self.sparam), self.full.data_ptr(),
+                None, 0, end)
+        if max_norm is None:
+            Z.zero3_step(*args, self.stream)
+            return
+        if self.clip_workspace.numel() == 0:
+            best = Z.zero3_step_clipped_workspace(self.plan, 0, end)[1]
+            self.clip_workspace = torch.empty(best, dtype=torch.uint8, device=self.dev)
+        Z.zero3_step_clipped(*args, max_norm, self.norm.data_ptr(), self.clip_workspace.data_ptr(),
+                             self.clip_workspace.numel(), self.stream)
 
 
 def id_type(tokens):
@@ -156,11 +170,11 @@ def distill_step(model, batches, temperature=1.0, hardest=None):
     return total / len(batches)
 
 
-def policy_step(model, batches, entropy_bonus=0.01):
+def policy_step(model, batches, entropy_bonus=0.01, max_norm=None):
     """One optimizer step that raises advantage * log p(target) + entropy_bonus *
     entropy on the ranks' batches (tokens [n], targets [n], advantage [n] float32;
-    a target outside the vocabulary is padding); returns the mean log
-    probability and entropy."""
+    a target outside the vocabulary is padding), its gradients clipped to max_norm;
+    returns the mean log probability and entropy."""
     lp = ent = 0.0
     for rank, (tokens, targets, advantage) in enumerate(batches):
         logits, saved = model.forward(tokens)
@@ -177,7 +191,7 @@ def policy_step(model, batches, entropy_bonus=0.01):
                                         model.stream)
         model.backward(rank, logits, saved)
         lp, ent = lp + logprob.mean(), ent + entropy.mean()
-    model.step()
+    model.step(max_norm)
     return lp / len(batches), ent / len(batches)
 
 
@@ -199,6 +213,48 @@ def decode(model, first, steps, k=5):
         model.release()
         tokens = ids[s, :, 0].contiguous()
     return ids, lps
+
+
+@torch.no_grad()
+def speculate(model, draft, last, k, generator, temperature=1.0):
+    """Up to k + 1 tokens after each of `last` [n] int32, distributed as the model's
+    own: k drawn by the smaller model `draft` one after another, verified by the
+    model in one pass over all of them (k = 0: drawn by the model).  Returns the
+    number of accepted drafts [n], the tokens [n, k + 1] int32 (-1 behind them) and
+    their log probabilities."""
+    n, vocab = last.numel(), model.vocab
+    new = lambda *shape, dtype=F32: torch.empty(*shape, dtype=dtype, device=model.dev)  # noqa: E731
+    inputs = new(n, k + 1, dtype=torch.int32)
+    inputs[:, 0] = last
+    q = new(n, k, vocab, dtype=BF)
+    counts, drawn = new(n, dtype=torch.int32), new(n, 1, dtype=torch.int32)
+    for j in range(k):
+        logits, _ = draft.forward(inputs[:, j].contiguous(), train=False)
+        draft.release()
+        q[:, j] = logits
+        noise = new(n, vocab).exponential_(generator=generator)
+        Z.zero3_verify_draft(logits.data_ptr(), Z.BF16, n, 0, vocab, vocab, 0, Z.BF16, vocab, 0, Z.I32,
+                             1.0 / temperature, 1.0, 0, noise.data_ptr(), vocab, counts.data_ptr(),
+                             drawn.data_ptr(), 0, model.stream)
+        inputs[:, j + 1] = drawn[:, 0]
+    logits, _ = model.forward(inputs.view(-1), train=False)
+    model.release()
+    ids = inputs[:, 1:].contiguous()
+    uniform = torch.rand(n, k, device=model.dev, generator=generator)
+    noise = new(n, vocab).exponential_(generator=generator)
+    tokens, logprobs = new(n, k + 1, dtype=torch.int32), new(n, k + 1)
+    Z.zero3_verify_draft(logits.data_ptr(), Z.BF16, n, k, vocab, vocab, q.data_ptr(), Z.BF16, vocab,
+                         ids.data_ptr(), Z.I32, 1.0 / temperature, 1.0 / temperature, uniform.data_ptr(),
+                         noise.data_ptr(), vocab, counts.data_ptr(), tokens.data_ptr(),
+                         logprobs.data_ptr(), model.stream)
+    return counts, tokens, logprobs
+
+
+def rollout_batch(last, tokens, advantage):
+    """A policy batch of speculate()'s tokens: each after its predecessor; padding
+    behind the drawn one stays padding."""
+    inputs = torch.cat([last[:, None], tokens[:, :-1]], 1).clamp(min=0)
+    return inputs.reshape(-1).contiguous(), tokens.reshape(-1).contiguous(), advantage.reshape(-1)
 
 
 def bigram_teacher(vocab, k, seed=1, device="cuda"):
@@ -229,13 +285,26 @@ def main():
                             hardest=1.0 if s % 4 == 3 else None)
         if s % 10 == 0 or s == 59:
             print(f"distillation step {s}: loss {float(loss):.4f}")
-    batch = []
-    for tokens, ids, _ in teacher_batches(teacher, vocab, n, model.nd, 1000):
-        batch.append((tokens, ids[:, 1].contiguous(), torch.ones(n, device=model.dev)))
+    # rollouts from a smaller model's drafts; tokens the teacher ranks second are rewarded
+    draft = TiedLM(vocab=vocab, dim=64, hidden=128, seed=1)
+    for s in range(30):
+        distill_step(draft, teacher_batches(teacher, vocab, n, draft.nd, 500 + s))
+    generator = torch.Generator("cuda").manual_seed(7)
+    second = teacher[0][:, 1]
     for s in range(10):
-        lp, ent = policy_step(model, batch)
+        batches, accepted, reward = [], 0.0, 0.0
+        for last, _, _ in teacher_batches(teacher, vocab, 256, model.nd, 1000 + s):
+            counts, tokens, _ = speculate(model, draft, last, 3, generator)
+            inputs, targets, _ = rollout_batch(last, tokens, torch.zeros_like(tokens))
+            hit = (second[inputs.long()] == targets).float()
+            batches.append((inputs, targets, hit))
+            accepted, reward = accepted + counts.float().mean(), reward + hit.mean()
+        lp, ent = policy_step(model, batches, max_norm=1.0)
+        if s % 3 == 0:
+            print(f"rollout {s}: accepted {float(accepted) / model.nd:.2f} of 3, reward "
+                  f"{float(reward) / model.nd:.3f}, gradient norm {float(model.norm):.3f}")
     print(f"policy steps: mean log probability {float(lp):.4f}, entropy {float(ent):.4f}")
-    ids, lps = decode(model, batch[0][0][:4].contiguous(), 6)
+    ids, lps = decode(model, batches[0][0][:4].contiguous(), 6)
     print("decoded:", ids[:, :, 0].t().tolist())
 
 

@@ -300,3 +300,150 @@ def test_clipped_step(z, name, keep):
         CO.scaled_step(plan, w.hparams, t, hG, st, full, hP, ps, c)
         assert_state(e, st, full, ps)
     assert e.check_guards() == []
+
+
+@pytest.mark.parametrize("name,bucketed", [("mini3", True), ("mini4", False), ("ragged7", True)])
+def test_emulation_steps_with_clipping(z, name, bucketed):
+    """Buckets: square sums, one coefficient, scaled steps; one chunk: one call."""
+    w = {"mini3": lambda: W.mini_gpt(3), "mini4": lambda: W.mini_gpt(4),
+         "ragged7": lambda: W.ragged_small(7)}[name]()
+    w.bucket = 100_003
+    plan, st, full, ps = oracle_state(w)
+    e = emulation(w, bucketed=bucketed, guard=64)
+    assert (len(e.chunks) > 3) == bucketed
+    for t, max_norm in ((1, 0.04), (2, 0.07), (3, 1e9)):
+        e.fill_grads(t)
+        e.step(t, max_norm=max_norm)
+        n = float(e.norm)
+        G, P = host_grads(w, plan, t), host_pgrads(w, plan, t)
+        s = CO.square_sum([g for g in CO.reduced(plan, G) if g is not None] +
+                          [O.reduce_sum(P, np.float32(1.0 / plan.n_ranks))])
+        assert abs(n - np.sqrt(s)) <= NORM_TOL * n
+        # the coefficient lies within its tolerance of the 64-bit one: find it
+        want = CO.clip_coefficient(s, max_norm)
+        tried = [np.float32(want)]
+        for _ in range(8):
+            tried += [np.nextafter(tried[0], np.float32(0)), np.nextafter(tried[-1], np.float32(2))]
+            tried.sort()
+        import copy
+        for c in tried:
+            st2, full2, ps2 = copy.deepcopy(st), full.copy(), copy.deepcopy(ps)
+            CO.scaled_step(plan, w.hparams, t, G, st2, full2, P, ps2, c)
+            if np.array_equal(bits(f32(e.m[0])), bits(st2.m[0])):
+                break
+        st, full, ps = st2, full2, ps2
+        assert_state(e, st, full, ps)
+    assert e.check_guards() == []
+
+
+@pytest.mark.parametrize("nd", [1, 2, 5, 8, 9])
+def test_scaled_replicated_step(z, nd):
+    """ZeRO-1/2: every rank's full copy and the shards' states, twice."""
+    w = W.mini_gpt(nd)
+    plan, st, full, ps = oracle_state(w)
+    e = emulation(w)
+    reps = [e.full.clone() for _ in range(nd)]
+    scale = torch.tensor([0.0], device="cuda")
+    for t, c in ((1, 0.3125), (2, 0.7)):
+        e.fill_grads(t)
+        scale.fill_(c)
+        z.zero3_step_stage12_scaled(e.plan, e.hp, t, e.ptrs(e.grads[0]), 0, e.ptrs(e.master), e.ptrs(e.m),
+                                    e.ptrs(e.v), e.ptrs(reps), 0, e.psi_pad, scale.data_ptr(), sid())
+        CO.scaled_step(plan, w.hparams, t, host_grads(w, plan, t), st, full, host_pgrads(w, plan, t), ps,
+                       np.float32(c))
+        for r in range(nd):
+            for name in ("master", "m", "v"):
+                assert np.array_equal(bits(f32(getattr(e, name)[r])), bits(getattr(st, name)[r]))
+            assert np.array_equal(u16(reps[r]), full)
+
+
+@pytest.mark.parametrize("bits_", [8, 4])
+@pytest.mark.parametrize("nd", [3, 8])
+def test_scaled_quantizing_step(z, nd, bits_):
+    w = W.ragged_small(nd)
+    plan, st, full, ps = oracle_state(w)
+    e = emulation(w)
+    n = (e.S + 255) // 256
+    codes = [torch.zeros(n * 256, dtype=torch.int8, device="cuda") for _ in range(nd)]
+    scales = [torch.zeros(n, device="cuda") for _ in range(nd)]
+    scale = torch.tensor([0.21], device="cuda")
+    e.fill_grads(1)
+    z.zero3_step_qwz_scaled(e.plan, e.hp, 1, e.ptrs(e.grads[0]), 0, e.ptrs(e.master), e.ptrs(e.m),
+                            e.ptrs(e.v), e.ptrs(e.sparam), e.ptrs(codes), e.ptrs(scales), e.persist, 0,
+                            e.psi_pad, scale.data_ptr(), sid(), bits=bits_)
+    CO.scaled_step(plan, w.hparams, 1, host_grads(w, plan, 1), st, full, host_pgrads(w, plan, 1), ps,
+                   np.float32(0.21))
+    for r in range(nd):
+        assert np.array_equal(bits(f32(e.master[r])), bits(st.master[r]))
+        c, s = O.qwz_quantize(st.sparam[r], bits=bits_)
+        packed = O.qwz_pack(c, bits_)
+        assert np.array_equal(codes[r].cpu().numpy().view(np.uint8)[:packed.size], packed.view(np.uint8))
+        assert np.array_equal(bits(f32(scales[r])), bits(s))
+    assert np.array_equal(bits(f32(e.pmaster)), bits(ps.master))
+
+
+def test_persistent_gradients_apart(z):
+    """Persistent gradients that are no common offset away: a launch of their own."""
+    w = W.mini_gpt(5)
+    plan, st, full, ps = oracle_state(w)
+    e = emulation(w)
+    e.fill_grads(1)
+    apart = [torch.zeros(e.psi_s + 64 * q + 8, dtype=torch.bfloat16, device="cuda") for q in range(5)]
+    for a, g in zip(apart, e.pgrads):
+        a[:e.psi_s] = g
+    persist = z.persist_state(e.ptrs(apart), e.pmaster.data_ptr(), e.pm.data_ptr(), e.pv.data_ptr(),
+                              e.pparam.data_ptr())
+    best = z.zero3_step_clipped_workspace(e.plan, 0, e.psi_pad)[1]
+    ws = torch.empty(best, dtype=torch.uint8, device="cuda")
+    nc = torch.empty(2, device="cuda")
+    sq = torch.zeros(1, dtype=torch.float64, device="cuda")
+    G = e.ptrs(e.grads[0])
+    z.zero3_grad_square_sum(e.plan, G, 0, e.ptrs(apart), 0, e.psi_pad, 0, sq.data_ptr(), ws.data_ptr(), best,
+                            sid())
+    z.zero3_clip_coefficient(sq.data_ptr(), 0.03, nc.data_ptr(), nc[1:].data_ptr(), sid())
+    z.zero3_step_clipped(e.plan, e.hp, 1, G, 0, e.ptrs(e.master), e.ptrs(e.m), e.ptrs(e.v),
+                         e.ptrs(e.sparam), e.full.data_ptr(), persist, 0, e.psi_pad, 0.03, nc.data_ptr(),
+                         ws.data_ptr(), best, sid())
+    hG, hP = check_coefficient(w, plan, 1, 0.03, *nc.cpu().tolist())
+    CO.scaled_step(plan, w.hparams, 1, hG, st, full, hP, ps, float(nc[1]))
+    assert_state(e, st, full, ps)
+
+
+def test_clipped_steps_in_a_graph(z):
+    """Captured once, replayed twice, with new gradients each time."""
+    w = W.ragged_small(7)
+    plan, st, full, ps = oracle_state(w)
+    e = emulation(w)
+    e.fill_grads(1)
+    e.step(1, max_norm=0.03)  # makes the workspace
+    e.init_params()
+    for x in [*e.m, *e.v, e.pm, e.pv]:
+        x.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        e.step(1, max_norm=0.03)
+    coef = torch.empty(2, device="cuda")
+    for t in (1, 2):
+        e.fill_grads(t)
+        z.zero3_grad_square_sum(e.plan, e.ptrs(e.grads[0]), 0, e.ptrs(e.pgrads), 0, e.psi_pad, 0,
+                                e.square_sum.data_ptr(), e.clip_ws.data_ptr(), e.clip_ws.numel(), sid())
+        z.zero3_clip_coefficient(e.square_sum.data_ptr(), 0.03, coef.data_ptr(), coef[1:].data_ptr(), sid())
+        g.replay()
+        assert float(coef[0]) == float(e.norm)
+        CO.scaled_step(plan, w.hparams, 1, host_grads(w, plan, t), st, full, host_pgrads(w, plan, t), ps,
+                       float(coef[1]))
+        assert_state(e, st, full, ps)
+
+
+def test_gradients_that_are_not_finite(z):
+    """An infinite gradient: norm inf, coefficient 0; the other elements take a step
+    with zero gradient, its own becomes NaN.  A NaN reaches every element."""
+    w = W.mini_gpt(2)
+    for bad in (float("inf"), float("nan")):
+        e = emulation(w)
+        e.fill_grads(1)
+        e.grads[0][1][12345] = bad
+        e.step(1, max_norm=1.0)
+        assert np.isnan(float(e.norm)) if np.isnan(bad) else np.isinf(float(e.norm))
+        n = sum(int(torch.isnan(x).sum()) for x in e.m) + int(torch.isnan(e.pm).sum())
+        assert n == (2 * e.S + e.psi_s if np.isnan(bad) else 1)

@@ -21,13 +21,19 @@ section "ZeRO-2：梯度为什么也可以分片"; ZERO tutorial, cnhsyj.com, se
   3. the parameter all-gather: every rank's updated bf16 shard into every
      rank's flat buffer `full`.
 
+With max_norm the gradients are clipped by their global norm between 1 and 2:
+each rank sums the squares of its reduced slice (rank 0 those of the persistent
+group too, which every rank holds), one all-reduce of a binary64 number adds
+the sums, and the step multiplies by the coefficient that every rank takes from
+the same total.
+
 Allocation and call plumbing only: the arithmetic of step 2 is the C-ABI
 library's (or, for CPU tests, a step function the caller passes in).  No
 multicast or peer-memory access is used; the collectives are the library's.
 """
 from __future__ import annotations
 
-from typing import Callable, Optional
+from typing import Callable, Optional, Tuple
 
 import torch
 import torch.distributed as dist
@@ -52,6 +58,7 @@ class ShardedRank:
       full    [psi_pad] bf16       the all-gathered flat parameters
       pmaster, pm, pv [psi_s] fp32; pparam [psi_s] bf16: the persistent
                                    group, replicated on every rank
+      square_sum [1] fp64; norm, coef [1] fp32: clipping
     Sending the persistent gradients in every row moves the same bytes as
     their all-gather and puts them at one offset (S8) from each rank's slice,
     so the local step is a single fused launch.
@@ -59,7 +66,9 @@ class ShardedRank:
 
     def __init__(self, plan: zero3.Plan, hp, rank: int, device="cuda",
                  group: Optional[dist.ProcessGroup] = None,
-                 local_step: Optional[Callable[["ShardedRank", int], None]] = None):
+                 local_step: Optional[Callable[["ShardedRank", int], None]] = None,
+                 local_clip: Optional[Tuple[Callable[["ShardedRank"], None],
+                                            Callable[["ShardedRank", float], None]]] = None):
         info = plan.info
         self.plan, self.hp, self.rank = plan, hp, rank
         self.nd, self.S = info.n_ranks, info.shard_len
@@ -77,7 +86,13 @@ class ShardedRank:
         self.sparam, self.full = z(self.S, bf), z(self.psi_pad, bf)
         self.pmaster, self.pm, self.pv = z(self.psi_s, f32), z(self.psi_s, f32), z(self.psi_s, f32)
         self.pparam = z(self.psi_s, bf)
+        self.square_sum = z(1, torch.float64)
+        self.norm, self.coef = z(1, f32), z(1, f32)
+        self.clip_ws: Optional[torch.Tensor] = None
+        self.clipping = False  # whether the local step multiplies by coef
         self.local_step = local_step or ShardedRank.fused_step
+        self.local_square_sum, self.local_coefficient = local_clip or (
+            ShardedRank.sum_squares, ShardedRank.clip_coefficient)
 
     def slice_of(self, q: int) -> torch.Tensor:
         """The received slice r of rank q's flat gradient (S elements)."""
@@ -103,8 +118,15 @@ class ShardedRank:
         if self.psi_pad > 0:
             dist.all_gather_into_tensor(self.full, self.sparam, group=self.group)
 
-    def step(self, t: int) -> None:
+    def step(self, t: int, max_norm: Optional[float] = None) -> None:
+        """One step; with max_norm, clipped by the gradients' global norm, which
+        self.norm receives on every rank."""
         self.exchange()
+        self.clipping = max_norm is not None
+        if self.clipping:
+            self.local_square_sum(self)
+            dist.all_reduce(self.square_sum, group=self.group)
+            self.local_coefficient(self, max_norm)
         self.local_step(self, t)
         self.gather()
 
@@ -121,9 +143,32 @@ class ShardedRank:
                                  self.pmaster.data_ptr(), self.pm.data_ptr(), self.pv.data_ptr(),
                                  self.pparam.data_ptr()) if self.psi_s > 0 else None
         stream = torch.cuda.current_stream(self.dev).cuda_stream
-        zero3.zero3_step(self.plan, self.hp, t, [self.slice_of(q).data_ptr() for q in range(nd)],
-                         lo, only(self.master), only(self.m), only(self.v), only(self.sparam),
-                         self.full.data_ptr(), ps, lo, hi, stream)
+        args = (self.plan, self.hp, t, [self.slice_of(q).data_ptr() for q in range(nd)], lo,
+                only(self.master), only(self.m), only(self.v), only(self.sparam),
+                self.full.data_ptr(), ps, lo, hi)
+        if self.clipping:
+            zero3.zero3_step_scaled(*args, self.coef.data_ptr(), stream)
+        else:
+            zero3.zero3_step(*args, stream)
+
+    def sum_squares(self) -> None:
+        """The squares of this rank's reduced slice into square_sum; rank 0 adds the
+        persistent group's."""
+        lo, hi = self.rank * self.S, (self.rank + 1) * self.S
+        need = zero3.zero3_grad_square_sum_workspace(self.plan, lo, hi)
+        if self.clip_ws is None:
+            self.clip_ws = torch.empty(need, dtype=torch.uint8, device=self.dev)
+        slices = [self.slice_of(q).data_ptr() for q in range(self.nd)]
+        persist = [self.persist_of(q).data_ptr() for q in range(self.nd)] \
+            if self.rank == 0 and self.psi_s > 0 else None
+        zero3.zero3_grad_square_sum(self.plan, slices, lo, persist, lo, hi, 0,
+                                    self.square_sum.data_ptr(), self.clip_ws.data_ptr(), need,
+                                    torch.cuda.current_stream(self.dev).cuda_stream)
+
+    def clip_coefficient(self, max_norm: float) -> None:
+        zero3.zero3_clip_coefficient(self.square_sum.data_ptr(), max_norm, self.norm.data_ptr(),
+                                     self.coef.data_ptr(),
+                                     torch.cuda.current_stream(self.dev).cuda_stream)
 
     def cast_params(self) -> None:
         """bf16 shard, this rank's part of `full` and the persistent params

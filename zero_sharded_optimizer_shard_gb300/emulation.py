@@ -17,6 +17,8 @@ Layout (all separate allocations, each 512-byte aligned by the allocator):
   full          bf16  the flat all-gathered parameter buffer (psi_pad)
   pmaster/pm/pv fp32, pparam bf16: the one resident copy of the persistent group
   out           bf16  the submodule gather buffer (largest submodule)
+  clip_ws       the clipped step's workspace; norm, coef float32 [1], square_sum
+                      float64 [1] (allocated on first use)
   arena         bf16  the gather buffers of one all-gather bucket (allocated on
                       first use): each submodule of the bucket at its own
                       16-byte aligned offset
@@ -103,6 +105,7 @@ class Emulation:
         self.max_sub = max([self.plan.submodule(k)[1] for k in range(info.n_submodules)] + [0])
         self.out = A(max(self.max_sub, 1), bf)
         self.arena: Optional[torch.Tensor] = None
+        self.norm: Optional[torch.Tensor] = None  # of the last clipped step
         self._buckets: dict = {}
         self.persist = zero3.persist_state([_ptr(g) for g in self.pgrads], _ptr(self.pmaster),
                                            _ptr(self.pm), _ptr(self.pv), _ptr(self.pparam))
@@ -186,9 +189,14 @@ class Emulation:
                                 outlier_sigma=w.outlier_sigma, cuda_stream=self.sid)
 
     # ------------------------------------------------------------ the path
-    def step(self, t: int, with_persistent: bool = True) -> None:
+    def step(self, t: int, with_persistent: bool = True, max_norm: Optional[float] = None) -> None:
         """The fused ZeRO-3 step over every chunk (one launch per chunk) and
-        the persistent group."""
+        the persistent group.  With max_norm the gradients are clipped by their
+        global norm, which is left in self.norm (float32 [1]): one clipped step
+        for a single chunk, else the chunks' square sums, the coefficient and the
+        scaled steps."""
+        if max_norm is not None:
+            return self._clipped_step(t, with_persistent, max_norm)
         for c, ((a, b), G) in enumerate(zip(self.chunks, self.grads)):
             zero3.zero3_step(self.plan, self.hp, t, self.ptrs(G), a, self.ptrs(self.master),
                              self.ptrs(self.m), self.ptrs(self.v), self.ptrs(self.sparam),
@@ -196,6 +204,37 @@ class Emulation:
                              a, b, self.sid)
         if with_persistent and not self.chunks:
             zero3.zero3_persistent_step(self.plan, self.hp, t, self.persist, self.sid)
+
+    def _clipped_step(self, t: int, with_persistent: bool, max_norm: float) -> None:
+        if self.norm is None:  # the workspace of the largest call, and three numbers
+            if len(self.chunks) == 1:
+                need = zero3.zero3_step_clipped_workspace(self.plan, *self.chunks[0])[1]
+            else:
+                need = max(zero3.zero3_grad_square_sum_workspace(self.plan, a, b)
+                           for a, b in self.chunks or [(0, 0)])
+            self.clip_ws = self.alloc(need, torch.int8)
+            self.norm, self.coef = self.alloc(1, torch.float32), self.alloc(1, torch.float32)
+            self.square_sum = torch.zeros(1, dtype=torch.float64, device=self.dev)
+        ws, n_ws = _ptr(self.clip_ws), self.clip_ws.numel()
+        states = [self.ptrs(x) for x in (self.master, self.m, self.v, self.sparam)]
+        persist = self.persist if with_persistent else None
+        if len(self.chunks) == 1:
+            (a, b), G = self.chunks[0], self.grads[0]
+            zero3.zero3_step_clipped(self.plan, self.hp, t, self.ptrs(G), a, *states, _ptr(self.full),
+                                     persist, a, b, max_norm, _ptr(self.norm), ws, n_ws, self.sid)
+            return
+        pgrads = self.ptrs(self.pgrads) if with_persistent else None
+        chunks = list(zip(self.chunks, self.grads)) or [((0, 0), None)]
+        for c, ((a, b), G) in enumerate(chunks):
+            zero3.zero3_grad_square_sum(self.plan, self.ptrs(G) if G else None, a,
+                                        pgrads if c == 0 else None, a, b, int(c > 0),
+                                        _ptr(self.square_sum), ws, n_ws, self.sid)
+        zero3.zero3_clip_coefficient(_ptr(self.square_sum), max_norm, _ptr(self.norm),
+                                     _ptr(self.coef), self.sid)
+        for c, ((a, b), G) in enumerate(chunks):
+            zero3.zero3_step_scaled(self.plan, self.hp, t, self.ptrs(G) if G else None, a, *states,
+                                    _ptr(self.full), persist if c == 0 else None, a, b,
+                                    _ptr(self.coef), self.sid)
 
     def fetch(self, k: int) -> None:
         zero3.zero3_fetch_submodule(self.plan, k, self.ptrs(self.sparam), _ptr(self.pparam),
