@@ -11,6 +11,14 @@
 // there; in a round each warp has a share of one row.  The race reads the target's
 // row again, mostly from L2, and the noise; of the draft's row only what may win.
 //
+// What bounds it: one sequence, a chain of latencies (12 us: a round's loads and its
+// exchange, the verdicts, the race and its exchange).  Many, the bytes that an SM has
+// in flight: 512 sequences of five tokens (50257 bf16) move 530 MB in 127 us, 6.8 TB/s in
+// the first round and less as sequences end (floor: the rows up to the refusal and
+// the noise once, 443 MB, 65 us).  256 threads with 64 registers, four blocks per SM; 512
+// threads, five or six blocks (spills), rows or noise through shared memory, the
+// race in a launch of its own: equal or slower.
+//
 // Decisions.  Weights are binary32, with errors that are bounded as they are
 // formed.  A test or a race closer than its bound is taken again by the same
 // blocks with weights of 31 bits, row sums in 64-bit integers and scores in
@@ -118,6 +126,13 @@ __device__ __forceinline__ void stream_row(Soft& q, const T* row, int32_t V, int
     }
 }
 
+// Element k of a chunk.
+template <typename T>
+__device__ __forceinline__ float chunk_element(const Chunk<T>& c, int k) {
+    float lo, hi;
+    upk2(c.pair(k >> 1), lo, hi);
+    return k & 1 ? hi : lo;
+}
 // ------------------------------------------------- 31-bit weights, exact sums
 // 2^(n + f), |f| <= 1/2, as y / 2^31 * 2^n with 0.70 < y / 2^31 < 1.42, from the Taylor
 // series of 2^f = e^(f ln 2), terms (f ln 2)^k / k!, k <= 9 (the next is below 8e-12),
@@ -315,12 +330,6 @@ struct Noise8 {
         return f[k + PH];
     }
 };
-template <typename T>
-__device__ __forceinline__ float chunk_element(const Chunk<T>& c, int k) {
-    float lo, hi;
-    upk2(c.pair(k >> 1), lo, hi);
-    return k & 1 ? hi : lo;
-}
 template <typename T, int PH>
 __device__ __forceinline__ int32_t sieve_chunk(const Sieve& sieve, const Chunk<T>& x, const Noise8& e) {
     int32_t least = 0x7fffffff;
@@ -377,19 +386,30 @@ template <typename T>
 __device__ __forceinline__ uint64_t exact_share(const T* row, int32_t V, float scale, float mz, int rank,
                                                 int C, int bits) {
     uint64_t s = 0;
-    const int64_t step = static_cast<int64_t>(C) * kNT;
-    for (int64_t i = rank * kNT + threadIdx.x; i < V; i += 4 * step) {
-        Weight w[4];
+    const int step = C * kNT;
+    // four at a time, the next four on their way (few registers: what this holds, the
+    // kernel around the call cannot)
+    float x[4];
+    const auto load = [&](int32_t i) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            w[u] = i + u * step < V ? weight31(row[i + u * step], scale, mz) : Weight{0, 0};
+        for (int u = 0; u < 4; ++u) x[u] = i < V - u * step ? to_f32(row[i + u * step]) : neg_inf();
+    };
+    int32_t i = rank * kNT + static_cast<int>(threadIdx.x);
+    load(i);
+    while (i < V) {
+        float now[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) now[u] = x[u];
+        i = i < V - 4 * step ? i + 4 * step : V;
+        load(i);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int shift = bits - 31 + w[u].n;  // y * 2^shift
+            const Weight w = weight31(now[u], scale, mz);
+            const int shift = bits - 31 + w.n;  // y * 2^shift
             if (shift >= 0)
-                s += static_cast<uint64_t>(w[u].y) << (shift < 32 ? shift : 32);
+                s += static_cast<uint64_t>(w.y) << (shift < 32 ? shift : 32);
             else if (shift > -34)  // rounded: the errors of many small weights cancel
-                s += (w[u].y + (uint64_t{1} << (-shift - 1))) >> -shift;
+                s += (w.y + (uint64_t{1} << (-shift - 1))) >> -shift;
         }
     }
     return s;
@@ -509,26 +529,42 @@ __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, T
 
 // The race among the tokens whose upper bound reaches `low`, with 31-bit weights
 // and scores in binary64; ties to the lowest token, -1 if no score is positive.
-template <typename TX, typename TY>
+template <typename TX, typename TY, bool DRAFT>
 __device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Rows<TX, TY>& r, const Sums& sums,
                                            float low, int32_t V, int rank, int C) {
     double best = 0.0;
     int32_t token = 0x7fffffff;
-    for (int64_t i = rank * kNT + threadIdx.x; i < V; i += static_cast<int64_t>(C) * kNT) {
-        const TX x = r.x[i];
-        const TY y = r.y ? r.y[i] : TY(0);
-        const float e = r.e[i];
-        float s, off;
-        score(r, x, y, e, static_cast<int32_t>(i), s, off);
-        if (!(s + off >= low) || !(e >= 0.0f) || i == r.without) continue;
-        double v = weight64(weight31(x, r.xs, r.pm));
-        if (r.y) v = v / sums.p - weight64(weight31(y, r.ys, r.qm)) / sums.q;
-        v = v / static_cast<double>(e);
-        if (v > best) {  // tokens come in ascending order
-            best = v;
-            token = static_cast<int32_t>(i);
+    // several at a time through the sieve of the bound that the race has found; one
+    // without a draft, where a close race is one in 10^5 and registers count
+    constexpr int U = DRAFT ? 4 : 1;
+    const Sieve sieve(r.xs, r.pm);
+    const int32_t limit = sieve.limit(__float_as_uint(low));
+    const int step = C * kNT;
+    for (int32_t i0 = rank * kNT + static_cast<int>(threadIdx.x); i0 < V;
+         i0 = i0 < V - U * step ? i0 + U * step : V) {
+        unsigned let = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 < V - u * step && sieve.of(to_f32(r.x[i0 + u * step]), r.e[i0 + u * step]) <= limit)
+                let |= 1u << u;
+        for (; let; let &= let - 1) {
+            const int32_t i = i0 + (__ffs(let) - 1) * step;
+            const TX x = r.x[i];
+            const TY y = r.y ? r.y[i] : TY(0);
+            const float e = r.e[i];
+            float s, off;
+            score(r, x, y, e, i, s, off);
+            if (!(s + off >= low) || !(e >= 0.0f) || i == r.without) continue;
+            double v = weight64(weight31(x, r.xs, r.pm));
+            if (r.y) v = v / sums.p - weight64(weight31(y, r.ys, r.qm)) / sums.q;
+            v = v / static_cast<double>(e);
+            if (v > best) {  // tokens come in ascending order
+                best = v;
+                token = i;
+            }
         }
     }
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const double v = __shfl_xor_sync(0xffffffffu, best, o);
@@ -670,7 +706,7 @@ __device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const VerifyArgs&
                 m = exact_sums<TX, TY>(sh, turn, r.x, r.y, a.vocab, r.xs, r.ys, r.pm, r.qm, rank, C);
                 ++turn;
             }
-            token = exact_race<TX, TY>(sh, turn, r, m, b.low, a.vocab, rank, C);
+            token = exact_race<TX, TY, DRAFT>(sh, turn, r, m, b.low, a.vocab, rank, C);
             ++turn;
         }
         if (token >= 0 || (!r.y && r.without < 0)) break;
@@ -811,10 +847,18 @@ cudaError_t launch_types(const VerifyArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_verify(const VerifyArgs& args, cudaStream_t stream) {
     VerifyArgs a = args;
-    // as many blocks per sequence as are resident at once (four on each of 152 SMs)
+    // As many blocks per sequence as are resident at once (four on each of 152 SMs),
+    // and two at least where there are drafts: with one, an SM whose sequences are all
+    // accepted far ends last (512 of 50257, ten tokens without probabilities: 130
+    // us with one, 104 with two; five with: 123 and 126; no draft: 49 and 53).
     a.cluster = 1;
     while (a.cluster < kMaxCluster && a.n * a.cluster * 2 <= 608) a.cluster *= 2;
-    a.ahead = a.y ? (a.n <= 100 ? 3 : 2) : (a.n <= 200 ? 7 : 3);
+    if (a.k > 0 && a.cluster == 1) a.cluster = 2;
+    // Positions per round, a row of which a warp has: all of them at once while
+    // the chain of rounds is the time (48 sequences of ten: 45 us one by one, 23 by
+    // seven), two where rows that turn out not to be needed are (512 of ten: 126 us by
+    // seven, 104 by two; 256 of five drafts: 76 by three, 71 by two, 73 one by one).
+    a.ahead = a.y ? (a.n <= 100 ? 3 : 2) : (a.n <= 200 ? 7 : 2);
     const int g = a.ahead < a.k ? a.ahead : a.k, rows = (a.y ? 2 * g : g) + 1;
     // Relative error of a row's sum.  Its terms: the unit's two ulp (2^-22), three
     // roundings of t, 1.2 * 2^-23 |t| on their average |t|, which is at most log2(V); a
