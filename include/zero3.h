@@ -624,7 +624,7 @@ zero3_status zero3_grad_norm(const void* const* tensors, const int64_t* numels, 
 /* out[i] = coef * tensors[i], rounded to binary32 and then to out_dtype; *coef is
  * one binary32 number in device memory.  out NULL: in place (then, and where
  * out[i] = tensors[i], the dtypes must be equal, and a coefficient of 1 writes
- * nothing).  Otherwise no output may overlap an input. */
+ * nothing).  Otherwise no output may overlap an input; no two outputs may overlap. */
 zero3_status zero3_clip_grads(const void* const* tensors, const int64_t* numels, int64_t n_tensors,
                               zero3_dtype dtype, const float* coef, void* const* out,
                               zero3_dtype out_dtype, zero3_stream stream);

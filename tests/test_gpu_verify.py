@@ -265,6 +265,19 @@ def test_probabilities_far_below_binary32(z):
     assert 0 < got[0].sum() < 40
 
 
+@pytest.mark.parametrize("unit", [1e-35, 1e30])
+@pytest.mark.parametrize("draft", ["f32", None])
+def test_logits_in_other_units(z, unit, draft):
+    """Tiny logits under a huge inverse temperature, and the other way round."""
+    c = Case(30, 2, 1200, "f32", draft, seed=13, scale=1 / unit, draft_scale=1 / unit)
+    c.x = (c.x.double() * unit).float()
+    c.ids = c.ids % 1200
+    if draft:
+        c.y = (c.y.double() * unit).float()
+        c.ids[:] = c.y.argmax(2)
+    c.run(z)
+
+
 def test_a_draft_equal_to_the_target(z):
     """Accepted at every u below 1; at u = 1 there is no residual and the draw is
     from the target."""

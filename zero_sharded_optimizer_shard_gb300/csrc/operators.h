@@ -1,5 +1,6 @@
-// Launch descriptions of the vocabulary operators, shared by their C ABI
-// (operators.cpp) and their kernels.
+// Launch descriptions of the vocabulary operators, the gradient lists and the
+// verification of drafted tokens, shared by their C ABI (operators.cpp, clip.cpp)
+// and their kernels.
 #pragma once
 
 #include <cstdint>

@@ -298,7 +298,7 @@ struct Sieve {
         // T is off by half a unit, and by the roundings of a and c; where they
         // overflow nothing is passed over
         const float m = 0x1p-13f + (fabsf(mz) + 150.0f) * 0x1p-21f;
-        margin = m < 64.0f ? static_cast<int32_t>(m * 8388608.0f) : 0x7fffffff;
+        margin = m < 64.0f && a < 0x1p100f ? static_cast<int32_t>(m * 8388608.0f) : 0x7fffffff;
     }
     // bits(e) - 512 T - bits(1): the bound with its sign turned.  Negative e are
     // never drawn and may come out anyhow.
