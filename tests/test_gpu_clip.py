@@ -153,6 +153,17 @@ def test_norm_beyond_the_range_of_squares(z, dtype, value):
     assert abs(coef - wcoef) <= NORM_TOL * wcoef + 2.0 ** -149
 
 
+@pytest.mark.parametrize("value", [2.0 ** 60, 2.0 ** 50, 2.0 ** -40])
+def test_norm_of_a_large_tensor_beyond_the_range_of_squares(z, value):
+    """2^30 equal numbers: a thread's 8 * 108 squares, and all other sums, are small
+    integers times a power of two, which binary32 holds exactly."""
+    x = torch.full((2 ** 30,), value, device="cuda", dtype=torch.bfloat16)
+    _, sq, total, coef = norm(z, z.TensorList([x.data_ptr()], [x.numel()], z.BF16), 1.0, tensor_norms=False)
+    assert sq == value * value * 2.0 ** 30
+    assert total == value * 2.0 ** 15
+    assert coef == min(1.0, float(np.float32(1.0 / (value * 2.0 ** 15 + 1e-6))))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_over_mixed_magnitudes(z, dtype):
     """Large and small numbers in one thread's share."""

@@ -43,13 +43,14 @@ __device__ __forceinline__ uint32_t bits_of(const Chunk<float>& c) {
     return u & 0x7fffffffu;
 }
 
-// Squares over the whole range of binary32: three sums, of numbers above 2^60
-// (times 2^-90), below 2^-40 (times 2^90) and between.
+// Squares over the whole range of binary32: three sums, of numbers above 2^50
+// (times 2^-90), below 2^-40 (times 2^90) and between.  2^27 squares of a thread fit
+// each of them.
 struct WideSquares {
     float big = 0.0f, mid = 0.0f, small = 0.0f;
     __device__ __forceinline__ void add(float x) {
         const float ax = fabsf(x);
-        if (ax > 0x1p60f) {
+        if (ax > 0x1p50f) {
             const float t = x * 0x1p-90f;
             big = fmaf(t, t, big);
         } else if (ax < 0x1p-40f) {
