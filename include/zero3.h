@@ -796,8 +796,9 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
  *    makes the drawn token -1 with a NaN log probability; in a draft row it refuses
  *    the token.
  * uniform [n, k], noise [n, vocab] with noise_stride; logits and draft_logits with
- * their strides.  draft_ids and uniform may be NULL when k = 0.  EINVAL also for k
- * outside [0, ZERO3_MAX_DRAFT] and n * (k + 1) above 2^27. */
+ * their strides.  draft_ids and uniform may be NULL when k = 0; no input may change
+ * before the call's work is done.  EINVAL also for k outside [0, ZERO3_MAX_DRAFT],
+ * n * (k + 1) above 2^27 and an output that overlaps an input. */
 zero3_status zero3_verify_draft(const void* logits, zero3_dtype dtype, int64_t n, int32_t k,
                                 int64_t vocab, int64_t stride, const void* draft_logits,
                                 zero3_dtype draft_dtype, int64_t draft_stride,

@@ -5,6 +5,7 @@ import ctypes as C
 import pytest
 
 A = 1 << 20  # a plausible, aligned address that is never read
+B = 1 << 30  # and one for outputs
 NAN, INF = float("nan"), float("inf")
 
 
@@ -24,7 +25,7 @@ def i64(*v):
 
 VERIFY = dict(logits=A, dtype=0, n=4, k=3, vocab=100, stride=100, draft_logits=A, draft_dtype=1,
               draft_stride=100, draft_ids=A, id_type=1, inv_temperature=1.0, draft_inv_temperature=1.0,
-              uniform=A, noise=A, noise_stride=100, accepted=A, tokens=A, logprobs=A, stream=None)
+              uniform=A, noise=A, noise_stride=100, accepted=B, tokens=B, logprobs=B, stream=None)
 
 
 @pytest.mark.parametrize("name,value", [
@@ -33,10 +34,21 @@ VERIFY = dict(logits=A, dtype=0, n=4, k=3, vocab=100, stride=100, draft_logits=A
     ("draft_dtype", 2), ("draft_stride", 99), ("draft_ids", None), ("draft_ids", A + 4), ("id_type", 2),
     ("inv_temperature", 0.0), ("inv_temperature", NAN), ("inv_temperature", INF),
     ("draft_inv_temperature", -1.0), ("draft_inv_temperature", NAN), ("uniform", None), ("uniform", A + 2),
-    ("noise", None), ("noise", A + 1), ("noise_stride", 99), ("accepted", None), ("accepted", A + 2),
-    ("tokens", None), ("tokens", A + 1), ("logprobs", A + 3)])
+    ("noise", None), ("noise", A + 1), ("noise_stride", 99), ("accepted", None), ("accepted", B + 2),
+    ("tokens", None), ("tokens", B + 1), ("logprobs", B + 3)])
 def test_verify_refuses(z, name, value):
     assert z.raw_status("zero3_verify_draft", *dict(VERIFY, **{name: value}).values()) == z.EINVAL
+
+
+@pytest.mark.parametrize("output,bytes_", [("accepted", 4 * 4), ("tokens", 4 * 4 * 4), ("logprobs", 4 * 4 * 4)])
+@pytest.mark.parametrize("name,size", [("logits", 2 * 16 * 100), ("draft_logits", 4 * 12 * 100),
+                                       ("draft_ids", 8 * 12), ("uniform", 4 * 12), ("noise", 4 * 4 * 100)])
+def test_verify_refuses_outputs_over_inputs(z, output, bytes_, name, size):
+    """The first and the last place where they share 4 bytes."""
+    for at in (B + 4 - bytes_, B + size - 4):
+        args = dict(VERIFY, accepted=2 * B, tokens=2 * B, logprobs=2 * B)
+        args.update({name: B, output: at})
+        assert z.raw_status("zero3_verify_draft", *args.values()) == z.EINVAL
 
 
 def test_verify_of_no_sequence(z):

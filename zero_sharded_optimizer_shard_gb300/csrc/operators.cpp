@@ -41,6 +41,22 @@ bool logits_ok(int64_t n, int64_t vocab, int64_t stride) {
     return n <= kMaxRows && vocab <= kMaxVocab && rows_ok(n, vocab, stride);
 }
 
+// Bytes of n rows of `cols` elements of `size` bytes, and whether two ranges have
+// one in common.
+struct Bytes {
+    const void* at;
+    unsigned __int128 size;
+};
+Bytes rows_bytes(const void* p, int64_t n, int64_t cols, int64_t stride, int64_t size) {
+    if (!p || n <= 0) return Bytes{p, 0};
+    return Bytes{p, (static_cast<unsigned __int128>(n - 1) * static_cast<uint64_t>(stride) +
+                     static_cast<uint64_t>(cols)) * static_cast<uint64_t>(size)};
+}
+bool overlap(const Bytes& a, const Bytes& b) {
+    const unsigned __int128 a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
+    return a.size > 0 && b.size > 0 && a0 < b0 + b.size && b0 < a0 + a.size;
+}
+
 // An embedding's two matrices.
 bool embedding_ok(int64_t vocab, int64_t dim, int64_t table_stride, int64_t n, int64_t row_stride) {
     return vocab >= 1 && vocab <= kMaxVocab && dim <= kMaxDim && rows_ok(vocab, dim, table_stride) &&
@@ -295,6 +311,18 @@ zero3_status zero3_verify_draft(const void* logits, zero3_dtype dtype, int64_t n
         return ZERO3_EINVAL;
     if (draft && !ptr_ok(draft_logits, size_of(draft_dtype))) return ZERO3_EINVAL;
     if (k > 0 && (!ptr_ok(draft_ids, size_of(id_type)) || !ptr_ok(uniform, 4))) return ZERO3_EINVAL;
+    // A sequence's blocks each read what decides and have to decide alike: no result
+    // of another sequence may change it.
+    const Bytes in[] = {rows_bytes(logits, n * (k + 1), vocab, stride, size_of(dtype)),
+                        rows_bytes(draft ? draft_logits : nullptr, n * k, vocab, draft_stride,
+                                   size_of(draft_dtype)),
+                        rows_bytes(draft_ids, n, k, k, size_of(id_type)), rows_bytes(uniform, n, k, k, 4),
+                        rows_bytes(noise, n, vocab, noise_stride, 4)};
+    const Bytes out[] = {rows_bytes(accepted, n, 1, 1, 4), rows_bytes(tokens, n, k + 1, k + 1, 4),
+                         rows_bytes(logprobs, n, k + 1, k + 1, 4)};
+    for (const Bytes& o : out)
+        for (const Bytes& i : in)
+            if (overlap(o, i)) return ZERO3_EINVAL;
     z3::VerifyArgs a;
     a.x = logits;
     a.y = draft ? draft_logits : nullptr;
