@@ -617,7 +617,7 @@ __device__ __noinline__ int decide(Shared& sh, int turn, const VerifyArgs& a, co
 
 // Position j, number g of the round, from the rows' sums (one warp).
 template <typename TX, typename TY, bool DRAFT>
-__device__ __forceinline__ void judge(Shared& sh, int turn, const VerifyArgs& a, int R, int g, int j, bool drafted,
+__device__ __forceinline__ void weigh(Shared& sh, int turn, const VerifyArgs& a, int R, int g, int j, bool drafted,
                                       const TX* xr, const TY* yr) {
     const int lane = threadIdx.x & 31;
     const int row = (DRAFT ? 2 * g : g) + (DRAFT && lane >= 16 && drafted);
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
         }
         if (warp < G + whole) {
             const int j = j0 + warp;
-            judge<TX, TY, DRAFT>(sh, turn, a, R, warp, j, warp < G, x + j * a.stride,
+            weigh<TX, TY, DRAFT>(sh, turn, a, R, warp, j, warp < G, x + j * a.stride,
                                  DRAFT ? y + j * a.y_stride : nullptr);
         }
         ++turn;
