@@ -318,3 +318,63 @@ def test_the_same_draw_over_again_and_in_a_graph(z):
         g.replay()
         np.testing.assert_array_equal(acc.cpu().numpy(), first[0])
         np.testing.assert_array_equal(tok.cpu().numpy(), first[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V", [(1, 1), (2, 7), (3, 9), (1, 50257), (5, 4099), (33, 1025), (70, 2050),
+                                 (140, 8191), (300, 1537), (700, 515)])
+def test_sampling(z, n, V, dtype):
+    """Without a draft, at every cluster size."""
+    Case(n, 0, V, dtype, None, scale=1.25 if n % 2 else 0.8, seed=20).run(z)
+
+
+@pytest.mark.parametrize("pad,shift", [(1, 0), (0, 1), (3, 5), (8, 7), (2, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sampling_strides_and_alignment(z, pad, shift, dtype):
+    for n in (3, 40, 310):
+        Case(n, 0, 2500, dtype, None, pad=pad, shift=shift, seed=21).run(z)
+
+
+@pytest.mark.parametrize("n", [1, 20, 320])
+def test_sampling_where_the_largest_logits_come_late(z, n):
+    """Rows that rise by 200, 60 and 30 over the row, that rise at the last element, that
+    begin with masked tokens or hold one token only."""
+    c = Case(n, 0, 20011, "f32", None, seed=22)
+    at = torch.arange(20011) / 20010.0
+    for s in range(n):
+        c.x[s, 0] += at * (200.0, 60.0, 30.0, 0.0, -60.0, -200.0)[s % 6]
+        if s % 7 == 1:
+            c.x[s, 0, -1] += 150.0
+        if s % 5 == 2:
+            c.x[s, 0, :19000] = -float("inf")
+        if s % 11 == 3:
+            c.x[s, 0, torch.arange(20011) != 20010 - s] = -float("inf")
+    c.run(z)
+
+
+def test_sampling_against_noise_of_all_sizes(z):
+    """Noise from 1e-37 to 1e38, which moves the winner to unlikely tokens."""
+    c = Case(64, 0, 3001, "f32", None, seed=23)
+    g = torch.Generator().manual_seed(24)
+    c.noise = torch.exp2(torch.rand(64, 3001, generator=g) * 250 - 123)
+    c.run(z)
+
+
+def test_sampling_of_equal_scores(z):
+    c = Case(50, 0, 4001, "bf16", None, seed=25)
+    c.x[:, 0] = 1.0
+    c.noise[:] = 0.5
+    c.noise[:, :100] = 2.0
+    assert (c.run(z)[1][:, 0] == 100).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sampling_rows_that_are_not_finite(z, dtype):
+    c = Case(8, 0, 5000, dtype, None, seed=26)
+    c.x[0, 0, 4999] = float("nan")
+    c.x[1, 0, 0] = float("inf")
+    c.x[2, 0] = float("nan")
+    c.x[3, 0] = -float("inf")
+    c.x[4, 0] = torch.finfo(c.x.dtype).min
+    c.x[5, 0, 1::2] = torch.finfo(c.x.dtype).min
+    c.run(z)

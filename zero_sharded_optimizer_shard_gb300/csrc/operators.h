@@ -135,7 +135,6 @@ struct VerifyArgs {
     float scale, y_scale;
     int32_t dtype, y_dtype, id64;
     int32_t cluster, ahead;  // blocks per sequence, positions per round (set by the launch)
-    int32_t pd, pr;
     float sum_error;         // relative, of a row's sum (set by the launch)
 };
 

@@ -836,9 +836,243 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
     }
 }
 
+// ------------------------------------------------------------ without a draft
+// Sampling (k = 0): the winner does not hang on the row's sum, so statistics and race
+// share one pass over row and noise and one exchange.  A warp's scores are relative to
+// a reference of its own (within 40 of the largest z it has met), and are taken to the
+// row's largest when they are joined.
+constexpr float kReach = 40.0f;
+
+// Scores relative to `from` taken to `to`.  Bounds stay bounds: an upper one gets the
+// least normal number on top, a lower one is given up where little is left.
+__device__ __forceinline__ void race_rebase(Race& r, float from, float to) {
+    const float t = __fmul_rn(__fsub_rn(from, to), kLog2e);
+    const float f = exp2_approx(0.5f * t), err = fmaf(fabsf(t), 0x1p-22f, 0x1p-20f);
+    r.low = t > -60.0f ? r.low * f * f * (1.0f - err) : 0.0f;
+    if (r.up > 0.0f && r.up < pos_inf()) r.up = fmaf(r.up * f, f * (1.0f + err), 0x1p-126f);
+    if (r.second > 0.0f && r.second < pos_inf()) r.second = fmaf(r.second * f, f * (1.0f + err), 0x1p-126f);
+}
+
+template <typename TX>
+__device__ __noinline__ int32_t draw_again(Shared& sh, const VerifyArgs& a, float pm, float ps, const TX* xr,
+                                           const float* noise, int rank) {
+    Position o;
+    o.pm = pm;
+    o.ps = ps;
+    o.qm = o.qs = o.xd = o.yd = o.u = 0.0f;
+    o.token = -1;
+    int turn = 1;
+    return draw<TX, TX, false>(sh, turn, a, o, kEnd, xr, nullptr, noise, rank);
+}
+
+template <typename TX>
+__global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ VerifyArgs a) {
+    __shared__ Shared sh;
+    __shared__ uint4 more[kWarps][kMaxCluster];
+    const int C = a.cluster;
+    const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+    if (C > 1) cluster_arrive();
+    const int64_t s = blockIdx.x / C;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const int32_t V = a.vocab;
+    const float scale = a.scale;
+    const TX* x = static_cast<const TX*>(a.x) + s * a.stride;
+    const float* noise = a.noise + s * a.noise_stride;
+    wait_prior_grids();
+    allow_next_grid();
+    if (tid < 2) sh.low[tid] = 0;
+    const RowCut<TX> cut(x, V);
+    const int step = C * kNT;
+    const TX* xs = x + cut.head;
+    const float* es = noise + cut.head;
+    const int ep = phase_of(es);
+    Soft q = soft_empty();
+    Race b{0.0f, 0.0f, 0.0f, -1};
+    Rows<TX, TX> r;
+    r.x = x;
+    r.y = nullptr;
+    r.e = noise;
+    r.xs = scale;
+    r.ys = 1.0f;
+    r.pm = neg_inf();  // the reference
+    r.qm = r.ratio = r.ratio_error = 0.0f;
+    r.without = -1;
+    float low = 0.0f, reach = neg_inf();
+    // a lower bound counts if the weight is far from the end of the range
+    const auto look = [&](TX v, float e, int32_t i) {
+        float sc, off;
+        score(r, v, TX(0), e, i, sc, off);
+        const float l = sc * e >= 0x1p-60f ? sc - off : 0.0f;
+        race_add(b, l, sc + off, i);
+        return l;
+    };
+    // the lanes' largest z: moves the reference if it is out of reach (all lanes)
+    const auto meet = [&](float z) {
+        if (!__any_sync(0xffffffffu, z > reach)) return;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+        if (r.pm != neg_inf()) {
+            race_rebase(b, r.pm, z);
+            b.low = low = 0.0f;
+        }
+        r.pm = z;
+        reach = z + kReach;
+    };
+    Chunk<TX> nx;
+    Noise8 ne;
+    int c = rank * kNT + tid;
+    if (c < cut.chunks) {
+        nx.load(xs + 8 * c);
+        ne.load(es + 8 * c, ep);
+    }
+    for (; c - lane < cut.chunks; c += step) {
+        Chunk<TX> xc[1];
+        xc[0] = nx;
+        const Noise8 e = ne;
+        if (c + step < cut.chunks) {
+            nx.load(xs + 8 * (c + step));
+            ne.load(es + 8 * (c + step), ep);
+        }
+        const bool mine = c < cut.chunks;
+        float z = neg_inf();
+        if (mine) {
+            z = __fmul_rn(xc[0].max(), scale);
+            soft_add<TX, false, 1>(q, xc, scale);
+        }
+        __syncwarp();
+        meet(z);
+        if (r.pm == neg_inf()) continue;  // masked tokens only
+        const Sieve sieve(scale, r.pm);
+        int32_t least = 0x7fffffff;
+        switch (ep) {
+            case 0: least = sieve_chunk<TX, 0>(sieve, xc[0], e); break;
+            case 1: least = sieve_chunk<TX, 1>(sieve, xc[0], e); break;
+            case 2: least = sieve_chunk<TX, 2>(sieve, xc[0], e); break;
+            default: least = sieve_chunk<TX, 3>(sieve, xc[0], e); break;
+        }
+        if (!mine) least = 0x7fffffff;
+        const int32_t i0 = cut.head + 8 * c;
+        if (low == 0.0f) {
+            // a first lower bound: of the warp's most promising chunk
+            const int32_t best = __reduce_min_sync(0xffffffffu, least);
+            const int from = __ffs(__ballot_sync(0xffffffffu, least == best)) - 1;
+            const int32_t i = __shfl_sync(0xffffffffu, i0, from) + (lane & 7);
+            float l = 0.0f;
+            if (lane < 8) {
+                float sc, off;
+                score(r, x[i], TX(0), noise[i], i, sc, off);
+                if (sc * noise[i] >= 0x1p-60f) l = fmaxf(sc - off, 0.0f);
+            }
+            __syncwarp();
+            low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(l)));
+        }
+        unsigned let = __ballot_sync(0xffffffffu, mine && least <= sieve.limit(__float_as_uint(low)));
+        if (let == 0) continue;
+        if (__popc(let) > 4) {
+            if (let >> lane & 1) {
+#pragma unroll 4
+                for (int k = 0; k < 8; ++k) look(x[i0 + k], noise[i0 + k], i0 + k);
+            }
+        } else {  // eight lanes for each chunk
+            int from = 0;
+            bool any = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k == lane >> 3 && let) {
+                    from = __ffs(let) - 1;
+                    any = true;
+                }
+                let &= let - 1;
+            }
+            const int32_t i = __shfl_sync(0xffffffffu, i0, from) + (lane & 7);
+            if (any) look(x[i], noise[i], i);
+        }
+        __syncwarp();
+        low = fmaxf(low, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.low))));
+    }
+    // the ends of the row
+    if (rank == 0 && warp == 0) {
+        const int32_t i = lane < 16 ? edge_element(0, cut.head, cut.head + 8 * cut.chunks, V) : -1;
+        float z = neg_inf();
+        if (i >= 0) {
+            Chunk<TX> xc[1];
+            xc[0].fill(neg_inf());
+            xc[0].set(0, x[i]);
+            z = __fmul_rn(xc[0].max(), scale);
+            soft_add<TX, false, 1>(q, xc, scale);
+        }
+        __syncwarp();
+        meet(z);
+        if (i >= 0 && r.pm != neg_inf()) look(x[i], noise[i], i);
+    }
+    __syncwarp();
+    soft_lanes<false, 32>(q);
+    b = race_lanes(b);
+    {
+        const uint4 v = make_uint4(__float_as_uint(q.mz), __float_as_uint(q.s), __float_as_uint(b.low),
+                                   __float_as_uint(b.up));
+        const uint4 w = make_uint4(__float_as_uint(b.second), static_cast<uint32_t>(b.token),
+                                   __float_as_uint(r.pm), 0u);
+        if (C == 1) {
+            if (lane == 0) {
+                sh.parts[0][warp][0] = v;
+                more[warp][0] = w;
+            }
+            __syncthreads();
+        } else {
+            cluster_wait();  // the others' shared memory is there
+            if (lane < C) {
+                send16(&sh.parts[0][warp][rank], lane, v);
+                send16(&more[warp][rank], lane, w);
+            }
+            cluster_sync();
+        }
+    }
+    // every warp joins all of them: lane i has the parts i and i + 32
+    Soft h = soft_empty();
+    if (lane < kWarps * C) h = unpack(sh.parts[0][lane / C][lane % C]);
+    if (lane + 32 < kWarps * C) {
+        Soft g = unpack(sh.parts[0][(lane + 32) / C][(lane + 32) % C]);
+        float top = fmaxf(soft_top(h), soft_top(g));
+        if (top == neg_inf()) top = 0.0f;
+        soft_rebase<false>(h, top);
+        soft_rebase<false>(g, top);
+        h.s = __fadd_rn(h.s, g.s);
+        if (top == pos_inf()) h.s = __int_as_float(0x7fffffff);
+    }
+    __syncwarp();
+    soft_lanes<false, 32>(h);
+    int32_t token = -1;
+    float lp = __int_as_float(0x7fffffff);
+    if (h.s == 0.0f) lp = neg_inf();
+    if (h.s > 0.0f) {
+        Race best{0.0f, 0.0f, 0.0f, -1};
+        for (int j = lane; j < kWarps * C; j += 32) {
+            const uint4 v = sh.parts[0][j / C][j % C], w = more[j / C][j % C];
+            Race o{__uint_as_float(v.z), __uint_as_float(v.w), __uint_as_float(w.x), static_cast<int32_t>(w.y)};
+            if (__uint_as_float(w.z) != neg_inf()) race_rebase(o, __uint_as_float(w.z), h.mz);
+            race_join(best, o);
+        }
+        __syncwarp();
+        best = race_lanes(best);
+        if (best.low > 0.0f && best.second < best.low)
+            token = best.token;
+        else
+            token = draw_again<TX>(sh, a, h.mz, h.s, x, noise, rank);
+        if (token >= 0 && rank == 0) lp = __fsub_rn(fmaf(to_f32(x[token]), scale, -h.mz), logf(h.s));
+        if (token < 0) lp = neg_inf();
+    }
+    if (rank == 0 && tid == 0) {
+        a.accepted[s] = 0;
+        a.tokens[s] = token;
+        if (a.logprobs) a.logprobs[s] = lp;
+    }
+}
+
 template <typename TX, typename TY>
 cudaError_t launch_types(const VerifyArgs& a, cudaStream_t stream) {
     const int64_t grid = a.n * a.cluster;
+    if (a.k == 0) return launch_vocab(sample_kernel<TX>, grid, kNT, 0, a.cluster, a, stream);
     return a.y ? launch_vocab(verify_kernel<TX, TY, true>, grid, kNT, 0, a.cluster, a, stream)
                : launch_vocab(verify_kernel<TX, TX, false>, grid, kNT, 0, a.cluster, a, stream);
 }
