@@ -838,19 +838,72 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------ without a draft
 // Sampling (k = 0): the winner does not hang on the row's sum, so statistics and race
-// share one pass over row and noise and one exchange.  A warp's scores are relative to
-// a reference of its own (within 40 of the largest z it has met), and are taken to the
-// row's largest when they are joined.
-constexpr float kReach = 40.0f;
+// share one pass over row and noise and one exchange.  A warp's weights are relative
+// to the largest z that it has met, and are taken to the row's largest when the warps
+// are joined.
 
 // Scores relative to `from` taken to `to`.  Bounds stay bounds: an upper one gets the
 // least normal number on top, a lower one is given up where little is left.
 __device__ __forceinline__ void race_rebase(Race& r, float from, float to) {
     const float t = __fmul_rn(__fsub_rn(from, to), kLog2e);
     const float f = exp2_approx(0.5f * t), err = fmaf(fabsf(t), 0x1p-22f, 0x1p-20f);
-    r.low = t > -60.0f ? r.low * f * f * (1.0f - err) : 0.0f;
+    r.low = t > -30.0f ? r.low * f * f * (1.0f - err) : 0.0f;
     if (r.up > 0.0f && r.up < pos_inf()) r.up = fmaf(r.up * f, f * (1.0f + err), 0x1p-126f);
     if (r.second > 0.0f && r.second < pos_inf()) r.second = fmaf(r.second * f, f * (1.0f + err), 0x1p-126f);
+}
+
+// Weights 2^((x scale - ref) log2(e)) of a chunk and their sum.
+template <typename T>
+__device__ __forceinline__ float chunk_weights(const Chunk<T>& x, float scale, float ref, float (&w)[8]) {
+    const uint64_t sc = pk2(scale, scale), nr = pk2(-ref, -ref), l2 = pk2(kLog2e, kLog2e);
+    uint64_t s[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float t0, t1;
+        upk2(mul2(fma2(x.pair(k), sc, nr), l2), t0, t1);
+        w[2 * k] = exp2_approx(t0);
+        w[2 * k + 1] = exp2_approx(t1);
+        s[k & 1] = add2(s[k & 1], pk2(w[2 * k], w[2 * k + 1]));
+    }
+    float a, b;
+    upk2(add2(s[0], s[1]), a, b);
+    return __fadd_rn(a, b);
+}
+// A chunk's noise in its order.
+__device__ __forceinline__ void in_order(const Noise8& e, int ph, float (&v)[8]) {
+    switch (ph) {
+        case 0:
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = e.get<0>(k);
+            break;
+        case 1:
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = e.get<1>(k);
+            break;
+        case 2:
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = e.get<2>(k);
+            break;
+        default:
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = e.get<3>(k);
+    }
+}
+
+// A token's score w / e, from a weight 2^t.  Relative errors: |t| 2^-23 of t's three
+// roundings, the units' two ulp and one, the product's; a lower bound counts if the weight
+// is far from the end of the range.  Nothing is drawn at e < 0 or NaN; 0 wins, and is
+// decided in 64 bits, as is a subnormal e.
+__device__ __forceinline__ void race_token(Race& b, float w, float e, int32_t i) {
+    const float inv = reciprocal(e);
+    const float v = w * inv;
+    const float off = v * (w > 0x1p-16f ? 0x1.8p-19f : 0x1p-15f);
+    float low = w >= 0x1p-60f ? v - off : 0.0f, up = v + off;
+    if (!(e > 0.0f && inv < pos_inf())) {
+        low = 0.0f;
+        up = e >= 0.0f && w > 0.0f ? pos_inf() : 0.0f;
+    }
+    race_add(b, low, up, i);
 }
 
 template <typename TX>
@@ -886,106 +939,64 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     const TX* xs = x + cut.head;
     const float* es = noise + cut.head;
     const int ep = phase_of(es);
-    Soft q = soft_empty();
+    float sum = 0.0f;
     Race b{0.0f, 0.0f, 0.0f, -1};
-    Rows<TX, TX> r;
-    r.x = x;
-    r.y = nullptr;
-    r.e = noise;
-    r.xs = scale;
-    r.ys = 1.0f;
-    r.pm = neg_inf();  // the reference
-    r.qm = r.ratio = r.ratio_error = 0.0f;
-    r.without = -1;
-    float low = 0.0f, reach = neg_inf();
-    // a lower bound counts if the weight is far from the end of the range
-    const auto look = [&](TX v, float e, int32_t i) {
-        float sc, off;
-        score(r, v, TX(0), e, i, sc, off);
-        const float l = sc * e >= 0x1p-60f ? sc - off : 0.0f;
-        race_add(b, l, sc + off, i);
-        return l;
-    };
-    // the lanes' largest z: moves the reference if it is out of reach (all lanes)
+    float ref = neg_inf();
+    // `low`: of a score that some token of the warp has; base: the reference of the oldest
+    float low = 0.0f, base = neg_inf();
+    // The lanes' largest z: the warp's weights become relative to it (all lanes).
     const auto meet = [&](float z) {
-        if (!__any_sync(0xffffffffu, z > reach)) return;
+        if (!__any_sync(0xffffffffu, z > ref)) return;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-        if (r.pm != neg_inf()) {
-            race_rebase(b, r.pm, z);
-            b.low = low = 0.0f;
+        if (ref != neg_inf()) {
+            sum = __fmul_rn(sum, exp2_approx(__fmul_rn(__fsub_rn(ref, z), kLog2e)));
+            race_rebase(b, ref, z);
+            if (!(z - base < 20.0f)) {
+                b.low = 0.0f;
+                base = z;
+            }
+            low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.low)));
+        } else {
+            base = z;
         }
-        r.pm = z;
-        reach = z + kReach;
+        ref = z;
     };
     Chunk<TX> nx;
     Noise8 ne;
     int c = rank * kNT + tid;
-    if (c < cut.chunks) {
-        nx.load(xs + 8 * c);
-        ne.load(es + 8 * c, ep);
-    }
+    const auto load = [&](int32_t at) {
+        if (at < cut.chunks) {
+            nx.load(xs + 8 * at);
+            ne.load(es + 8 * at, ep);
+        } else {
+            nx.fill(neg_inf());
+        }
+    };
+    ne.a = ne.b = ne.c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    load(c);
     for (; c - lane < cut.chunks; c += step) {
-        Chunk<TX> xc[1];
-        xc[0] = nx;
+        const Chunk<TX> xc = nx;
         const Noise8 e = ne;
-        if (c + step < cut.chunks) {
-            nx.load(xs + 8 * (c + step));
-            ne.load(es + 8 * (c + step), ep);
-        }
-        const bool mine = c < cut.chunks;
-        float z = neg_inf();
-        if (mine) {
-            z = __fmul_rn(xc[0].max(), scale);
-            soft_add<TX, false, 1>(q, xc, scale);
-        }
+        load(c + step);
         __syncwarp();
-        meet(z);
-        if (r.pm == neg_inf()) continue;  // masked tokens only
-        const Sieve sieve(scale, r.pm);
-        int32_t least = 0x7fffffff;
-        switch (ep) {
-            case 0: least = sieve_chunk<TX, 0>(sieve, xc[0], e); break;
-            case 1: least = sieve_chunk<TX, 1>(sieve, xc[0], e); break;
-            case 2: least = sieve_chunk<TX, 2>(sieve, xc[0], e); break;
-            default: least = sieve_chunk<TX, 3>(sieve, xc[0], e); break;
-        }
-        if (!mine) least = 0x7fffffff;
-        const int32_t i0 = cut.head + 8 * c;
-        if (low == 0.0f) {
-            // a first lower bound: of the warp's most promising chunk
-            const int32_t best = __reduce_min_sync(0xffffffffu, least);
-            const int from = __ffs(__ballot_sync(0xffffffffu, least == best)) - 1;
-            const int32_t i = __shfl_sync(0xffffffffu, i0, from) + (lane & 7);
-            float l = 0.0f;
-            if (lane < 8) {
-                float sc, off;
-                score(r, x[i], TX(0), noise[i], i, sc, off);
-                if (sc * noise[i] >= 0x1p-60f) l = fmaxf(sc - off, 0.0f);
-            }
-            __syncwarp();
-            low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(l)));
-        }
-        unsigned let = __ballot_sync(0xffffffffu, mine && least <= sieve.limit(__float_as_uint(low)));
-        if (let == 0) continue;
-        if (__popc(let) > 4) {
-            if (let >> lane & 1) {
-#pragma unroll 4
-                for (int k = 0; k < 8; ++k) look(x[i0 + k], noise[i0 + k], i0 + k);
-            }
-        } else {  // eight lanes for each chunk
-            int from = 0;
-            bool any = false;
+        meet(__fmul_rn(xc.max(), scale));
+        // (a NaN, which max passes over, goes into the sum)
+        float w[8], ev[8];
+        sum = __fadd_rn(sum, chunk_weights(xc, scale, ref == neg_inf() ? 0.0f : ref, w));
+        in_order(e, ep, ev);
+        // Tokens whose w - low e is not below 0 may reach `low` (less 2^-14, which is more
+        // than the weights' errors).  A NaN e is passed over, a negative one may come out.
+        const float under = -low * (1.0f - 0x1p-14f);
+        float d = fmaf(ev[0], under, w[0]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k == lane >> 3 && let) {
-                    from = __ffs(let) - 1;
-                    any = true;
-                }
-                let &= let - 1;
-            }
-            const int32_t i = __shfl_sync(0xffffffffu, i0, from) + (lane & 7);
-            if (any) look(x[i], noise[i], i);
+        for (int k = 1; k < 8; ++k) d = fmaxf(d, fmaf(ev[k], under, w[k]));
+        const bool pass = c < cut.chunks && ref != neg_inf() && d >= 0.0f;
+        if (!__any_sync(0xffffffffu, pass)) continue;
+        if (pass) {
+            const int32_t i0 = cut.head + 8 * c;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) race_token(b, w[k], ev[k], i0 + k);
         }
         __syncwarp();
         low = fmaxf(low, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.low))));
@@ -993,18 +1004,16 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     // the ends of the row
     if (rank == 0 && warp == 0) {
         const int32_t i = lane < 16 ? edge_element(0, cut.head, cut.head + 8 * cut.chunks, V) : -1;
-        float z = neg_inf();
-        if (i >= 0) {
-            Chunk<TX> xc[1];
-            xc[0].fill(neg_inf());
-            xc[0].set(0, x[i]);
-            z = __fmul_rn(xc[0].max(), scale);
-            soft_add<TX, false, 1>(q, xc, scale);
-        }
+        Chunk<TX> xc;
+        xc.fill(neg_inf());
+        if (i >= 0) xc.set(0, x[i]);
         __syncwarp();
-        meet(z);
-        if (i >= 0 && r.pm != neg_inf()) look(x[i], noise[i], i);
+        meet(__fmul_rn(xc.max(), scale));
+        float w[8];
+        sum = __fadd_rn(sum, chunk_weights(xc, scale, ref == neg_inf() ? 0.0f : ref, w));
+        if (i >= 0 && ref != neg_inf()) race_token(b, w[0], noise[i], i);
     }
+    Soft q{neg_inf(), ref == neg_inf() ? 0.0f : ref, sum, 0.0f};
     __syncwarp();
     soft_lanes<false, 32>(q);
     b = race_lanes(b);
@@ -1012,7 +1021,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         const uint4 v = make_uint4(__float_as_uint(q.mz), __float_as_uint(q.s), __float_as_uint(b.low),
                                    __float_as_uint(b.up));
         const uint4 w = make_uint4(__float_as_uint(b.second), static_cast<uint32_t>(b.token),
-                                   __float_as_uint(r.pm), 0u);
+                                   __float_as_uint(ref), 0u);
         if (C == 1) {
             if (lane == 0) {
                 sh.parts[0][warp][0] = v;
