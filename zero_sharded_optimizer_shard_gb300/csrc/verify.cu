@@ -985,6 +985,14 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         float w[8], ev[8];
         sum = __fadd_rn(sum, chunk_weights(xc, scale, ref == neg_inf() ? 0.0f : ref, w));
         in_order(e, ep, ev);
+        if (low == 0.0f && ref != neg_inf()) {  // about what the warp's best token has
+            float l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (ev[k] > 0x1p-100f) l = fmaxf(l, w[k] * reciprocal(ev[k]));
+            if (c >= cut.chunks) l = 0.0f;
+            low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(l)));
+        }
         // Tokens whose w - low e is not below 0 may reach `low` (less 2^-14, which is more
         // than the weights' errors).  A NaN e is passed over, a negative one may come out.
         const float under = -low * (1.0f - 0x1p-14f);
@@ -996,7 +1004,8 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         if (pass) {
             const int32_t i0 = cut.head + 8 * c;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) race_token(b, w[k], ev[k], i0 + k);
+            for (int k = 0; k < 8; ++k)
+                if (fmaf(ev[k], under, w[k]) >= 0.0f) race_token(b, w[k], ev[k], i0 + k);
         }
         __syncwarp();
         low = fmaxf(low, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.low))));
@@ -1037,24 +1046,21 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
             cluster_sync();
         }
     }
-    // every warp joins all of them: lane i has the parts i and i + 32
-    Soft h = soft_empty();
-    if (lane < kWarps * C) h = unpack(sh.parts[0][lane / C][lane % C]);
-    if (lane + 32 < kWarps * C) {
-        Soft g = unpack(sh.parts[0][(lane + 32) / C][(lane + 32) % C]);
-        float top = fmaxf(soft_top(h), soft_top(g));
-        if (top == neg_inf()) top = 0.0f;
-        soft_rebase<false>(h, top);
-        soft_rebase<false>(g, top);
-        h.s = __fadd_rn(h.s, g.s);
-        if (top == pos_inf()) h.s = __int_as_float(0x7fffffff);
-    }
-    __syncwarp();
-    soft_lanes<false, 32>(h);
-    int32_t token = -1;
-    float lp = __int_as_float(0x7fffffff);
-    if (h.s == 0.0f) lp = neg_inf();
-    if (h.s > 0.0f) {
+    // One warp joins all of them: lane i has the parts i and i + 32.
+    if (warp == 0) {
+        Soft h = soft_empty();
+        if (lane < kWarps * C) h = unpack(sh.parts[0][lane / C][lane % C]);
+        if (lane + 32 < kWarps * C) {
+            Soft g = unpack(sh.parts[0][(lane + 32) / C][(lane + 32) % C]);
+            float top = fmaxf(soft_top(h), soft_top(g));
+            if (top == neg_inf()) top = 0.0f;
+            soft_rebase<false>(h, top);
+            soft_rebase<false>(g, top);
+            h.s = __fadd_rn(h.s, g.s);
+            if (top == pos_inf()) h.s = __int_as_float(0x7fffffff);
+        }
+        __syncwarp();
+        soft_lanes<false, 32>(h);
         Race best{0.0f, 0.0f, 0.0f, -1};
         for (int j = lane; j < kWarps * C; j += 32) {
             const uint4 v = sh.parts[0][j / C][j % C], w = more[j / C][j % C];
@@ -1064,17 +1070,26 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         }
         __syncwarp();
         best = race_lanes(best);
-        if (best.low > 0.0f && best.second < best.low)
-            token = best.token;
-        else
-            token = draw_again<TX>(sh, a, h.mz, h.s, x, noise, rank);
-        if (token >= 0 && rank == 0) lp = __fsub_rn(fmaf(to_f32(x[token]), scale, -h.mz), logf(h.s));
-        if (token < 0) lp = neg_inf();
+        if (lane == 0) {
+            Position& o = sh.pos[0];
+            o.pm = h.mz;
+            o.ps = h.s;
+            // whether the answer is there: no sum, or a race that is certain
+            o.verdict = !(h.s > 0.0f) || (best.low > 0.0f && best.second < best.low) ? kEnd : kClose;
+            o.token = h.s > 0.0f ? best.token : -1;
+        }
     }
+    __syncthreads();
+    const Position o = sh.pos[0];
+    int32_t token = o.token;
+    if (o.verdict == kClose) token = draw_again<TX>(sh, a, o.pm, o.ps, x, noise, rank);
     if (rank == 0 && tid == 0) {
         a.accepted[s] = 0;
         a.tokens[s] = token;
-        if (a.logprobs) a.logprobs[s] = lp;
+        if (a.logprobs)
+            a.logprobs[s] = o.ps != o.ps ? __int_as_float(0x7fffffff)
+                            : token < 0  ? neg_inf()
+                                         : __fsub_rn(fmaf(to_f32(x[token]), scale, -o.pm), logf(o.ps));
     }
 }
 
