@@ -194,8 +194,12 @@ class Emulation:
         the persistent group.  With max_norm the gradients are clipped by their
         global norm, which is left in self.norm (float32 [1]): one clipped step
         for a single chunk, else the chunks' square sums, the coefficient and the
-        scaled steps."""
+        scaled steps.  That needs every rank's gradients: with state_ranks that leave
+        some out, max_norm is refused (ValueError)."""
         if max_norm is not None:
+            if self.psi_pad > 0 and len(self.state_ranks) != self.nd:
+                raise ValueError(f"max_norm needs the gradients of all {self.nd} ranks; the states of "
+                                 f"{self.state_ranks} alone are resident")
             return self._clipped_step(t, with_persistent, max_norm)
         for c, ((a, b), G) in enumerate(zip(self.chunks, self.grads)):
             zero3.zero3_step(self.plan, self.hp, t, self.ptrs(G), a, self.ptrs(self.master),
