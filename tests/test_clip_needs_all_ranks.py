@@ -41,3 +41,29 @@ def test_all_ranks_clip(calls, monkeypatch, ranks, bucketed):
     e.step(1, max_norm=1.0)
     assert "zero3_step" not in calls
     assert ("zero3_step_clipped" in calls) == (len(e.chunks) == 1)
+
+
+@pytest.mark.parametrize("own_clip", [False, True])
+def test_a_local_step_that_does_not_clip_is_refused_a_norm(lib, monkeypatch, own_clip):
+    """A caller's local step alone would take an unclipped step beside a reported norm."""
+    from zero_sharded_optimizer_shard_gb300 import distributed, zero3
+    ran = []
+    monkeypatch.setattr(distributed.ShardedRank, "exchange", lambda self: ran.append("exchange"))
+    monkeypatch.setattr(distributed.ShardedRank, "gather", lambda self: ran.append("gather"))
+    monkeypatch.setattr(distributed.dist, "all_reduce", lambda *a, **k: ran.append("all_reduce"))
+    w = W.mini_gpt(2)
+    plan = zero3.Plan(w.numels, w.submodule_of, 2, w.threshold, w.bucket)
+    clip = (lambda rk: ran.append("squares"), lambda rk, max_norm: ran.append("coefficient"))
+    rk = distributed.ShardedRank(plan, zero3.hparams(**w.hparams), 0, device="cpu",
+                                 local_step=lambda rk, t: ran.append(rk.clipping),
+                                 local_clip=clip if own_clip else None)
+    if own_clip:
+        rk.step(1, max_norm=1.0)
+        assert ran == ["exchange", "squares", "all_reduce", "coefficient", True, "gather"]
+    else:
+        with pytest.raises(ValueError, match="local_clip"):
+            rk.step(1, max_norm=1.0)
+        assert ran == []
+    ran.clear()
+    rk.step(2)
+    assert ran == ["exchange", False, "gather"]

@@ -90,6 +90,7 @@ class ShardedRank:
         self.norm, self.coef = z(1, f32), z(1, f32)
         self.clip_ws: Optional[torch.Tensor] = None
         self.clipping = False  # whether the local step multiplies by coef
+        self.can_clip = local_step is None or local_clip is not None
         self.local_step = local_step or ShardedRank.fused_step
         self.local_square_sum, self.local_coefficient = local_clip or (
             ShardedRank.sum_squares, ShardedRank.clip_coefficient)
@@ -120,7 +121,11 @@ class ShardedRank:
 
     def step(self, t: int, max_norm: Optional[float] = None) -> None:
         """One step; with max_norm, clipped by the gradients' global norm, which
-        self.norm receives on every rank."""
+        self.norm receives on every rank.  A caller's own local_step clips only if
+        it multiplies by self.coef where self.clipping says so; local_clip, which
+        comes with it, stands for that, and max_norm without it is refused."""
+        if max_norm is not None and not self.can_clip:
+            raise ValueError("max_norm with a local_step of the caller's needs local_clip too")
         self.exchange()
         self.clipping = max_norm is not None
         if self.clipping:
