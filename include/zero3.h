@@ -533,7 +533,8 @@ zero3_status zero3_merge_shards(const zero3_plan* plan, const char* const* shard
  * (zero3_grad_square_sum, zero3_clip_coefficient, the scaled steps), and over
  * plain lists of tensors (zero3_grad_norm, zero3_clip_grads).
  *  - Norms and coefficients are device memory: nothing waits for the GPU.
- *    Sums are kept in binary64 beyond a block's elements, in a fixed order;
+ *    Sums are kept in binary64 beyond 64 squares in a row, however long the list, in
+ *    a fixed order;
  *    squares that would overflow or vanish in binary32 do not.  N is rounded
  *    to binary32 when it is stored (infinite above its range), coef is taken
  *    from the unrounded N.

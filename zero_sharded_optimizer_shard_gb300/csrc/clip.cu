@@ -44,8 +44,7 @@ __device__ __forceinline__ uint32_t bits_of(const Chunk<float>& c) {
 }
 
 // Squares over the whole range of binary32: three sums, of numbers above 2^50
-// (times 2^-90), below 2^-40 (times 2^90) and between.  2^27 squares of a thread fit
-// each of them.
+// (times 2^-90), below 2^-40 (times 2^90) and between, of one chunk.
 struct WideSquares {
     float big = 0.0f, mid = 0.0f, small = 0.0f;
     __device__ __forceinline__ void add(float x) {
@@ -68,11 +67,15 @@ struct WideSquares {
 
 // Blocks of 256 threads with 64 bytes per thread on their way, 1024 chunks of 8 per
 // block and more only where that would make over 4864 blocks (32 per SM), so that
-// the blocks' sums stay few.  GPT-2-small's 148 binary32 tensors: 77 us, 498 MB at 82%
-// of the DRAM peak; 2000 ragged bf16 tensors, 1.05 GB: 155 us with the join (6.8 TB/s).
+// the blocks' sums stay few.  A thread's four binary32 sums are taken into a binary64 one
+// every kFold batches, so that their rounding errors (one-sided for equal numbers) do not
+// grow with the list: 64 squares of bf16 each, 32 of binary32.  GPT-2-small's 148 binary32
+// tensors: 77 us, 498 MB at 82% of the DRAM peak; 2000 ragged bf16 tensors, 1.05 GB: 153
+// us with the join (6.9 TB/s; 171 with one batch per turn of the loop, 188 with four).
 template <typename T, int MAXT>
 __global__ void __launch_bounds__(kThreads) list_norm_kernel(const __grid_constant__ ListArgs<MAXT> a) {
     constexpr int U = sizeof(T) == 2 ? 4 : 2;  // chunks in flight per thread: 64 bytes
+    constexpr int kFold = 16;
     __shared__ double sh[kThreads / 32];
     wait_prior_grids();
     allow_next_grid();
@@ -86,35 +89,51 @@ __global__ void __launch_bounds__(kThreads) list_norm_kernel(const __grid_consta
     const int64_t head = ph && n > 0 ? (P - ph < n ? P - ph : n) : 0;
     const int64_t chunks = (n - head) / 8;
     const int64_t tail = n - head - 8 * chunks;
+    // the block's own chunks (fewer than 2^26: the list has 2^41 elements at most)
     const int64_t c0 = static_cast<int64_t>(b) * a.per;
-    const int64_t c1 = c0 + a.per < chunks ? c0 + a.per : chunks;
-    const T* p = x + head;
+    const int64_t left = chunks - c0 < a.per ? chunks - c0 : a.per;
+    const int own = left > 0 ? static_cast<int>(left) : 0;
     const int tid = static_cast<int>(threadIdx.x);
     // the element at the tensor's ends that the thread has
     const T* edge = nullptr;
     if (b == 0 && tid < head) edge = x + tid;
-    if (last && tid >= 8 && tid - 8 < tail) edge = p + 8 * chunks + (tid - 8);
+    if (last && tid >= 8 && tid - 8 < tail) edge = x + head + 8 * chunks + (tid - 8);
+    const T* p = x + head + 8 * c0;
 
     uint64_t acc[4] = {0, 0, 0, 0};
     uint32_t any = 0;
-    int64_t i = c0 + tid;
-    for (; i + (U - 1) * kThreads < c1; i += U * kThreads) {
-        Chunk<T> c[U];
+    double d = 0.0;
+    const auto sum = [&]() {
+        float s, s1;
+        upk2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), s, s1);
+        return __fadd_rn(s, s1);
+    };
+    int i = tid;
+    while (i + (U - 1) * kThreads < own) {
+        const int stop = i + kFold * U * kThreads < own ? i + kFold * U * kThreads : own;
+#pragma unroll 2
+        for (; i + (U - 1) * kThreads < stop; i += U * kThreads) {
+            Chunk<T> c[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) c[u].load(p + 8 * (i + u * kThreads));
+            for (int u = 0; u < U; ++u) c[u].load(p + 8 * static_cast<int64_t>(i + u * kThreads));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            any |= bits_of(c[u]);
+            for (int u = 0; u < U; ++u) {
+                any |= bits_of(c[u]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint64_t v = c[u].pair(k);
-                acc[k] = fma2(v, v, acc[k]);
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t v = c[u].pair(k);
+                    acc[k] = fma2(v, v, acc[k]);
+                }
             }
         }
+        if (stop < own) {
+            d += static_cast<double>(sum());
+            acc[0] = acc[1] = acc[2] = acc[3] = 0;
+        }
     }
-    for (; i < c1; i += kThreads) {
+    for (; i < own; i += kThreads) {
         Chunk<T> c;
-        c.load(p + 8 * i);
+        c.load(p + 8 * static_cast<int64_t>(i));
         any |= bits_of(c);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -122,23 +141,27 @@ __global__ void __launch_bounds__(kThreads) list_norm_kernel(const __grid_consta
             acc[k] = fma2(v, v, acc[k]);
         }
     }
-    float s, s1;
-    upk2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), s, s1);
-    s = __fadd_rn(s, s1);
+    float s = sum();
     if (edge) {
         const float f = to_f32(*edge);
         s = fmaf(f, f, s);
         any |= __float_as_uint(f) & 0x7fffffffu;
     }
+    d += static_cast<double>(s);
     // A sum near the ends of binary32's range (numbers beyond 2^60, or so small
     // that squares have lost bits): the thread's share is read again.
-    double d = static_cast<double>(s);
-    if (any && !(s >= 0x1p-90f && s <= 0x1p120f)) {
-        WideSquares w;
-        for (int64_t j = c0 + tid; j < c1; j += kThreads)
-            for (int e = 0; e < 8; ++e) w.add(to_f32(p[8 * j + e]));
-        if (edge) w.add(to_f32(*edge));
-        d = w.value();
+    if (any && !(d >= 0x1p-90 && d <= 0x1p120)) {
+        d = 0.0;
+        for (int j = tid; j < own; j += kThreads) {
+            WideSquares w;
+            for (int e = 0; e < 8; ++e) w.add(to_f32(p[8 * static_cast<int64_t>(j) + e]));
+            d += w.value();
+        }
+        if (edge) {
+            WideSquares w;
+            w.add(to_f32(*edge));
+            d += w.value();
+        }
     }
     if (__any_sync(0xffffffffu, d != static_cast<double>(s))) {  // a NaN too
 #pragma unroll
