@@ -35,6 +35,7 @@ LIBS = {
 }
 HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "device_common.cuh"),
            os.path.join(CSRC, "operators.h"), os.path.join(CSRC, "vocab_common.cuh"),
+           os.path.join(CSRC, "race_cut.h"),
            os.path.join(INCLUDE, "zero3.h")]
 
 

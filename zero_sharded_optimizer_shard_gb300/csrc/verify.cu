@@ -28,6 +28,7 @@
 
 #include <cstdint>
 
+#include "race_cut.h"
 #include "vocab_common.cuh"
 
 namespace z3 {
@@ -55,15 +56,24 @@ struct Position {
     int32_t verdict;
 };
 
-// The 4-byte word of global memory that holds *p, on its way to shared memory,
-// and *p from there.
-template <typename T>
-__device__ __forceinline__ void send_word(uint32_t* to, const T* p) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(3);
+// The 4-byte word of global memory that holds element d of a row of V, on its way to
+// shared memory, and the element from there.
+__device__ __forceinline__ void copy_word(uint32_t* to, uintptr_t at) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(to))),
                  "l"(at)
                  : "memory");
+}
+__device__ __forceinline__ void send_word(uint32_t* to, const float* row, int32_t d, int32_t) {
+    copy_word(to, reinterpret_cast<uintptr_t>(row + d));
+}
+__device__ __forceinline__ void send_word(uint32_t* to, const uint16_t* row, int32_t d, int32_t V) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + d);
+    const bool upper = (at & 2) != 0;
+    if (word_in_row(upper, d, V))
+        copy_word(to, at & ~static_cast<uintptr_t>(3));
+    else  // a row's first or last element: its other half may be no one's
+        *to = static_cast<uint32_t>(row[d]) << (upper ? 16 : 0);
 }
 __device__ __forceinline__ float from_word(uint32_t w, const float*) { return __uint_as_float(w); }
 __device__ __forceinline__ float from_word(uint32_t w, const uint16_t* p) {
@@ -315,7 +325,7 @@ struct Sieve {
 };
 
 // 8 elements of noise from an address whose place on 16 bytes is `ph`, by the aligned
-// blocks that hold them (each of which holds one of them at least).
+// blocks that hold them (which lie in the row: race_cut).
 struct Noise8 {
     float4 a, b, c;
     __device__ __forceinline__ void load(const float* p, int ph) {
@@ -449,11 +459,12 @@ template <typename TX, typename TY>
 __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, TY>& r, int32_t V,
                                           int rank, int C, volatile uint32_t* shared_low) {
     Race b{0.0f, 0.0f, 0.0f, -1};
-    const RowCut<TX> cut(r.x, V);
+    const RowCut<TX> row(r.x, V);
+    const int ep = phase_of(r.e + row.head);
+    const RaceCut cut = race_cut(row.head, row.chunks, ep, V);
     const int step = C * kNT, lane = threadIdx.x & 31;
     const TX* xs = r.x + cut.head;
     const float* es = r.e + cut.head;
-    const int ep = phase_of(es);
     const Sieve sieve(r.xs, r.pm);
     const auto look = [&](TX x, float e, int32_t i) {
         float s, off;
@@ -510,8 +521,8 @@ __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, T
         if (lane == 0 && found > low) atomicMax(const_cast<uint32_t*>(shared_low), found);
     }
     // the ends of the row
-    if (rank == 0 && threadIdx.x < 16) {
-        const int32_t i = edge_element(0, cut.head, cut.head + 8 * cut.chunks, V);
+    if (rank == 0 && threadIdx.x < 32) {
+        const int32_t i = end_token(lane, cut.head, cut.head + 8 * cut.chunks, V);
         if (i >= 0) look(r.x[i], r.e[i], i);
     }
     __syncwarp();
@@ -768,9 +779,9 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
         if (warp == 0) {
             if (lane < G) {
                 const int j = j0 + lane, d = sh.ids[j];
-                send_word(&sh.words[lane][0], x + j * a.stride + d);
-                if (DRAFT) send_word(&sh.words[lane][1], y + j * a.y_stride + d);
-                send_word(&sh.words[lane][2], a.uniform + s * K + j);
+                send_word(&sh.words[lane][0], x + j * a.stride, d, V);
+                if (DRAFT) send_word(&sh.words[lane][1], y + j * a.y_stride, d, V);
+                send_word(&sh.words[lane][2], a.uniform + s * K, j, K);
             }
         }
         {
@@ -942,11 +953,12 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     wait_prior_grids();
     allow_next_grid();
     if (tid < 2) sh.low[tid] = 0;
-    const RowCut<TX> cut(x, V);
+    const RowCut<TX> row(x, V);
+    const int ep = phase_of(noise + row.head);
+    const RaceCut cut = race_cut(row.head, row.chunks, ep, V);
     const int step = C * kNT;
     const TX* xs = x + cut.head;
     const float* es = noise + cut.head;
-    const int ep = phase_of(es);
     float sum = 0.0f;
     Race b{0.0f, 0.0f, 0.0f, -1};
     float ref = neg_inf();
@@ -1020,7 +1032,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     }
     // the ends of the row
     if (rank == 0 && warp == 0) {
-        const int32_t i = lane < 16 ? edge_element(0, cut.head, cut.head + 8 * cut.chunks, V) : -1;
+        const int32_t i = end_token(lane, cut.head, cut.head + 8 * cut.chunks, V);
         Chunk<TX> xc;
         xc.fill(neg_inf());
         if (i >= 0) xc.set(0, x[i]);
