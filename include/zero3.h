@@ -791,7 +791,8 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
  *    residual the draw is from p_A.  A NaN or negative u refuses.
  *  - Log probabilities are exact to about 2^-22 of themselves plus 2^-22 (a nearly
  *    certain token's keeps fewer digits).
- *  - Masked tokens are -inf logits.  A target row without any token accepts
+ *  - Masked tokens are -inf logits.  A finite mask is a logit like any other: a row
+ *    that it covers is uniform, at every temperature.  A target row without any token accepts
  *    nothing and draws -1 (log probability -inf), a draft row without any has
  *    q = 0.  A NaN or +inf logit in a target row, or in a draft row that refuses,
  *    makes the drawn token -1 with a NaN log probability; in a draft row it refuses

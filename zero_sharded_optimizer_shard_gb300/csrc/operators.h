@@ -121,6 +121,16 @@ inline int64_t list_blocks(int64_t numel, int64_t per) {
     return b < 1 ? 1 : b;
 }
 
+// An inverse temperature a as weights are formed with it: of x relative to the row's
+// largest logit m, exp(a (x - m)) = 2^((x h - m h) (c + cl)), z = a / h; h is 1, or in a
+// FarScale a power of two.
+struct LogitScale {
+    float c, cl, z;
+};
+struct FarScale : LogitScale {
+    float h;
+};
+
 struct VerifyArgs {
     const void* x;
     const void* y;          // draft logits, or null: the draft is certain of its tokens
@@ -132,7 +142,7 @@ struct VerifyArgs {
     float* logprobs;
     int64_t n, stride, y_stride, noise_stride;
     int32_t vocab, k;
-    float scale, y_scale;
+    float scale, y_scale;    // inverse temperatures
     int32_t dtype, y_dtype, id64;
     int32_t cluster, ahead;  // blocks per sequence, positions per round (set by the launch)
     float sum_error;         // relative, of a row's sum (set by the launch)

@@ -20,6 +20,10 @@
 // race in a launch of its own: equal or slower.  Without a draft (k = 0) a kernel of its
 // own takes statistics and race in one pass.
 //
+// Weights are 2^((x - m) c), m the row's largest logit and c = a log2(e): of the
+// difference of two logits, not of the difference of two products, whose rounding is
+// many units where a x is large (finite masks, draws that are nearly greedy).
+//
 // Decisions.  Weights are binary32, with errors that are bounded as they are
 // formed.  A test or a race closer than its bound is taken again by the same
 // blocks with weights of 31 bits, row sums in 64-bit integers and scores in
@@ -27,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "race_cut.h"
 #include "vocab_common.cuh"
@@ -45,11 +50,17 @@ __device__ __forceinline__ void send16(uint4* p, uint32_t rank, const uint4& v) 
 
 constexpr int kNT = 256, kWarps = kNT / 32;
 
+// A launch's arguments; S: LogitScale, or FarScale.
+template <typename S>
+struct Args : VerifyArgs {
+    S x_unit, y_unit;
+};
+
 // What decides about a drafted token.
 enum Verdict : int { kAccept = 0, kRefuse = 1, kClose = 2, kBroken = 3, kEnd = 4 };
 
 struct Position {
-    float pm, ps, qm, qs;  // the two rows' mz and s (Soft)
+    float pm, ps, qm, qs;  // the two rows' m (0 without a token) and s (RowSum)
     float xd, yd;    // the drafted token's logits
     float u;
     int32_t token;
@@ -86,17 +97,96 @@ __device__ __forceinline__ void prefetch_line(const void* p) {
 
 constexpr int kMaxPositions = kWarps;  // per round: a warp each
 
-__device__ __forceinline__ uint4 pack(const Soft& s) {
-    return make_uint4(__float_as_uint(s.mz), __float_as_uint(s.s), 0u, 0u);
+// Differences of logits.  h is 1 (LogitScale) but for inverse temperatures next to the ends
+// of binary32 (FarScale), whose instances are compiled apart: products with h cost 1 to 4%
+// of a call.
+__device__ __forceinline__ float in_unit(const LogitScale&, float x) { return x; }
+__device__ __forceinline__ float in_unit(const FarScale& u, float x) { return __fmul_rn(x, u.h); }
+// x h - m
+__device__ __forceinline__ float less(const LogitScale&, float x, float m) { return __fsub_rn(x, m); }
+__device__ __forceinline__ float less(const FarScale& u, float x, float m) { return fmaf(x, u.h, -m); }
+__device__ __forceinline__ uint64_t less2(const LogitScale&, uint64_t x, float m) {
+    return add2(x, pk2(-m, -m));
 }
-__device__ __forceinline__ Soft unpack(const uint4& v) {
-    return Soft{neg_inf(), __uint_as_float(v.x), __uint_as_float(v.y), 0.0f};
+__device__ __forceinline__ uint64_t less2(const FarScale& u, uint64_t x, float m) {
+    return fma2(x, pk2(u.h, u.h), pk2(-m, -m));
+}
+// Its product with the inverse temperature.
+template <typename S>
+__device__ __forceinline__ float scaled(const S& u, float x, float m) {
+    return __fmul_rn(less(u, x, m), u.z);
+}
+
+// Sum of weights 2^((x h - m) c) of the logits that a thread has seen, m the largest
+// x h of them (the lowest finite number before any: no difference of two infinities is
+// taken).  A NaN is passed over by m and turns s into NaN, as an infinite m does.
+struct RowSum {
+    float m, s;
+};
+__device__ __forceinline__ uint4 pack(const RowSum& q) {
+    return make_uint4(__float_as_uint(q.m), __float_as_uint(q.s), 0u, 0u);
+}
+__device__ __forceinline__ RowSum unpack(const uint4& v) {
+    return RowSum{__uint_as_float(v.x), __uint_as_float(v.y)};
+}
+__device__ __forceinline__ float lowest() { return __int_as_float(0xff7fffff); }
+
+template <typename T, int U, typename S>
+__device__ __forceinline__ void row_add(RowSum& q, const Chunk<T> (&c)[U], const S& u) {
+    float bm = c[0].max();
+#pragma unroll
+    for (int i = 1; i < U; ++i) bm = fmaxf(bm, c[i].max());
+    bm = in_unit(u, bm);
+    if (bm > q.m) {
+        if (q.s != 0.0f) q.s = __fmul_rn(q.s, exp2_approx(__fmul_rn(__fsub_rn(q.m, bm), u.c)));
+        q.m = bm;
+    }
+    const uint64_t cc = pk2(u.c, u.c);
+    uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float t0, t1;
+            upk2(mul2(less2(u, c[i].pair(k), q.m), cc), t0, t1);
+            const uint64_t e = pk2(exp2_approx(t0), exp2_approx(t1));
+            if (k & 1)
+                s1 = add2(s1, e);
+            else
+                s0 = add2(s0, e);
+        }
+    }
+    float x, y;
+    upk2(add2(s0, s1), x, y);
+    q.s = __fadd_rn(q.s, __fadd_rn(x, y));
+}
+
+// Joins the sums of `WIDTH` lanes (a power of two); every lane gets the result, in a
+// fixed order.
+template <int WIDTH>
+__device__ __forceinline__ void row_lanes(RowSum& q, float c) {
+    float top = q.m;
+#pragma unroll
+    for (int o = WIDTH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    q.s = __fmul_rn(q.s, exp2_approx(__fmul_rn(__fsub_rn(q.m, top), c)));
+    q.m = top;
+#pragma unroll
+    for (int o = WIDTH / 2; o > 0; o >>= 1) q.s = __fadd_rn(q.s, __shfl_xor_sync(0xffffffffu, q.s, o));
+}
+
+// A whole row's: a largest logit whose product with the inverse temperature overflows
+// counts as infinite, which leaves a NaN above and no token below.
+__device__ __forceinline__ RowSum whole_row(RowSum q, float z) {
+    const float top = __fmul_rn(q.m, z);
+    if (top == pos_inf()) q.s = __int_as_float(0x7fffffff);
+    if (top == neg_inf() && q.s == q.s) q.s = 0.0f;
+    return q;
 }
 
 // Thread `tid`'s share, of `nt` threads in each of C blocks, of a row.
-template <typename T>
-__device__ __forceinline__ void stream_row(Soft& q, const T* row, int32_t V, int rank, int C,
-                                           float scale, int tid, int nt) {
+template <typename T, typename S>
+__device__ __forceinline__ void stream_row(RowSum& q, const T* row, int32_t V, int rank, int C,
+                                           const S& u, int tid, int nt) {
     constexpr int U = sizeof(T) == 2 ? 4 : 2;
     const RowCut<T> cut(row, V);
     const int32_t per = (cut.chunks + C - 1) / C;
@@ -109,21 +199,21 @@ __device__ __forceinline__ void stream_row(Soft& q, const T* row, int32_t V, int
     if (i + (U - 1) * nt < c1) {  // the next batch is on its way while one is added
         Chunk<T> c[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) c[u].load(p + 8 * static_cast<int64_t>(i + u * nt));
+        for (int k = 0; k < U; ++k) c[k].load(p + 8 * static_cast<int64_t>(i + k * nt));
         for (i += U * nt; i + (U - 1) * nt < c1; i += U * nt) {
             Chunk<T> d[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) d[u].load(p + 8 * static_cast<int64_t>(i + u * nt));
-            soft_add<T, false, U>(q, c, scale);
+            for (int k = 0; k < U; ++k) d[k].load(p + 8 * static_cast<int64_t>(i + k * nt));
+            row_add<T, U>(q, c, u);
 #pragma unroll
-            for (int u = 0; u < U; ++u) c[u] = d[u];
+            for (int k = 0; k < U; ++k) c[k] = d[k];
         }
-        soft_add<T, false, U>(q, c, scale);
+        row_add<T, U>(q, c, u);
     }
     for (; i < c1; i += nt) {
         Chunk<T> c[1];
         c[0].load(p + 8 * static_cast<int64_t>(i));
-        soft_add<T, false, 1>(q, c, scale);
+        row_add<T, 1>(q, c, u);
     }
     if (head || tail) {
         const T* f = head ? row : p + 8 * static_cast<int64_t>(cut.chunks);
@@ -133,7 +223,7 @@ __device__ __forceinline__ void stream_row(Soft& q, const T* row, int32_t V, int
 #pragma unroll
         for (int e = 0; e < 7; ++e)
             if (e < n) c[0].set(e, f[e]);
-        soft_add<T, false, 1>(q, c, scale);
+        row_add<T, 1>(q, c, u);
     }
 }
 
@@ -145,7 +235,7 @@ __device__ __forceinline__ float chunk_element(const Chunk<T>& c, int k) {
     return k & 1 ? hi : lo;
 }
 // ------------------------------------------------- 31-bit weights, exact sums
-// 2^(n + f), |f| <= 1/2, as y / 2^31 * 2^n with 0.70 < y / 2^31 < 1.42, from the Taylor
+// 2^(n + f), |f| <= 0.5002, as y / 2^31 * 2^n with 0.70 < y / 2^31 < 1.42, from the Taylor
 // series of 2^f = e^(f ln 2), terms (f ln 2)^k / k!, k <= 9 (the next is below 8e-12),
 // in fixed point.
 struct Weight {
@@ -153,20 +243,17 @@ struct Weight {
     int32_t n;  // below -1000: no weight
 };
 
-template <typename T>
-__device__ __forceinline__ Weight weight31(T x, float scale, float mz) {
-    const float f = to_f32(x);
-    // z - mz as a sum of two numbers: the product and the difference with
-    // their rounding errors
-    const float z = __fmul_rn(f, scale);
-    const float zl = fmaf(f, scale, -z);
-    const float d = __fsub_rn(z, mz);
+template <typename T, typename S>
+__device__ __forceinline__ Weight weight31(T x, const S& u, float m) {
+    const float z = in_unit(u, to_f32(x));
+    // z - m as a sum of two numbers: the difference with its rounding error
+    const float d = __fsub_rn(z, m);
     const float bb = __fsub_rn(d, z);
-    const float dl = __fadd_rn(__fadd_rn(__fsub_rn(z, __fsub_rn(d, bb)), -__fadd_rn(mz, bb)), zl);
-    // times log2(e) = hi + lo
-    const float hi = 1.44269502162933349609375f, lo = 1.92596299112661746e-8f;
-    const float t = __fmul_rn(d, hi);
-    const float tl = fmaf(d, hi, -t) + fmaf(d, lo, __fmul_rn(dl, hi));
+    const float dl = __fadd_rn(__fsub_rn(z, __fsub_rn(d, bb)), -__fadd_rn(m, bb));
+    // times c + cl (the second part is 2^-23 of the first at most, and -1000 < t here:
+    // below 2^-12)
+    const float t = __fmul_rn(d, u.c);
+    const float tl = fmaf(d, u.c, -t) + fmaf(d, u.cl, __fmul_rn(dl, u.c));
     Weight w;
     if (!(t > -1000.0f)) {  // masked tokens too
         w.y = 0;
@@ -235,12 +322,13 @@ __device__ __forceinline__ Race race_lanes(const Race& r) {
     return o;
 }
 
-// A weight 2^t, t = (x scale - mz) log2(e), and its relative error: the unit's two
-// ulp, and three roundings of t.  Without weight below 2^-126.
-template <typename T>
-__device__ __forceinline__ float weight(T x, float scale, float mz, float& rel) {
-    const float t = __fmul_rn(fmaf(to_f32(x), scale, -mz), kLog2e);
-    rel = fmaf(fabsf(fmaxf(t, -128.0f)), 0x1p-23f, 0x1p-21f);
+// A weight 2^t, t = (x h - m) c, and its relative error: the unit's two ulp, and three
+// roundings of t (of the difference, of c and of the product: 3 ln2 2^-24 = 1.04 * 2^-23 of
+// |t|).  Without weight below 2^-126.
+template <typename T, typename S>
+__device__ __forceinline__ float weight(T x, const S& u, float m, float& rel) {
+    const float t = __fmul_rn(less(u, to_f32(x), m), u.c);
+    rel = fmaf(fabsf(fmaxf(t, -128.0f)), 0x1.2p-23f, 0x1p-21f);
     return exp2_approx(t);
 }
 
@@ -261,22 +349,28 @@ struct Rows {
     const TX* x;
     const TY* y;       // the draft's row, or null
     const float* e;
-    float xs, ys, pm, qm;  // scales and mz
+    float pm, qm;      // m
     float ratio;       // sum of the target's weights over the draft's
     float ratio_error; // relative
     int32_t without;   // this token is not drawn (a refused token without probabilities)
 };
 
+// How the exact race, which is not inlined, takes them: by value, without a place in memory
+// (512 sequences of ten tokens without probabilities: 96 -> 93 us), but by reference beside a
+// draft, where the kernel around the call then comes out worse (512 of five: 126 -> 139).
+template <typename TX, typename TY, bool DRAFT>
+using RowsOf = std::conditional_t<DRAFT, const Rows<TX, TY>&, Rows<TX, TY>>;
+
 // Score of token i: (wp - ratio wq) / e, and how far it may be off.
-template <typename TX, typename TY>
-__device__ __forceinline__ void score(const Rows<TX, TY>& r, TX x, TY y, float e, int32_t i, float& s,
-                                      float& off) {
+template <typename TX, typename TY, typename S>
+__device__ __forceinline__ void score(const Args<S>& a, const Rows<TX, TY>& r, TX x, TY y, float e,
+                                      int32_t i, float& s, float& off) {
     float rel;
-    const float wp = weight(x, r.xs, r.pm, rel);
+    const float wp = weight(x, a.x_unit, r.pm, rel);
     float v = wp;
     off = wp * rel;
     if (r.y) {
-        const float wq = weight(y, r.ys, r.qm, rel) * r.ratio;
+        const float wq = weight(y, a.y_unit, r.qm, rel) * r.ratio;
         v = wp - wq;
         off = fmaf(wq, rel + r.ratio_error, off);
     }
@@ -303,13 +397,15 @@ struct Sieve {
     float a, c;
     int32_t margin;
     static constexpr float kFloor = 8388608.0f + 27.0f * 16384.0f;  // t = -100, masked tokens too
-    __device__ __forceinline__ Sieve(float scale, float mz) {
-        a = scale * kLog2e * 16384.0f;
-        c = 8388608.0f + 127.0f * 16384.0f - mz * kLog2e * 16384.0f;
-        // T is off by half a unit, and by the roundings of a and c; where they
-        // overflow nothing is passed over
-        const float m = 0x1p-13f + (fabsf(mz) + 150.0f) * 0x1p-21f;
-        margin = m < 64.0f && a < 0x1p100f ? static_cast<int32_t>(m * 8388608.0f) : 0x7fffffff;
+    template <typename S>
+    __device__ __forceinline__ Sieve(const S& u, float m) {
+        const float unit = u.c * 16384.0f;
+        a = in_unit(u, unit);
+        c = fmaf(-m, unit, 8388608.0f + 127.0f * 16384.0f);
+        // T is off by half a unit, by the rounding of u.c in at most 100 and by that of c;
+        // where they overflow nothing is passed over
+        const float off = 0x1p-13f + (fabsf(m * u.c) + 150.0f) * 0x1p-21f;
+        margin = off < 64.0f && a < 0x1p100f ? static_cast<int32_t>(off * 8388608.0f) : 0x7fffffff;
     }
     // bits(e) - 512 T - bits(1): the bound with its sign turned.  Negative e are
     // never drawn and may come out anyhow.
@@ -354,7 +450,7 @@ struct Shared {
     Position pos[kMaxPositions];
     uint32_t words[kMaxPositions][4];  // words that hold a position's two logits, and its uniform number
     int32_t ids[ZERO3_MAX_DRAFT];
-    float z[ZERO3_MAX_DRAFT], sum[ZERO3_MAX_DRAFT];  // an accepted token's z - mz, its row's s
+    float z[ZERO3_MAX_DRAFT], sum[ZERO3_MAX_DRAFT];  // an accepted token's (x - m) a, its row's s
     uint32_t low[2];   // bits of the race's best lower bound, first and second pass
 };
 
@@ -374,28 +470,33 @@ __device__ __forceinline__ void exchange(Shared& sh, int turn, int C, uint32_t r
 
 // Joins what the warps `row`, `row` + R, ... of all blocks have sent, each half of
 // the calling warp for a row of its own; every lane of the half gets the result.
-__device__ __forceinline__ Soft join_rows(const Shared& sh, int turn, int row, int R, int C) {
-    Soft o = soft_empty();
+__device__ __forceinline__ RowSum join_rows(const Shared& sh, int turn, int row, int R, int C, float c) {
     const int n = (kWarps - row + R - 1) / R * C;
-    int i = threadIdx.x & 15;
-    if (i < n) o = unpack(sh.parts[turn & 1][row + i / C * R][i % C]);
-    for (i += 16; i < n; i += 16) {
-        Soft s = unpack(sh.parts[turn & 1][row + i / C * R][i % C]);
-        float top = fmaxf(soft_top(o), soft_top(s));
-        if (top == neg_inf()) top = 0.0f;
-        soft_rebase<false>(o, top);
-        soft_rebase<false>(s, top);
-        o.s = __fadd_rn(o.s, s.s);
-        if (top == pos_inf()) o.s = __int_as_float(0x7fffffff);
+    const int lg = 31 - __clz(C);
+    const auto part = [&](int i) { return unpack(sh.parts[turn & 1][row + (i >> lg) * R][i & (C - 1)]); };
+    const int i0 = threadIdx.x & 15;
+    RowSum p{lowest(), 0.0f};
+    if (i0 < n) p = part(i0);
+    float top = p.m;
+    for (int i = i0 + 16; i < n; i += 16) top = fmaxf(top, part(i).m);
+    __syncwarp();
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    RowSum q{top, __fmul_rn(p.s, exp2_approx(__fmul_rn(__fsub_rn(p.m, top), c)))};
+    for (int i = i0 + 16; i < n; i += 16) {
+        p = part(i);
+        q.s = __fadd_rn(q.s, __fmul_rn(p.s, exp2_approx(__fmul_rn(__fsub_rn(p.m, top), c))));
     }
-    soft_lanes<false, 16>(o);
-    return o;
+    __syncwarp();
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) q.s = __fadd_rn(q.s, __shfl_xor_sync(0xffffffffu, q.s, o));
+    return q;
 }
 
 // This thread's share of the integer sum of a row's weights.
-template <typename T>
-__device__ __forceinline__ uint64_t exact_share(const T* row, int32_t V, float scale, float mz, int rank,
-                                                int C, int bits) {
+template <typename T, typename S>
+__device__ __forceinline__ uint64_t exact_share(const T* row, int32_t V, const S& scale, float m,
+                                                int rank, int C, int bits) {
     uint64_t s = 0;
     const int step = C * kNT;
     // four at a time, the next four on their way (few registers: what this holds, the
@@ -415,7 +516,7 @@ __device__ __forceinline__ uint64_t exact_share(const T* row, int32_t V, float s
         load(i);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const Weight w = weight31(now[u], scale, mz);
+            const Weight w = weight31(now[u], scale, m);
             const int shift = bits - 31 + w.n;  // y * 2^shift
             if (shift >= 0)
                 s += static_cast<uint64_t>(w.y) << (shift < 32 ? shift : 32);
@@ -426,12 +527,13 @@ __device__ __forceinline__ uint64_t exact_share(const T* row, int32_t V, float s
     return s;
 }
 
-template <typename TX, typename TY>
-__device__ __noinline__ Sums exact_sums(Shared& sh, int turn, const TX* xr, const TY* yr, int32_t V,
-                                        float xs, float ys, float mzp, float mzq, int rank, int C) {
-    const int bits = sum_bits(V);
-    uint64_t s = exact_share(xr, V, xs, mzp, rank, C, bits);
-    uint64_t t = yr ? exact_share(yr, V, ys, mzq, rank, C, bits) : 0;
+template <typename TX, typename TY, typename S>
+__device__ __noinline__ Sums exact_sums(Shared& sh, int turn, const Args<S>& a, const TX* xr, const TY* yr,
+                                        float pm, float qm, int rank) {
+    const int32_t V = a.vocab;
+    const int C = a.cluster, bits = sum_bits(V);
+    uint64_t s = exact_share(xr, V, a.x_unit, pm, rank, C, bits);
+    uint64_t t = yr ? exact_share(yr, V, a.y_unit, qm, rank, C, bits) : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -455,9 +557,11 @@ __device__ __noinline__ Sums exact_sums(Shared& sh, int turn, const TX* xr, cons
 // only for them the draft's row is read.  (The best lower bound of the block, by
 // which it sieves, depends on the warps' timing; the winner does not: what is
 // passed over lies below a lower bound of another token's score.)
-template <typename TX, typename TY>
-__device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, TY>& r, int32_t V,
-                                          int rank, int C, volatile uint32_t* shared_low) {
+template <typename TX, typename TY, typename S>
+__device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Args<S>& a, const Rows<TX, TY>& r,
+                                          int rank, volatile uint32_t* shared_low) {
+    const int32_t V = a.vocab;
+    const int C = a.cluster;
     Race b{0.0f, 0.0f, 0.0f, -1};
     const RowCut<TX> row(r.x, V);
     const int ep = phase_of(r.e + row.head);
@@ -465,10 +569,10 @@ __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, T
     const int step = C * kNT, lane = threadIdx.x & 31;
     const TX* xs = r.x + cut.head;
     const float* es = r.e + cut.head;
-    const Sieve sieve(r.xs, r.pm);
+    const Sieve sieve(a.x_unit, r.pm);
     const auto look = [&](TX x, float e, int32_t i) {
         float s, off;
-        score(r, x, r.y ? r.y[i] : TY(0), e, i, s, off);
+        score(a, r, x, r.y ? r.y[i] : TY(0), e, i, s, off);
         race_add(b, s - off, s + off, i);
     };
     // a warp takes 32 chunks at a time, and loads the next ones meanwhile
@@ -541,15 +645,17 @@ __device__ __forceinline__ Race race_pass(Shared& sh, int turn, const Rows<TX, T
 
 // The race among the tokens whose upper bound reaches `low`, with 31-bit weights
 // and scores in binary64; ties to the lowest token, -1 if no score is positive.
-template <typename TX, typename TY, bool DRAFT>
-__device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Rows<TX, TY>& r, const Sums& sums,
-                                           float low, int32_t V, int rank, int C) {
+template <typename TX, typename TY, bool DRAFT, typename S>
+__device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Args<S>& a, RowsOf<TX, TY, DRAFT> r,
+                                           const Sums sums, float low, int rank) {
+    const int32_t V = a.vocab;
+    const int C = a.cluster;
     double best = 0.0;
     int32_t token = 0x7fffffff;
     // several at a time through the sieve of the bound that the race has found; one
     // without a draft, where a close race is one in 10^5 and registers count
     constexpr int U = DRAFT ? 4 : 1;
-    const Sieve sieve(r.xs, r.pm);
+    const Sieve sieve(a.x_unit, r.pm);
     const int32_t limit = sieve.limit(__float_as_uint(low));
     const int step = C * kNT;
     for (int32_t i0 = rank * kNT + static_cast<int>(threadIdx.x); i0 < V;
@@ -565,10 +671,10 @@ __device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Rows<TX, 
             const TY y = r.y ? r.y[i] : TY(0);
             const float e = r.e[i];
             float s, off;
-            score(r, x, y, e, i, s, off);
+            score(a, r, x, y, e, i, s, off);
             if (!(s + off >= low) || !(e >= 0.0f) || i == r.without) continue;
-            double v = weight64(weight31(x, r.xs, r.pm));
-            if (r.y) v = v / sums.p - weight64(weight31(y, r.ys, r.qm)) / sums.q;
+            double v = weight64(weight31(x, a.x_unit, r.pm));
+            if (r.y) v = v / sums.p - weight64(weight31(y, a.y_unit, r.qm)) / sums.q;
             v = v / static_cast<double>(e);
             if (v > best) {  // tokens come in ascending order
                 best = v;
@@ -607,37 +713,40 @@ __device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Rows<TX, 
 
 // ---------------------------------------------------------------- the kernel
 // Exact decision about a close position.
-template <typename TX, typename TY, bool DRAFT>
-__device__ __noinline__ int decide(Shared& sh, int turn, const VerifyArgs& a, const Position& o, const TX* xr,
+template <typename TX, typename TY, bool DRAFT, typename S>
+__device__ __noinline__ int decide(Shared& sh, int turn, const Args<S>& a, const Position& o, const TX* xr,
                                    const TY* yr, int rank) {
-    const Sums m = exact_sums<TX, TY>(sh, turn, xr, yr, a.vocab, a.scale, a.y_scale, o.pm, o.qm, rank,
-                                      a.cluster);
-    const double wp = weight64(weight31(xr[o.token], a.scale, o.pm));
+    const Sums m = exact_sums<TX, TY>(sh, turn, a, xr, yr, o.pm, o.qm, rank);
+    const double wp = weight64(weight31(xr[o.token], a.x_unit, o.pm));
     double wq = 1.0, sq = 1.0;
     if (DRAFT) {
-        wq = weight64(weight31(yr[o.token], a.y_scale, o.qm));
+        wq = weight64(weight31(yr[o.token], a.y_unit, o.qm));
         sq = m.q;
     }
     bool less = static_cast<double>(o.u) * wq * m.p < wp * sq;
     if (wp == 0.0 || wq == 0.0) {  // below 2^-1000: by their logarithms
-        const double lp = static_cast<double>(o.xd) * a.scale - o.pm - log(m.p);
-        const double lq = DRAFT ? static_cast<double>(o.yd) * a.y_scale - o.qm - log(m.q) : 0.0;
+        const S &u = a.x_unit, &w = a.y_unit;
+        const double xd = in_unit(u, o.xd), yd = in_unit(w, o.yd);
+        const double lp = (xd - o.pm) * u.z - log(m.p);
+        const double lq = DRAFT ? (yd - o.qm) * w.z - log(m.q) : 0.0;
         less = log(static_cast<double>(o.u)) + lq < lp;
     }
     return less ? kAccept : kRefuse;
 }
 
 // Position j, number g of the round, from the rows' sums (one warp).
-template <typename TX, typename TY, bool DRAFT>
-__device__ __forceinline__ void weigh(Shared& sh, int turn, const VerifyArgs& a, int R, int g, int j, bool drafted,
+template <typename TX, typename TY, bool DRAFT, typename S>
+__device__ __forceinline__ void weigh(Shared& sh, int turn, const Args<S>& a, int R, int g, int j, bool drafted,
                                       const TX* xr, const TY* yr) {
     const int lane = threadIdx.x & 31;
     const int row = (DRAFT ? 2 * g : g) + (DRAFT && lane >= 16 && drafted);
-    const Soft h = join_rows(sh, turn, row, R, a.cluster);
+    const bool of_draft = DRAFT && lane >= 16;
+    const RowSum h = whole_row(join_rows(sh, turn, row, R, a.cluster, of_draft ? a.y_unit.c : a.x_unit.c),
+                               of_draft ? a.y_unit.z : a.x_unit.z);
     Position o;
-    o.pm = __shfl_sync(0xffffffffu, h.mz, 0);
+    o.pm = __shfl_sync(0xffffffffu, h.m, 0);
     o.ps = __shfl_sync(0xffffffffu, h.s, 0);
-    o.qm = __shfl_sync(0xffffffffu, h.mz, 16);
+    o.qm = __shfl_sync(0xffffffffu, h.m, 16);
     o.qs = __shfl_sync(0xffffffffu, h.s, 16);
     o.verdict = o.ps != o.ps ? kBroken : kEnd;
     o.xd = o.yd = o.u = 0.0f;
@@ -648,16 +757,16 @@ __device__ __forceinline__ void weigh(Shared& sh, int turn, const VerifyArgs& a,
         o.u = __uint_as_float(sh.words[g][2]);
         bool q_nan = false, in_q = true;
         float rel, rel_q = 0.0f, wq = 1.0f, sq = 1.0f;
-        const float wp = weight(o.xd, a.scale, o.pm, rel);
+        const float wp = weight(o.xd, a.x_unit, o.pm, rel);
         if (DRAFT) {
             o.yd = from_word(sh.words[g][1], yr + o.token);
             q_nan = o.qs != o.qs;
             in_q = o.qs != 0.0f && __fmul_rn(o.yd, a.y_scale) != neg_inf();
-            wq = weight(o.yd, a.y_scale, o.qm, rel_q);
+            wq = weight(o.yd, a.y_unit, o.qm, rel_q);
             sq = o.qs;
         }
         if (lane == 0) {
-            sh.z[j] = fmaf(o.xd, a.scale, -o.pm);
+            sh.z[j] = scaled(a.x_unit, o.xd, o.pm);
             sh.sum[j] = o.ps;
         }
         if (o.ps != o.ps || q_nan) {
@@ -682,16 +791,13 @@ __device__ __forceinline__ void weigh(Shared& sh, int turn, const VerifyArgs& a,
 }
 
 // The token after position o: the row of the target, the draft's, the noise.
-template <typename TX, typename TY, bool DRAFT>
-__device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const VerifyArgs& a, const Position& o,
+template <typename TX, typename TY, bool DRAFT, typename S>
+__device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const Args<S>& a, const Position& o,
                                         int verdict, const TX* xr, const TY* yr, const float* noise, int rank) {
-    const int C = a.cluster;
     Rows<TX, TY> r;
     r.x = xr;
     r.y = nullptr;
     r.e = noise;
-    r.xs = a.scale;
-    r.ys = a.y_scale;
     r.pm = o.pm;
     r.qm = o.qm;
     r.ratio = 0.0f;
@@ -708,17 +814,17 @@ __device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const VerifyArgs&
     }
     int32_t token = -1;
     for (int pass = 0; pass < 2; ++pass) {
-        const Race b = race_pass<TX, TY>(sh, turn, r, a.vocab, rank, C, &sh.low[pass]);
+        const Race b = race_pass<TX, TY>(sh, turn, a, r, rank, &sh.low[pass]);
         ++turn;
         if (b.low > 0.0f && b.second < b.low) {
             token = b.token;
         } else {
             Sums m{1.0, 1.0};
             if (r.y) {
-                m = exact_sums<TX, TY>(sh, turn, r.x, r.y, a.vocab, r.xs, r.ys, r.pm, r.qm, rank, C);
+                m = exact_sums<TX, TY>(sh, turn, a, r.x, r.y, r.pm, r.qm, rank);
                 ++turn;
             }
-            token = exact_race<TX, TY, DRAFT>(sh, turn, r, m, b.low, a.vocab, rank, C);
+            token = exact_race<TX, TY, DRAFT>(sh, turn, a, r, m, b.low, rank);
             ++turn;
         }
         if (token >= 0 || (!r.y && r.without < 0)) break;
@@ -728,8 +834,8 @@ __device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const VerifyArgs&
     return token;
 }
 
-template <typename TX, typename TY, bool DRAFT>
-__global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
+template <typename TX, typename TY, bool DRAFT, typename S>
+__global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ Args<S> a) {
     __shared__ Shared sh;
     const int C = a.cluster;
     const uint32_t rank = C > 1 ? cluster_rank() : 0u;
@@ -788,13 +894,14 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
             const int row = warp % R, nt = (kWarps - row + R - 1) / R * 32;
             const int tr = warp / R * 32 + lane;
             const int j = j0 + (DRAFT ? row >> 1 : row);
-            Soft q = soft_empty();
-            if (DRAFT && (row & 1))
-                stream_row<TY>(q, y + j * a.y_stride, V, rank, C, a.y_scale, tr, nt);
+            RowSum q{lowest(), 0.0f};
+            const bool of_draft = DRAFT && (row & 1);
+            if (of_draft)
+                stream_row<TY>(q, y + j * a.y_stride, V, rank, C, a.y_unit, tr, nt);
             else
-                stream_row<TX>(q, x + j * a.stride, V, rank, C, a.scale, tr, nt);
+                stream_row<TX>(q, x + j * a.stride, V, rank, C, a.x_unit, tr, nt);
             __syncwarp();
-            soft_lanes<false, 32>(q);
+            row_lanes<32>(q, of_draft ? a.y_unit.c : a.x_unit.c);
             if (warp == 0) drain_copies();
             exchange(sh, turn, C, rank, pack(q));
         }
@@ -823,7 +930,7 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
         // (the next round's barrier lies before the positions' next writing)
     }
     const int A = j0 + at;
-    const Position o = sh.pos[at];
+    const Position& o = sh.pos[at];
     int32_t token = -1;
     float lp = __int_as_float(0x7fffffff);
     if (verdict != kBroken) {
@@ -834,7 +941,7 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
             token = draw<TX, TY, DRAFT>(sh, turn, a, o, verdict, xr, DRAFT ? y + A * a.y_stride : nullptr, noise,
                                         rank);
             if (token >= 0 && rank == 0)
-                lp = __fsub_rn(fmaf(to_f32(xr[token]), a.scale, -o.pm), logf(o.ps));
+                lp = __fsub_rn(scaled(a.x_unit, to_f32(xr[token]), o.pm), logf(o.ps));
         }
     }
     if (rank == 0) {
@@ -851,7 +958,7 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
 // ------------------------------------------------------------ without a draft
 // Sampling (k = 0): the winner does not hang on the row's sum, so statistics and race
 // share one pass over row and noise and one exchange.  A warp's weights are relative
-// to the largest z that it has met, and are taken to the row's largest when the warps
+// to the largest x h that it has met, and are taken to the row's largest when the warps
 // are joined; the sum's weights w sift the race too, as no token with w < low e can reach
 // a score of `low`.  A race that is not certain goes to the general kernel's code.
 //
@@ -863,23 +970,23 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
 
 // Scores relative to `from` taken to `to`.  Bounds stay bounds: an upper one gets the
 // least normal number on top, a lower one is given up where little is left.
-__device__ __forceinline__ void race_rebase(Race& r, float from, float to) {
-    const float t = __fmul_rn(__fsub_rn(from, to), kLog2e);
+__device__ __forceinline__ void race_rebase(Race& r, float from, float to, float c) {
+    const float t = fmaxf(__fmul_rn(__fsub_rn(from, to), c), -1024.0f);
     const float f = exp2_approx(0.5f * t), err = fmaf(fabsf(t), 0x1p-22f, 0x1p-20f);
     r.low = t > -30.0f ? r.low * f * f * (1.0f - err) : 0.0f;
     if (r.up > 0.0f && r.up < pos_inf()) r.up = fmaf(r.up * f, f * (1.0f + err), 0x1p-126f);
     if (r.second > 0.0f && r.second < pos_inf()) r.second = fmaf(r.second * f, f * (1.0f + err), 0x1p-126f);
 }
 
-// Weights 2^((x scale - ref) log2(e)) of a chunk and their sum.
-template <typename T>
-__device__ __forceinline__ float chunk_weights(const Chunk<T>& x, float scale, float ref, float (&w)[8]) {
-    const uint64_t sc = pk2(scale, scale), nr = pk2(-ref, -ref), l2 = pk2(kLog2e, kLog2e);
+// Weights 2^((x h - ref) c) of a chunk and their sum.
+template <typename T, typename S>
+__device__ __forceinline__ float chunk_weights(const Chunk<T>& x, const S& u, float ref, float (&w)[8]) {
+    const uint64_t cc = pk2(u.c, u.c);
     uint64_t s[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float t0, t1;
-        upk2(mul2(fma2(x.pair(k), sc, nr), l2), t0, t1);
+        upk2(mul2(less2(u, x.pair(k), ref), cc), t0, t1);
         w[2 * k] = exp2_approx(t0);
         w[2 * k + 1] = exp2_approx(t1);
         s[k & 1] = add2(s[k & 1], pk2(w[2 * k], w[2 * k + 1]));
@@ -909,7 +1016,7 @@ __device__ __forceinline__ void in_order(const Noise8& e, int ph, float (&v)[8])
     }
 }
 
-// A token's score w / e, from a weight 2^t.  Relative errors: |t| 2^-23 of t's three
+// A token's score w / e, from a weight 2^t.  Relative errors: |t| 1.04 * 2^-23 of t's three
 // roundings, the units' two ulp and one, the product's; a lower bound counts if the weight
 // is far from the end of the range.  Nothing is drawn at e < 0 or NaN; 0 wins, and is
 // decided in 64 bits, as is a subnormal e.
@@ -925,8 +1032,8 @@ __device__ __forceinline__ void race_token(Race& b, float w, float e, int32_t i)
     race_add(b, low, up, i);
 }
 
-template <typename TX>
-__device__ __noinline__ int32_t draw_again(Shared& sh, const VerifyArgs& a, float pm, float ps, const TX* xr,
+template <typename TX, typename S>
+__device__ __noinline__ int32_t draw_again(Shared& sh, const Args<S>& a, float pm, float ps, const TX* xr,
                                            const float* noise, int rank) {
     Position o;
     o.pm = pm;
@@ -937,8 +1044,8 @@ __device__ __noinline__ int32_t draw_again(Shared& sh, const VerifyArgs& a, floa
     return draw<TX, TX, false>(sh, turn, a, o, kEnd, xr, nullptr, noise, rank);
 }
 
-template <typename TX>
-__global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ VerifyArgs a) {
+template <typename TX, typename S>
+__global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ Args<S> a) {
     __shared__ Shared sh;
     __shared__ uint4 more[kWarps][kMaxCluster];
     const int C = a.cluster;
@@ -947,7 +1054,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     const int64_t s = blockIdx.x / C;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int32_t V = a.vocab;
-    const float scale = a.scale;
+    const S& u = a.x_unit;
     const TX* x = static_cast<const TX*>(a.x) + s * a.stride;
     const float* noise = a.noise + s * a.noise_stride;
     wait_prior_grids();
@@ -961,25 +1068,21 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     const float* es = noise + cut.head;
     float sum = 0.0f;
     Race b{0.0f, 0.0f, 0.0f, -1};
-    float ref = neg_inf();
+    float ref = lowest();  // before any token above that, none of which is in the race
     // `low`: of a score that some token of the warp has; base: the reference of the oldest
-    float low = 0.0f, base = neg_inf();
-    // The lanes' largest z: the warp's weights become relative to it (all lanes).
+    float low = 0.0f, base = lowest();
+    // The lanes' largest x h: the warp's weights become relative to it (all lanes).
     const auto meet = [&](float z) {
         if (!__any_sync(0xffffffffu, z > ref)) return;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-        if (ref != neg_inf()) {
-            sum = __fmul_rn(sum, exp2_approx(__fmul_rn(__fsub_rn(ref, z), kLog2e)));
-            race_rebase(b, ref, z);
-            if (!(z - base < 20.0f)) {
-                b.low = 0.0f;
-                base = z;
-            }
-            low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.low)));
-        } else {
+        sum = __fmul_rn(sum, exp2_approx(__fmul_rn(__fsub_rn(ref, z), u.c)));
+        race_rebase(b, ref, z, u.c);
+        if (!((z - base) * u.c < 28.0f)) {
+            b.low = 0.0f;
             base = z;
         }
+        low = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.low)));
         ref = z;
     };
     Chunk<TX> nx;
@@ -1000,12 +1103,12 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         const Noise8 e = ne;
         load(c + step);
         __syncwarp();
-        meet(__fmul_rn(xc.max(), scale));
+        meet(in_unit(u, xc.max()));
         // (a NaN, which max passes over, goes into the sum)
         float w[8], ev[8];
-        sum = __fadd_rn(sum, chunk_weights(xc, scale, ref == neg_inf() ? 0.0f : ref, w));
+        sum = __fadd_rn(sum, chunk_weights(xc, u, ref, w));
         in_order(e, ep, ev);
-        if (low == 0.0f && ref != neg_inf()) {  // about what the warp's best token has
+        if (low == 0.0f && ref != lowest()) {  // about what the warp's best token has
             float l = 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -1019,7 +1122,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         float d = fmaf(ev[0], under, w[0]);
 #pragma unroll
         for (int k = 1; k < 8; ++k) d = fmaxf(d, fmaf(ev[k], under, w[k]));
-        const bool pass = c < cut.chunks && ref != neg_inf() && d >= 0.0f;
+        const bool pass = c < cut.chunks && ref != lowest() && d >= 0.0f;
         if (!__any_sync(0xffffffffu, pass)) continue;
         if (pass) {
             const int32_t i0 = cut.head + 8 * c;
@@ -1037,20 +1140,19 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         xc.fill(neg_inf());
         if (i >= 0) xc.set(0, x[i]);
         __syncwarp();
-        meet(__fmul_rn(xc.max(), scale));
+        meet(in_unit(u, xc.max()));
         float w[8];
-        sum = __fadd_rn(sum, chunk_weights(xc, scale, ref == neg_inf() ? 0.0f : ref, w));
-        if (i >= 0 && ref != neg_inf()) race_token(b, w[0], noise[i], i);
+        sum = __fadd_rn(sum, chunk_weights(xc, u, ref, w));
+        if (i >= 0 && ref != lowest()) race_token(b, w[0], noise[i], i);
     }
-    Soft q{neg_inf(), ref == neg_inf() ? 0.0f : ref, sum, 0.0f};
+    RowSum q{ref, sum};
     __syncwarp();
-    soft_lanes<false, 32>(q);
+    row_lanes<32>(q, u.c);
     b = race_lanes(b);
     {
-        const uint4 v = make_uint4(__float_as_uint(q.mz), __float_as_uint(q.s), __float_as_uint(b.low),
+        const uint4 v = make_uint4(__float_as_uint(q.m), __float_as_uint(q.s), __float_as_uint(b.low),
                                    __float_as_uint(b.up));
-        const uint4 w = make_uint4(__float_as_uint(b.second), static_cast<uint32_t>(b.token),
-                                   __float_as_uint(ref), 0u);
+        const uint4 w = make_uint4(__float_as_uint(b.second), static_cast<uint32_t>(b.token), 0u, 0u);
         if (C == 1) {
             if (lane == 0) {
                 sh.parts[0][warp][0] = v;
@@ -1068,31 +1170,30 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
     }
     // One warp joins all of them: lane i has the parts i and i + 32.
     if (warp == 0) {
-        Soft h = soft_empty();
-        if (lane < kWarps * C) h = unpack(sh.parts[0][lane / C][lane % C]);
-        if (lane + 32 < kWarps * C) {
-            Soft g = unpack(sh.parts[0][(lane + 32) / C][(lane + 32) % C]);
-            float top = fmaxf(soft_top(h), soft_top(g));
-            if (top == neg_inf()) top = 0.0f;
-            soft_rebase<false>(h, top);
-            soft_rebase<false>(g, top);
-            h.s = __fadd_rn(h.s, g.s);
-            if (top == pos_inf()) h.s = __int_as_float(0x7fffffff);
-        }
-        __syncwarp();
-        soft_lanes<false, 32>(h);
+        RowSum g{lowest(), 0.0f}, h = g;
+        if (lane < kWarps * C) g = unpack(sh.parts[0][lane / C][lane % C]);
+        if (lane + 32 < kWarps * C) h = unpack(sh.parts[0][(lane + 32) / C][(lane + 32) % C]);
+        float top = fmaxf(g.m, h.m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        h.s = __fadd_rn(__fmul_rn(g.s, exp2_approx(__fmul_rn(__fsub_rn(g.m, top), u.c))),
+                        __fmul_rn(h.s, exp2_approx(__fmul_rn(__fsub_rn(h.m, top), u.c))));
+        h.m = top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) h.s = __fadd_rn(h.s, __shfl_xor_sync(0xffffffffu, h.s, o));
+        h = whole_row(h, u.z);
         Race best{0.0f, 0.0f, 0.0f, -1};
         for (int j = lane; j < kWarps * C; j += 32) {
             const uint4 v = sh.parts[0][j / C][j % C], w = more[j / C][j % C];
             Race o{__uint_as_float(v.z), __uint_as_float(v.w), __uint_as_float(w.x), static_cast<int32_t>(w.y)};
-            if (__uint_as_float(w.z) != neg_inf()) race_rebase(o, __uint_as_float(w.z), h.mz);
+            race_rebase(o, __uint_as_float(v.x), h.m, u.c);
             race_join(best, o);
         }
         __syncwarp();
         best = race_lanes(best);
         if (lane == 0) {
             Position& o = sh.pos[0];
-            o.pm = h.mz;
+            o.pm = h.m;
             o.ps = h.s;
             // whether the answer is there: no sum, or a race that is certain
             o.verdict = !(h.s > 0.0f) || (best.low > 0.0f && best.second < best.low) ? kEnd : kClose;
@@ -1109,16 +1210,43 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
         if (a.logprobs)
             a.logprobs[s] = o.ps != o.ps ? __int_as_float(0x7fffffff)
                             : token < 0  ? neg_inf()
-                                         : __fsub_rn(fmaf(to_f32(x[token]), scale, -o.pm), logf(o.ps));
+                                         : __fsub_rn(scaled(u, to_f32(x[token]), o.pm), logf(o.ps));
     }
 }
 
-template <typename TX, typename TY>
-cudaError_t launch_types(const VerifyArgs& a, cudaStream_t stream) {
+template <typename TX, typename TY, typename S>
+cudaError_t launch_types(const Args<S>& a, cudaStream_t stream) {
     const int64_t grid = a.n * a.cluster;
-    if (a.k == 0) return launch_vocab(sample_kernel<TX>, grid, kNT, 0, a.cluster, a, stream);
-    return a.y ? launch_vocab(verify_kernel<TX, TY, true>, grid, kNT, 0, a.cluster, a, stream)
-               : launch_vocab(verify_kernel<TX, TX, false>, grid, kNT, 0, a.cluster, a, stream);
+    if (a.k == 0) return launch_vocab(sample_kernel<TX, S>, grid, kNT, 0, a.cluster, a, stream);
+    return a.y ? launch_vocab(verify_kernel<TX, TY, true, S>, grid, kNT, 0, a.cluster, a, stream)
+               : launch_vocab(verify_kernel<TX, TX, false, S>, grid, kNT, 0, a.cluster, a, stream);
+}
+
+void set_scale(LogitScale& u, double scale) {
+    const double c = scale * 1.4426950408889634;
+    u.c = static_cast<float>(c);
+    u.cl = static_cast<float>(c - static_cast<double>(u.c));
+    u.z = static_cast<float>(scale);
+}
+bool far(float scale) { return scale > 0x1p100f || scale < 0x1p-100f; }
+// h keeps differences of logits, and what they are multiplied by, inside binary32: where
+// the inverse temperature is small they may be over 2^128, where it is large c may be.
+void set_scale(FarScale& u, double scale) {
+    const double h = scale > 0x1p100 ? 0x1p64 : scale < 0x1p-100 ? 0x1p-64 : 1.0;
+    set_scale(static_cast<LogitScale&>(u), scale / h);
+    u.h = static_cast<float>(h);
+}
+
+template <typename S>
+cudaError_t launch_scaled(const VerifyArgs& args, cudaStream_t stream) {
+    Args<S> a;
+    static_cast<VerifyArgs&>(a) = args;
+    set_scale(a.x_unit, a.scale);
+    set_scale(a.y_unit, a.y_scale);
+    if (a.dtype == ZERO3_BF16)
+        return a.y_dtype == ZERO3_BF16 ? launch_types<uint16_t, uint16_t>(a, stream)
+                                       : launch_types<uint16_t, float>(a, stream);
+    return a.y_dtype == ZERO3_BF16 ? launch_types<float, uint16_t>(a, stream) : launch_types<float, float>(a, stream);
 }
 
 }  // namespace
@@ -1146,10 +1274,7 @@ cudaError_t launch_verify(const VerifyArgs& args, cudaStream_t stream) {
     while (a.vocab >> bits) ++bits;
     const int chain = a.vocab / (16 * 32 * a.cluster * (kWarps / rows)) + 32;
     a.sum_error = 6 * 0x1p-22f + 1.2f * 0x1p-23f * static_cast<float>(bits) + static_cast<float>(chain) * 0x1p-24f;
-    if (a.dtype == ZERO3_BF16)
-        return a.y_dtype == ZERO3_BF16 ? launch_types<uint16_t, uint16_t>(a, stream)
-                                       : launch_types<uint16_t, float>(a, stream);
-    return a.y_dtype == ZERO3_BF16 ? launch_types<float, uint16_t>(a, stream) : launch_types<float, float>(a, stream);
+    return far(a.scale) || far(a.y_scale) ? launch_scaled<FarScale>(a, stream) : launch_scaled<LogitScale>(a, stream);
 }
 
 }  // namespace z3
