@@ -1266,14 +1266,22 @@ cudaError_t launch_verify(const VerifyArgs& args, cudaStream_t stream) {
     // seven, 104 by two; 256 of five drafts: 76 by three, 71 by two, 73 one by one).
     a.ahead = a.y ? (a.n <= 100 ? 3 : 2) : (a.n <= 200 ? 7 : 2);
     const int g = a.ahead < a.k ? a.ahead : a.k, rows = (a.y ? 2 * g : g) + 1;
-    // Relative error of a row's sum.  Its terms: the unit's two ulp (2^-22), three
-    // roundings of t, 1.2 * 2^-23 |t| on their average |t|, which is at most log2(V); a
-    // thread's chain of additions and the joins (its batches, then at most 32
-    // more); five changes of the reference, 2^-22 each.
+    // Relative error of a row's sum.  Its terms: the unit's two ulp (2^-22), and three
+    // roundings of t, 1.04 * 2^-23 |t| on their average |t|, which is at most log2(V).  A thread's
+    // chain of additions and the joins: its batches, then at most 32 more.  Changes of the
+    // reference, two ulp and a product each: where logits rise, every batch may be one, and the
+    // sum before it keeps nearly all of its weight; four chunks and ends, and two joins, on top;
+    // the roundings of their differences 2^-21, as a sum with |t| that much lower counts that
+    // much less.  (Rows that rise by 0.01 to 3000 were off by a quarter of what the additions
+    // alone allow.)
     int bits = 1;
     while (a.vocab >> bits) ++bits;
-    const int chain = a.vocab / (16 * 32 * a.cluster * (kWarps / rows)) + 32;
-    a.sum_error = 6 * 0x1p-22f + 1.2f * 0x1p-23f * static_cast<float>(bits) + static_cast<float>(chain) * 0x1p-24f;
+    const int threads = 32 * a.cluster * (kWarps / rows);  // of a row
+    const bool wide = a.dtype == ZERO3_F32 || (a.y && a.y_dtype == ZERO3_F32);
+    const int batches = a.vocab / ((wide ? 16 : 32) * threads);
+    a.sum_error = 0x1p-22f + 0x1p-21f + 1.2f * 0x1p-23f * static_cast<float>(bits) +
+                  static_cast<float>(batches + 32) * 0x1p-24f +
+                  static_cast<float>(batches + 6) * (0x1p-22f + 0x1p-24f);
     return far(a.scale) || far(a.y_scale) ? launch_scaled<FarScale>(a, stream) : launch_scaled<LogitScale>(a, stream);
 }
 
