@@ -786,8 +786,8 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
  * The answer is that of exact arithmetic on the given numbers: binary32 decides where
  * it is certain, closer decisions are taken again with weights of 31 bits or more.
  *  - Tokens whose e is negative (-0 too), NaN or infinite, or whose probability is
- *    below 2^-126 of the row's largest, are not drawn; e = 0 wins over every
- *    e > 0 where the residual is positive.  Where no token has a positive
+ *    below 2^-126 of the row's largest, are not drawn, even where no other is left
+ *    (they are accepted like any); e = 0 wins over every e > 0 where the residual is positive.  Where no token has a positive
  *    residual the draw is from p_A.  A NaN or negative u refuses.
  *  - Log probabilities are exact to about 2^-22 of themselves plus 2^-22 (a nearly
  *    certain token's keeps fewer digits).

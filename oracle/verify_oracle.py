@@ -5,6 +5,9 @@ from __future__ import annotations
 import numpy as np
 
 
+LEAST = 2.0 ** -126  # of the row's largest probability: below this tokens are not drawn
+
+
 def _row(z):
     """Log probabilities of one row of logits; -inf everywhere in a row without any
     token, NaN where a NaN or +inf spoils it."""
@@ -67,6 +70,7 @@ def verify(logits, draft_logits, ids, uniform, noise, scale=1.0, draft_scale=1.0
             lps[s, j] = np.nan
             continue
         p = np.exp(lp)
+        p[p < p.max() * LEAST] = 0  # too unlikely to be drawn
         e = np.asarray(noise[s], np.float64)
         t = _draw(p - np.exp(q), e) if refused else -1
         if t < 0:
