@@ -361,6 +361,10 @@ struct Rows {
 template <typename TX, typename TY, bool DRAFT>
 using RowsOf = std::conditional_t<DRAFT, const Rows<TX, TY>&, Rows<TX, TY>>;
 
+// Below this scores decide nothing: they, and their bounds, are next to the subnormal
+// numbers, and 1 / e of huge noise is 0.
+constexpr float kLeastScore = 0x1p-100f;
+
 // Score of token i: (wp - ratio wq) / e, and how far it may be off.
 template <typename TX, typename TY, typename S>
 __device__ __forceinline__ void score(const Args<S>& a, const Rows<TX, TY>& r, TX x, TY y, float e,
@@ -392,7 +396,9 @@ __device__ __forceinline__ void score(const Args<S>& a, const Rows<TX, TY>& r, T
 // bound without a special function: log2(1 / e) is at most what the bits of e say
 // (a line between powers of two lies below log2, by 0.086 at most), and t with 14
 // bits behind the point is the integer part of one multiply-add on 2^23.  In
-// 2^-23:  bound = 512 T - bits(e) + bits(1).
+// 2^-23:  bound = 512 T - bits(e) + bits(1).  Below the normal numbers (and at 0) the bits of e
+// say too much; such noise is never passed over, as no low above 2^26 is asked for (T is at
+// least -100, and log2(1 / e) over 126 there).
 struct Sieve {
     float a, c;
     int32_t margin;
@@ -415,8 +421,9 @@ struct Sieve {
     }
     // What is above this cannot reach a score of `low`.
     __device__ __forceinline__ int32_t limit(uint32_t low) const {
-        return low == 0u || margin == 0x7fffffff ? 0x7fffffff
-                                                 : 0x3f800000 - static_cast<int32_t>(low) + margin;
+        const int32_t most = 0x4c800000;  // 2^26
+        const int32_t l = static_cast<int32_t>(low) < most ? static_cast<int32_t>(low) : most;
+        return low == 0u || margin == 0x7fffffff ? 0x7fffffff : 0x3f800000 - l + margin;
     }
 };
 
@@ -816,8 +823,9 @@ __device__ __forceinline__ int32_t draw(Shared& sh, int& turn, const Args<S>& a,
     }
     int32_t token = -1;
     for (int pass = 0; pass < 2; ++pass) {
-        const Race b = race_pass<TX, TY>(sh, turn, a, r, rank, &sh.low[pass]);
+        Race b = race_pass<TX, TY>(sh, turn, a, r, rank, &sh.low[pass]);
         ++turn;
+        if (b.low < kLeastScore) b.low = 0.0f;
         if (b.low > 0.0f && b.second < b.low) {
             token = b.token;
         } else {
@@ -1198,7 +1206,7 @@ __global__ void __launch_bounds__(kNT, 4) sample_kernel(const __grid_constant__ 
             o.pm = h.m;
             o.ps = h.s;
             // whether the answer is there: no sum, or a race that is certain
-            o.verdict = !(h.s > 0.0f) || (best.low > 0.0f && best.second < best.low) ? kEnd : kClose;
+            o.verdict = !(h.s > 0.0f) || (best.low >= kLeastScore && best.second < best.low) ? kEnd : kClose;
             o.token = h.s > 0.0f ? best.token : -1;
         }
     }
