@@ -22,8 +22,8 @@ def _row(z):
 
 def _draw(residual, noise):
     """The token with the largest residual / noise among those with a positive one
-    and a noise of 0 or more (0 wins); the lowest index of equal ones; or -1."""
-    ok = (residual > 0) & (noise >= 0) & (noise < np.inf)
+    and a noise of 0 or more (0 wins, -0 is less); the lowest index of equal ones; or -1."""
+    ok = (residual > 0) & (noise >= 0) & ~np.signbit(noise) & (noise < np.inf)
     if not ok.any():
         return -1
     with np.errstate(divide="ignore", invalid="ignore"):

@@ -66,3 +66,18 @@ def test_scores_that_binary32_holds_to_few_digits(z, k, draft):  # noqa: F811
     c.noise[:] = 2.0 ** 81 * (1 + 0.01 * torch.rand(n, V, generator=g))
     c.noise[:, V - 2] = INF
     c.run(z)
+
+
+@pytest.mark.parametrize("small", [0.0, 1e-42])
+def test_negative_zero_beside_a_negative_residual(z, small):  # noqa: F811
+    """The draft's token is above the target's, its noise -0: minus by minus is no plus."""
+    for n, V in ((4, 40), (4, 3001), (320, 500)):
+        c = Case(n, 1, V, "f32", "f32", seed=46)
+        c.x[:], c.y[:] = 0.0, 0.0
+        c.y[:, :, 2] = 3.0
+        c.ids[:], c.u[:] = 2, 0.9
+        c.noise[:] = INF
+        c.noise[:, 2] = -0.0
+        c.noise[:, 5] = small
+        got = c.run(z)
+        assert (got[0] == 0).all() and (got[1][:, 0] == 5).all()

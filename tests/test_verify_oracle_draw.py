@@ -1,5 +1,5 @@
 """What the 64-bit definition of the draw leaves out: tokens below 2^-126 of the row's
-largest probability."""
+largest probability, and negative noise, -0 among it."""
 import numpy as np
 import pytest
 
@@ -28,3 +28,9 @@ def test_acceptance_has_no_such_bound():
     z, y = np.array([[[0.0, -200.0], [0.0, 0.0]]]), np.array([[[0.0, -201.0]]])
     a, t, _ = VO.verify(z, y, np.array([[1]]), np.array([[0.5]]), np.ones((1, 2)))
     assert a[0] == 1 and t[0].tolist() == [1, 0]
+
+
+@pytest.mark.parametrize("noise", [(-0.0, -0.0), (-0.0, float("nan"))])
+def test_negative_zero_is_negative(noise):
+    assert draw((0.0, 1.0), noise)[0] == -1
+    assert draw((0.0, 1.0, 0.5), noise + (3.0,))[0] == 2

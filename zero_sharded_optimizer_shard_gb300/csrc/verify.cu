@@ -680,7 +680,8 @@ __device__ __noinline__ int32_t exact_race(Shared& sh, int turn, const Args<S>& 
             float s, off, rel;
             score(a, r, x, y, e, i, s, off);
             // a token below the range of binary32 weights is not drawn, even alone
-            if (!(s + off >= low) || !(e >= 0.0f) || i == r.without || weight(x, a.x_unit, r.pm, rel) == 0.0f)
+            if (!(s + off >= low) || !(e >= 0.0f) || __float_as_int(e) < 0 || i == r.without ||
+                weight(x, a.x_unit, r.pm, rel) == 0.0f)
                 continue;
             double v = weight64(weight31(x, a.x_unit, r.pm));
             if (r.y) v = v / sums.p - weight64(weight31(y, a.y_unit, r.qm)) / sums.q;
