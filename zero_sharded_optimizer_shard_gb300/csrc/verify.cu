@@ -238,9 +238,11 @@ __device__ __forceinline__ float chunk_element(const Chunk<T>& c, int k) {
 // 2^(n + f), |f| <= 0.5002, as y / 2^31 * 2^n with 0.70 < y / 2^31 < 1.42, from the Taylor
 // series of 2^f = e^(f ln 2), terms (f ln 2)^k / k!, k <= 9 (the next is below 8e-12),
 // in fixed point.
+// Below 2^kLeast31 there is none: y * 2^(n - 31) stays a normal binary64 number (2^-1022).
+constexpr int kLeast31 = -960, kNoWeight31 = -2000;
 struct Weight {
     uint32_t y;
-    int32_t n;  // below -1000: no weight
+    int32_t n;  // kNoWeight31: no weight
 };
 
 template <typename T, typename S>
@@ -250,14 +252,14 @@ __device__ __forceinline__ Weight weight31(T x, const S& u, float m) {
     const float d = __fsub_rn(z, m);
     const float bb = __fsub_rn(d, z);
     const float dl = __fadd_rn(__fsub_rn(z, __fsub_rn(d, bb)), -__fadd_rn(m, bb));
-    // times c + cl (the second part is 2^-23 of the first at most, and -1000 < t here:
+    // times c + cl (the second part is 2^-23 of the first at most, and -960 < t here:
     // below 2^-12)
     const float t = __fmul_rn(d, u.c);
     const float tl = fmaf(d, u.c, -t) + fmaf(d, u.cl, __fmul_rn(dl, u.c));
     Weight w;
-    if (!(t > -1000.0f)) {  // masked tokens too
+    if (!(t > static_cast<float>(kLeast31))) {  // masked tokens too
         w.y = 0;
-        w.n = -2000;
+        w.n = kNoWeight31;
         return w;
     }
     const float r = rintf(t);
@@ -274,7 +276,7 @@ __device__ __forceinline__ Weight weight31(T x, const S& u, float m) {
 }
 
 __device__ __forceinline__ double weight64(const Weight& w) {
-    if (w.n < -1000) return 0.0;
+    if (w.n == kNoWeight31) return 0.0;
     return static_cast<double>(w.y) * __hiloint2double((1023 + w.n - 31) << 20, 0);
 }
 
@@ -734,7 +736,7 @@ __device__ __noinline__ int decide(Shared& sh, int turn, const Args<S>& a, const
         sq = m.q;
     }
     bool less = static_cast<double>(o.u) * wq * m.p < wp * sq;
-    if (wp == 0.0 || wq == 0.0) {  // below 2^-1000: by their logarithms
+    if (wp == 0.0 || wq == 0.0) {  // too far below: by their logarithms
         const S &u = a.x_unit, &w = a.y_unit;
         const double xd = in_unit(u, o.xd), yd = in_unit(w, o.yd);
         const double lp = (xd - o.pm) * u.z - log(m.p);
