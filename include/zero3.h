@@ -784,7 +784,9 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
  * accepted [n]: A.  tokens [n, k + 1]: the accepted tokens, the drawn one, then -1.
  * logprobs [n, k + 1] (optional): log p_j of those tokens, 0 behind them.
  * The answer is that of exact arithmetic on the given numbers: binary32 decides where
- * it is certain, closer decisions are taken again with weights of 31 bits or more.
+ * it is certain, closer decisions are taken again with weights of 31 bits or more (what
+ * differs by less than about 1e-9, two scores or p and q of a token, counts as equal or falls
+ * either way).
  *  - Tokens whose e is negative (-0 too), NaN or infinite, or whose probability is
  *    below 2^-126 of the row's largest, are not drawn, even where no other is left
  *    (they are accepted like any); e = 0 wins over every e > 0 where the residual is positive.  Where no token has a positive
