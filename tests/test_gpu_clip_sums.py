@@ -55,3 +55,18 @@ def test_equal_numbers_beyond_the_range_of_squares(z, scale):  # noqa: F811
     _, sq, _, _ = norm(z, z.TensorList([x.data_ptr()] * 16, [x.numel()] * 16, z.BF16), 1.0, tensor_norms=False)
     want = 16 * x.numel() * (0.54296875 * scale) ** 2
     assert abs(sq - want) <= 9 * 2.0 ** -24 * want
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [2.0 ** 62, 1.5 * 2.0 ** 62, 2.0 ** 63, 1.25 * 2.0 ** 63, 2.0 ** -75])
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 7, 8, 11, 40, 263])
+def test_few_numbers_whose_squares_fit_alone(z, n, value, dtype):  # noqa: F811
+    """A square of 2^124 to 2^127.3 is a binary32 number, as is 2^-150's neighbour; a warp's
+    sum of them is none.  Small integers times a power of two: sums are exact in 64 bits."""
+    x = torch.full((n + 3,), value, device="cuda", dtype=dtype)
+    t = [x[1:1 + n], x[:n], x[3:3 + n]]
+    tn, sq, total, _ = norm(z, z.TensorList([v.data_ptr() for v in t], [n] * 3, z.BF16 if dtype == torch.bfloat16
+                                            else z.F32), 1.0)
+    assert sq == 3 * n * value * value
+    assert abs(total - (3 * n) ** 0.5 * value) <= 2.0 ** -23 * total
+    assert all(abs(float(v) - n ** 0.5 * value) <= 2.0 ** -23 * value * n ** 0.5 for v in tn)

@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads) list_norm_kernel(const __grid_consta
     d += static_cast<double>(s);
     // A sum near the ends of binary32's range (numbers beyond 2^60, or so small
     // that squares have lost bits): the thread's share is read again.
-    if (any && !(d >= 0x1p-90 && d <= 0x1p120)) {
+    const bool again = any && !(d >= 0x1p-90 && d <= 0x1p120);
+    if (again) {
         d = 0.0;
         for (int j = tid; j < own; j += kThreads) {
             WideSquares w;
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) list_norm_kernel(const __grid_consta
             d += w.value();
         }
     }
-    if (__any_sync(0xffffffffu, d != static_cast<double>(s))) {  // a NaN too
+    if (__any_sync(0xffffffffu, again || d != static_cast<double>(s))) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     } else {
