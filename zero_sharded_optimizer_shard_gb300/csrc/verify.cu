@@ -11,12 +11,13 @@
 // there; in a round each warp has a share of one row.  The race reads the target's
 // row again, mostly from L2, and the noise; of the draft's row only what may win.
 //
-// What bounds it: one sequence, a chain of latencies (12 us: a round's loads and its
-// exchange, the verdicts, the race and its exchange).  Many, the bytes that an SM has
-// in flight: 512 sequences of five tokens (50257 bf16) move 530 MB in 127 us, 6.8 TB/s in
+// What bounds it: one sequence, a chain of latencies (12.4 us: a round's loads and its
+// exchange, the verdicts, the race and its exchange).  Many, the sequences that run
+// longest: 512 of five tokens (50257 bf16) move 550 MB in 126 us, 6.8 TB/s in
 // the first round and less as sequences end (floor: the rows up to the refusal and
-// the noise once, 443 MB, 65 us).  256 threads with 64 registers, four blocks per SM; 512
-// threads, five or six blocks (spills), rows or noise through shared memory, the
+// the noise once, 443 MB, 65 us).  256 threads with 64 registers, four blocks per SM, at
+// which the instances with a draft spill 132 to 188 bytes and those without 8 to 12; five or
+// six blocks, with more of them, 512 threads, rows or noise through shared memory, the
 // race in a launch of its own: equal or slower.  Without a draft (k = 0) a kernel of its
 // own takes statistics and race in one pass.
 //
@@ -975,11 +976,13 @@ __global__ void __launch_bounds__(kNT, 4) verify_kernel(const __grid_constant__ 
 // are joined; the sum's weights w sift the race too, as no token with w < low e can reach
 // a score of `low`.  A race that is not certain goes to the general kernel's code.
 //
-// 128 sequences of 32000 masked binary32 logits: 10.0 us (statistics first and the race
+// 128 sequences of 32000 masked binary32 logits: 10.1 us (statistics first and the race
 // behind them: 16.7), 33 MB, a chain of latencies around four batches per warp; 512 of
-// 50257 bf16: 33.7 us (49.7), 154 MB at 4.6 TB/s, bound by instructions (170 per 256
-// elements, 42% of the issue slots) and by 512 blocks on 608 places.  80 registers and two batches
-// ahead: 45; five blocks per SM (spills): 40; lines brought to L2 further ahead: 34 to 36.
+// 50257 bf16: 32.1 us (49.7), 154 MB at 4.8 TB/s, bound by the loads in flight: one batch
+// ahead is 48 bytes a thread, 41 KB per SM, and 59% of the warps' time is waiting for them
+// (150 instructions per 256 elements take 43% of the issue slots; 512 blocks stand on 608
+// places).  80 registers and two batches ahead: 45; five blocks per SM (spills): 40; lines
+// brought to L2 further ahead: 34 to 36.
 
 // Scores relative to `from` taken to `to`.  Bounds stay bounds: an upper one gets the
 // least normal number on top, a lower one is given up where little is left.
@@ -1276,7 +1279,12 @@ cudaError_t launch_verify(const VerifyArgs& args, cudaStream_t stream) {
     // Positions per round, a row of which a warp has: all of them at once while
     // the chain of rounds is the time (48 sequences of ten: 45 us one by one, 23 by
     // seven), two where rows that turn out not to be needed are (512 of ten: 126 us by
-    // seven, 104 by two; 256 of five drafts: 76 by three, 71 by two, 73 one by one).
+    // seven, 104 by two; 256 of five drafts: 76 by three, 71 by two, 73 one by one).  Next to the
+    // places of the rule, 50257 tokens: five drafts, 76 sequences 40.9 by three, 41.8 by two,
+    // 100 42.2 and 41.1, 130 46.8 and 44.9; ten tokens, 150 44.0 by seven, 45.0 by two, 200
+    // 56.2 and 58.1, 260 65.7 and 61.4.  It looks at the sequences alone, and is late for short
+    // rows, of which more in vain would pay (8192 tokens: 180 of five drafts 21.4 by three,
+    // 22.8 by two; 350 of ten tokens 26.9 by seven, 30.8 by two).
     a.ahead = a.y ? (a.n <= 100 ? 3 : 2) : (a.n <= 200 ? 7 : 2);
     const int g = a.ahead < a.k ? a.ahead : a.k, rows = (a.y ? 2 * g : g) + 1;
     // Relative error of a row's sum.  Its terms: the unit's two ulp (2^-22), and three
