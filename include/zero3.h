@@ -789,8 +789,9 @@ zero3_status zero3_distill_backward(const void* logits, zero3_dtype dtype, int64
  * either way).
  *  - Tokens whose e is negative (-0 too), NaN or infinite, or whose probability is
  *    below 2^-126 of the row's largest, are not drawn, even where no other is left
- *    (they are accepted like any); e = 0 wins over every e > 0 where the residual is positive.  Where no token has a positive
- *    residual the draw is from p_A.  A NaN or negative u refuses.
+ *    (as drafted tokens they are accepted like any); e = 0 wins over every e > 0 where
+ *    the residual is positive.  Where no token has a positive residual the draw is
+ *    from p_A.  A NaN or negative u refuses.
  *  - Log probabilities are off by at most 2^-22 of themselves and the relative error of a
  *    row's binary32 sum, 2^-22 * (40 + vocab / 680) at most (2.7e-5 with 50257 tokens, where
  *    logits rise all along the row; 4e-8 is usual).  A nearly certain token's keeps
