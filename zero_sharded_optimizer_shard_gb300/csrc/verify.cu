@@ -11,12 +11,12 @@
 // there; in a round each warp has a share of one row.  The race reads the target's
 // row again, mostly from L2, and the noise; of the draft's row only what may win.
 //
-// What bounds it: one sequence, a chain of latencies (12.4 us: a round's loads and its
+// What bounds it: one sequence, a chain of latencies (12.3 us: a round's loads and its
 // exchange, the verdicts, the race and its exchange).  Many, the sequences that run
 // longest: 512 of five tokens (50257 bf16) move 550 MB in 126 us, 6.8 TB/s in
 // the first round and less as sequences end (floor: the rows up to the refusal and
 // the noise once, 443 MB, 65 us).  256 threads with 64 registers, four blocks per SM, at
-// which the instances with a draft spill 132 to 188 bytes and those without 8 to 12; five or
+// which the instances with a draft spill 148 to 188 bytes and those without 8 to 12; five or
 // six blocks, with more of them, 512 threads, rows or noise through shared memory, the
 // race in a launch of its own: equal or slower.  Without a draft (k = 0) a kernel of its
 // own takes statistics and race in one pass.
@@ -138,8 +138,8 @@ __device__ __forceinline__ void row_add(RowSum& q, const Chunk<T> (&c)[U], const
 #pragma unroll
     for (int i = 1; i < U; ++i) bm = fmaxf(bm, c[i].max());
     bm = in_unit(u, bm);
-    if (bm > q.m) {
-        if (q.s != 0.0f) q.s = __fmul_rn(q.s, exp2_approx(__fmul_rn(__fsub_rn(q.m, bm), u.c)));
+    if (bm > q.m) {  // (before any token: 0 times 0; another branch around it costs 2%)
+        q.s = __fmul_rn(q.s, exp2_approx(__fmul_rn(__fsub_rn(q.m, bm), u.c)));
         q.m = bm;
     }
     const uint64_t cc = pk2(u.c, u.c);
